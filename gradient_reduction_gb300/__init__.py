@@ -4,7 +4,10 @@ K data-parallel ranks are simulated as K buffers in one GPU's memory.  The
 library libdpr (C ABI in include/dpr.h, CUDA kernels in csrc/) provides the
 flat-bucket gather of fragmented gradients, the ring-order reduce-scatter
 with averaging and the fp32 partition cast, the all-gather and the fused
-all-reduce.  This package is the thin Python binding of those calls.
+all-reduce, and the operators of the backward pass that make those gradients
+(include/dpr_ops.h): layer norm, 8-bit activation checkpoints and the weight
+gradient read from them.  This package is the thin Python binding of those
+calls.
 """
 from ._binding import (  # noqa: F401
     WAIT_PER_BUFFER,
@@ -50,4 +53,14 @@ from ._binding import (  # noqa: F401
     dpr_strerror,
     dpr_version,
     lib,
+)
+from ._operators import (  # noqa: F401
+    CHECKPOINT_BLOCK,
+    Checkpoint,
+    dpr_checkpoint_empty,
+    dpr_checkpoint_load,
+    dpr_checkpoint_save,
+    dpr_layernorm_backward,
+    dpr_layernorm_forward,
+    dpr_linear_weight_grad,
 )

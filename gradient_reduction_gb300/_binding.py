@@ -1,4 +1,4 @@
-"""ctypes binding of libdpr (include/dpr.h), with the same entry-point names.
+"""ctypes binding of libdpr (include/dpr.h, include/dpr_ops.h), with the same entry-point names.
 
 Argument marshalling only: tensors are turned into device pointers and sizes,
 the current CUDA stream is passed along, and a non-zero status becomes a
@@ -24,6 +24,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "lib
 _c_p = ctypes.c_void_p
 _pp = ctypes.POINTER(ctypes.c_void_p)
 _i64p = ctypes.POINTER(ctypes.c_int64)
+_i64, _int = ctypes.c_int64, ctypes.c_int
 _SIGS = {
     "dpr_reduce_scatter": [_pp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, _pp, ctypes.c_int,
                            ctypes.c_float, ctypes.c_int, _c_p],
@@ -82,6 +83,16 @@ _SIGS = {
                            ctypes.c_int, ctypes.c_float],
     "dpr_start": [_c_p, _c_p],
     "dpr_request_free": [_c_p],
+    "dpr_layernorm_forward": [_c_p, _i64, _i64, _i64, _int, _c_p, _c_p, _int, ctypes.c_float,
+                              _c_p, _i64, _c_p, _c_p, _c_p, _c_p, _c_p],
+    "dpr_layernorm_backward_workspace": [_i64, _i64, _i64p],
+    "dpr_layernorm_backward": [_c_p, _i64, _c_p, _i64, _c_p, _i64, _i64, _int, _c_p, _int, _c_p,
+                               _c_p, _c_p, _i64, _c_p, _c_p, _int, _int, _c_p, _i64, _c_p],
+    "dpr_checkpoint_save": [_c_p, _i64, _i64, _i64, _int, _c_p, _c_p],
+    "dpr_checkpoint_load": [_c_p, _i64, _i64, _c_p, _i64, _int, _c_p],
+    "dpr_linear_weight_grad_workspace": [_i64, _i64, _i64, _i64p],
+    "dpr_linear_weight_grad": [_c_p, _i64, _c_p, _i64, _i64, _i64, _c_p, _i64, _int, _int, _c_p,
+                               _i64, _c_p],
     "dpr_strerror": [ctypes.c_int],
     "dpr_last_cuda_error": [],
     "dpr_version": [],

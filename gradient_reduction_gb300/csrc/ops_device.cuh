@@ -1,0 +1,255 @@
+// Device-side helpers of the backward-pass operators: V-element accesses of
+// bf16 and fp32 rows, sums over the threads that share a row, and the 8-bit
+// checkpoint format (see dpr_checkpoint in dpr_ops.h).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "dpr_device.cuh"
+
+namespace dpr {
+
+constexpr int kBlockChannels = 32;   // channels that share a step
+
+// --- V consecutive elements of a row ----------------------------------------
+// T is uint16_t (bf16 bits) or float.  V = 16 (bf16) and V = 8 (fp32) are
+// 32-byte accesses, V = 8 (bf16) 16-byte ones, V = 1 single elements.
+
+template <typename T, int V>
+struct Raw {
+    static constexpr int kWords = V * int(sizeof(T)) < 4 ? 1 : V * int(sizeof(T)) / 4;
+    uint32_t w[kWords];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void load_raw(const T* p, Raw<T, V>& r) {
+    static_assert(V == 1 || r.kWords == 4 || r.kWords == 8, "16- or 32-byte accesses");
+    if constexpr (V == 1) {
+        if constexpr (sizeof(T) == 2) {
+            uint16_t h;
+            asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(p));
+            r.w[0] = h;
+        } else {
+            asm volatile("ld.global.u32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
+        }
+    } else if constexpr (Raw<T, V>::kWords == 8) {
+        ld_v8(p, r.w);
+    } else {
+        const uint4 v = ld_v4(p);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void zero_raw(Raw<T, V>& r) {
+#pragma unroll
+    for (int i = 0; i < Raw<T, V>::kWords; ++i) r.w[i] = 0;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V>& r, float (&f)[V]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = __uint_as_float(r.w[i]);
+    } else if constexpr (V == 1) {
+        f[0] = bf_lo(r.w[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            f[2 * i] = bf_lo(r.w[i]);
+            f[2 * i + 1] = bf_hi(r.w[i]);
+        }
+    }
+}
+
+// fp32 -> T, rounded to nearest even (identity for fp32).
+template <typename T, int V>
+__device__ __forceinline__ void pack(const float (&f)[V], Raw<T, V>& r) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(f[i]);
+    } else if constexpr (V == 1) {
+        r.w[0] = to_bf16(f[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T, V>& r) {
+    if constexpr (V == 1) {
+        if constexpr (sizeof(T) == 2) *p = T(r.w[0]);
+        else *reinterpret_cast<uint32_t*>(p) = r.w[0];
+    } else if constexpr (Raw<T, V>::kWords == 8) {
+        st_v8(p, r.w);
+    } else {
+        st_v4(p, make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]));
+    }
+}
+
+// V parameter values (weight, bias), bf16 or fp32 by `is_bf16`; `vec`:
+// 16-byte accesses are allowed.
+template <int V>
+__device__ __forceinline__ void load_params(const void* p, bool is_bf16, bool vec, int64_t at,
+                                            float (&f)[V]) {
+    if (is_bf16) {
+        const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+        if (V >= 8 && vec) {
+#pragma unroll
+            for (int i = 0; i < V / 8; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(q + 8 * i);
+                f[8 * i + 0] = bf_lo(v.x); f[8 * i + 1] = bf_hi(v.x);
+                f[8 * i + 2] = bf_lo(v.y); f[8 * i + 3] = bf_hi(v.y);
+                f[8 * i + 4] = bf_lo(v.z); f[8 * i + 5] = bf_hi(v.z);
+                f[8 * i + 6] = bf_lo(v.w); f[8 * i + 7] = bf_hi(v.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = bf_1(q[i]);
+        }
+    } else {
+        const float* q = static_cast<const float*>(p) + at;
+        if (V >= 8 && vec) {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(q + 4 * i);
+                f[4 * i + 0] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = q[i];
+        }
+    }
+}
+
+// --- sums over the threads of a row -------------------------------------------
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
+// Sum of `v` over the blockDim.x (a multiple of 32, at most 1024) threads
+// that share threadIdx.y; every one of them gets it.  `s` has one row of 32
+// floats per threadIdx.y.  Every thread of the block calls it.  Two calls in
+// a row need different `s` (one barrier, none behind the reads).
+__device__ __forceinline__ float row_sum(float v, float (*s)[32]) {
+    v = warp_sum(v);
+    if (blockDim.x == 32) return v;
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) s[threadIdx.y][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < nw ? s[threadIdx.y][lane] : 0.0f;
+    return warp_sum(v);
+}
+
+// --- the 8-bit format -----------------------------------------------------------
+
+// |x| as bits: integer order is magnitude order, with infinities and NaN
+// above every finite value.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// The step byte of a block whose largest |x| has these bits.  For a peak in
+// [2^k, 2^(k+1)) the smallest step keeping peak / step below 127.5 is
+// 2^(k-6), or 2^(k-5) when the mantissa puts the peak at 127.5 * 2^(k-6) or
+// above; steps are kept in [2^-126, 2^121] (the byte in [1, 248]).
+__device__ __forceinline__ uint32_t step_byte(uint32_t peak) {
+    if (peak >= 0x7F800000u) return 255u;
+    if (peak == 0) return 0u;
+    int b = int((peak + 0x00010000u) >> 23) - 6;   // carries into the exponent from 127.5/128 up
+    return uint32_t(min(max(b, 1), 248));
+}
+
+__device__ __forceinline__ float step_value(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// 1 / step for bytes 1 .. 248; of no use (finite) for 0 and 255.
+__device__ __forceinline__ float step_inverse(uint32_t byte) {
+    return __uint_as_float((254u - min(byte, 248u)) << 23);
+}
+
+// x / step rounded to the nearest integer (ties to even), as the low byte of
+// the result.  x * inverse is exact or far below 1/2, and adding 1.5 * 2^23
+// rounds it to an integer whose two's complement is the sum's low bits.  The
+// limits bind only where the step is at its largest.
+__device__ __forceinline__ uint32_t encode(float x, float inverse) {
+    const float v = fminf(fmaxf(__fmul_rn(x, inverse), -127.0f), 127.0f);
+    return __float_as_uint(__fadd_rn(v, 12582912.0f));
+}
+
+// The low bytes of four encode() results.
+__device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Saves V channels starting at channel c (a multiple of V) of one row.  The
+// 32 / V threads of a block of channels are neighbouring lanes and all call
+// it; channels at or past `width` are zeros (`on` false: nothing stored).
+// `codes` and `steps` point at the row's start.
+template <int V>
+__device__ __forceinline__ void save_vector(const float (&x)[V], int64_t c, bool on, int8_t* codes,
+                                            uint8_t* steps) {
+    uint32_t peak = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) peak = max(peak, abs_bits(x[i]));
+#pragma unroll
+    for (int d = 1; d < kBlockChannels / V; d <<= 1)
+        peak = max(peak, __shfl_xor_sync(0xFFFFFFFFu, peak, d));
+    const uint32_t byte = step_byte(peak);
+    if (!on) return;
+    const float inv = step_inverse(byte);
+    if constexpr (V == 1) {
+        codes[c] = byte == 255u ? int8_t(0) : int8_t(encode(x[0], inv) & 0xFFu);
+    } else {
+        uint32_t w[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            w[i] = pack_codes(encode(x[4 * i], inv), encode(x[4 * i + 1], inv),
+                              encode(x[4 * i + 2], inv), encode(x[4 * i + 3], inv));
+            if (byte == 255u) w[i] = 0;
+        }
+        if constexpr (V == 16)
+            st_v4(codes + c, make_uint4(w[0], w[1], w[2], w[3]));
+        else
+            *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+    }
+    if ((c & (kBlockChannels - 1)) == 0) steps[c / kBlockChannels] = uint8_t(byte);
+}
+
+// V codes of a row.
+template <int V>
+struct CodeRaw {
+    uint32_t w[V < 4 ? 1 : V / 4];
+};
+
+template <int V>
+__device__ __forceinline__ void load_codes(const int8_t* p, CodeRaw<V>& r) {
+    if constexpr (V == 1) {
+        uint16_t h;
+        asm volatile("ld.global.u8 %0, [%1];" : "=h"(h) : "l"(p));
+        r.w[0] = h;
+    } else if constexpr (V == 8) {
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(r.w[0]), "=r"(r.w[1])
+                     : "l"(p));
+    } else {
+        const uint4 v = ld_v4(p);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    }
+}
+
+// code * step: flipping the code's sign bit gives code + 128, which as the
+// low byte of 2^23's bits is the float 2^23 + 128 + code.
+template <int V>
+__device__ __forceinline__ void decode(const CodeRaw<V>& r, float step, float (&f)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t u = r.w[i / 4] ^ 0x80808080u;
+        const uint32_t bits = __byte_perm(u, 0x4B000000u, 0x7650 + (i & 3));
+        f[i] = __fmul_rn(__fadd_rn(__uint_as_float(bits), -8388736.0f), step);
+    }
+}
+
+}  // namespace dpr

@@ -1,0 +1,60 @@
+// Host-side pieces shared by the backward-pass operators (internal): launch
+// with any block size, argument checks, and the selection of access widths.
+#pragma once
+
+#include <cstdint>
+#include <vector>
+
+#include <cuda_runtime.h>
+
+#include "../../include/dpr_ops.h"
+#include "dpr_kernels.h"
+#include "host_checks.h"
+
+namespace dpr {
+
+// As launch_kernel, with a block shape and dynamic shared memory.
+cudaError_t launch_grid(const void* kernel, dim3 grid, dim3 block, size_t smem, void** args,
+                        cudaStream_t s);
+
+bool programmatic_launch_enabled();   // defined beside launch_kernel
+
+// SMs of the current device (0 and an error on failure).
+cudaError_t current_sm_count(int* sms);
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+inline bool dtype_ok(int d) { return d == DPR_BF16 || d == DPR_FP32; }
+inline int64_t dtype_size(int d) { return d == DPR_BF16 ? 2 : 4; }
+
+// Bytes from the first to one past the last element of a strided matrix.
+inline uint64_t matrix_bytes(int64_t rows, int64_t width, int64_t stride, int64_t size) {
+    return rows > 0 ? uint64_t((rows - 1) * stride + width) * uint64_t(size) : 0;
+}
+
+// Is every row start of the matrix a multiple of `a` bytes?
+inline bool rows_aligned(const void* p, int64_t stride, int64_t size, int64_t a) {
+    return aligned(p, uintptr_t(a)) && (stride * size) % a == 0;
+}
+
+dpr_status check_matrix_size(int64_t rows, int64_t width);
+// `written`: the rows must not overlap (an input's may, down to stride 0 for
+// a broadcast row).
+dpr_status check_matrix(const void* p, int64_t stride, int64_t width, int dtype, bool written);
+dpr_status check_checkpoint(const dpr_checkpoint* c, int64_t width);
+// Appends the spans of a checkpoint's codes and steps.
+void add_spans(const dpr_checkpoint& c, int64_t rows, int64_t width, std::vector<Span>* v);
+
+// Elements per access for an activation of `dtype` whose rows are `width`
+// long: 32-byte accesses (16 bf16 or 8 fp32 elements) or 16-byte ones (8
+// bf16) where every row start allows it, else single elements.
+// `aligned32`, `aligned16`: whether every matrix of the call has such rows.
+inline int vector_elems(int dtype, int64_t width, bool aligned32, bool aligned16) {
+    if (dtype == DPR_FP32) return aligned32 && width % 8 == 0 ? 8 : 1;
+    if (aligned32 && width % 16 == 0) return 16;
+    if (aligned16 && width % 8 == 0) return 8;
+    return 1;
+}
+
+}  // namespace dpr
