@@ -60,6 +60,7 @@ from ._operators import (  # noqa: F401
     dpr_checkpoint_empty,
     dpr_checkpoint_load,
     dpr_checkpoint_save,
+    dpr_device_wait_failures,
     dpr_layernorm_backward,
     dpr_layernorm_forward,
     dpr_linear_weight_grad,

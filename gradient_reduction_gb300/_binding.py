@@ -90,7 +90,8 @@ _SIGS = {
                                _c_p, _c_p, _i64, _c_p, _c_p, _int, _int, _c_p, _i64, _c_p],
     "dpr_checkpoint_save": [_c_p, _i64, _i64, _i64, _int, _c_p, _c_p],
     "dpr_checkpoint_load": [_c_p, _i64, _i64, _c_p, _i64, _int, _c_p],
-    "dpr_linear_weight_grad_workspace": [_i64, _i64, _i64, _i64p],
+    "dpr_linear_weight_grad_workspace": [_c_p, _i64, _c_p, _i64, _i64, _i64, _i64p],
+    "dpr_device_wait_failures": [ctypes.POINTER(ctypes.c_uint32)],
     "dpr_linear_weight_grad": [_c_p, _i64, _c_p, _i64, _i64, _i64, _c_p, _i64, _int, _int, _c_p,
                                _i64, _c_p],
     "dpr_strerror": [ctypes.c_int],

@@ -237,8 +237,20 @@ def dpr_linear_weight_grad(dy: torch.Tensor, x_checkpoint: Checkpoint, dweight: 
         raise ValueError("dweight: need a matrix")
     pw, *shape, sw = _matrix(dweight, "dweight")
     _same("dweight", shape, (out_features, in_features))
-    nbytes = _workspace_bytes("dpr_linear_weight_grad_workspace", rows, out_features, in_features)
+    ref = ctypes.byref(arg)
+    need = ctypes.c_int64()
+    _check("dpr_linear_weight_grad", lib().dpr_linear_weight_grad_workspace(
+        pd, sd, ref, rows, out_features, in_features, ctypes.byref(need)))
+    nbytes = need.value
     ws = _workspace(workspace, nbytes, stream)
     _check("dpr_linear_weight_grad", lib().dpr_linear_weight_grad(
-        pd, sd, ctypes.byref(arg), rows, out_features, in_features, pw, sw, _DTYPES[dweight.dtype],
+        pd, sd, ref, rows, out_features, in_features, pw, sw, _DTYPES[dweight.dtype],
         int(bool(accumulate)), 0 if ws is None else ws.data_ptr(), nbytes, _stream(stream)))
+
+
+def dpr_device_wait_failures() -> int:
+    """Waits inside the weight gradient's kernel that have run out (0 in
+    working order); waits for the device."""
+    n = ctypes.c_uint32()
+    _check("dpr_device_wait_failures", lib().dpr_device_wait_failures(ctypes.byref(n)))
+    return n.value

@@ -1,29 +1,127 @@
 // A linear layer's weight gradient dW = dY^T X~ from the 8-bit checkpoint of
-// X: a product of a [rows, out] and a [rows, in] matrix along their rows.
+// X, on the tensor cores.  The sum runs along the tokens, the slow dimension
+// of both inputs, so both operands are "M/N-major": dY goes from memory to
+// shared memory by TMA as it is, X~ is restored there from its codes on the
+// way (exactly: a code times a power of two is a bf16 number).
+//
+// A pair of CTAs computes a tile of 256 in-features (the M of the
+// instruction, 128 in each CTA) by 256 out-features (N) with cta_group::2
+// instructions, so each CTA loads only half of the dY tile.  Restoring
+// happens on the M side: 128 channels per CTA are restored once for 256
+// out-features, 8192 codes per 64 tokens, against 256 cycles of matrix
+// instructions.  With in-features on the lanes of the accumulator, a warp's
+// store writes 32 consecutive elements of a row of dW straight from
+// registers.
+//
+// Warps of a CTA: 0 issues the TMA loads, 1 the matrix instructions (first
+// CTA only), 4-7 store finished accumulators while the next tile is summed
+// (two accumulators of 256 columns fill the tensor memory), 8-15 restore.
+//
+// Work: whole waves of tiles first, then the tokens of the tiles left over are
+// dealt out evenly to all pairs; parts of a tile are summed in fp32 in the
+// workspace and joined in token order by a second kernel.
 #include <algorithm>
+#include <atomic>
 
 #include "ops_device.cuh"
 #include "ops_kernels.h"
+#include "tensor_core.cuh"
 
 namespace dpr {
 
+namespace {
+
+constexpr int kTile = 256;               // in-features and out-features of a tile
+constexpr int kHalf = 128;               // of each CTA
+constexpr int kTokens = 64;              // per step of the main loop
+constexpr int kStages = 7;               // TMA ring
+constexpr int kBuffers = 3;              // ring of restored operands
+constexpr int kDyBytes = kHalf * kTokens * 2;
+constexpr int kCodeBytes = kHalf * kTokens;
+constexpr int kStepBytes = 16 * kTokens; // 16 step bytes a token, 4 of them used
+constexpr int kStageBytes = kDyBytes + kCodeBytes + kStepBytes;
+constexpr int kOperandBytes = kHalf * kTokens * 2;
+constexpr int kGroupBytes = 64 * kTokens * 2;   // 64 channels of an operand
+constexpr int kSmemBytes = 1024 + kBuffers * kOperandBytes + kStages * kStageBytes;
+constexpr int kGradThreads = 512;
+constexpr int kRestoreWarps = 8;
+
+}  // namespace
+
 struct WeightGradParams {
-    const uint16_t* dy;
-    int64_t dy_stride;
-    dpr_checkpoint x;
-    int64_t rows;
-    int out_features;
-    int in_features;
+    CUtensorMap dy, codes, steps;
     void* dw;
     int64_t dw_stride;
+    float* partial;          // [2 * pairs][256 out][256 in]
+    int out_features;
+    int in_features;
+    int out_tiles;
+    int in_tiles;
+    int blocks;              // steps of the main loop per tile
+    int waves;               // whole tiles per pair, before the dealt-out rest
+    int rest_tiles;          // tiles dealt out: the last ones
+    int64_t rest_chunk;      // steps per pair of those
     int dw_bf16;
     int accumulate;
 };
 
 namespace {
 
-__device__ __forceinline__ void store_grad(const WeightGradParams& p, int o, int i, float v) {
-    const int64_t at = int64_t(o) * p.dw_stride + i;
+__device__ unsigned int g_wait_failures;
+
+// A pair's piece of work: steps [first, last) of a tile.
+struct Segment {
+    int tile;
+    int first, last;
+    bool whole;
+    int slot;                // of the partial sums, when not whole
+};
+
+// The n-th piece of pair `pair`; false when there is none.
+__device__ __forceinline__ bool segment(const WeightGradParams& p, int pairs, int pair, int n,
+                                        Segment& s) {
+    if (n < p.waves) {
+        s.tile = n * pairs + pair;
+        s.first = 0; s.last = p.blocks; s.whole = true; s.slot = 0;
+        return true;
+    }
+    if (p.rest_tiles == 0) return false;
+    const int64_t total = int64_t(p.rest_tiles) * p.blocks;
+    const int64_t begin = min(int64_t(pair) * p.rest_chunk, total);
+    const int64_t end = min(begin + p.rest_chunk, total);
+    if (begin >= end) return false;
+    const int t = int(begin / p.blocks) + (n - p.waves);
+    const int64_t t0 = int64_t(t) * p.blocks;
+    if (t0 >= end) return false;
+    s.tile = p.waves * pairs + t;
+    s.first = int(max(begin - t0, int64_t(0)));
+    s.last = int(min(end - t0, int64_t(p.blocks)));
+    s.whole = s.first == 0 && s.last == p.blocks;
+    s.slot = 2 * pair + (n - p.waves);
+    return true;
+}
+
+// Tiles in columns of 8 out-tiles, so that the tiles of a wave share inputs.
+__device__ __forceinline__ void tile_origin(const WeightGradParams& p, int tile, int& o, int& i) {
+    const int group = tile / (8 * p.in_tiles);
+    const int rest = tile - group * 8 * p.in_tiles;
+    const int height = min(8, p.out_tiles - group * 8);
+    i = rest / height * kTile;
+    o = (group * 8 + rest % height) * kTile;
+}
+
+// Two codes, in the low bytes of the halves of `w`, as bf16: the seven low
+// bits on top of 128, less 128 or (sign bit) 256, times the step.
+__device__ __forceinline__ uint32_t restore_pair(uint32_t w, uint32_t step2) {
+    const uint32_t low = (w & 0x007F007Fu) | 0x43004300u;
+    const uint32_t base = (w & 0x00800080u) | 0x43004300u;
+    uint32_t v, r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(low), "r"(base));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(step2));
+    return r;
+}
+
+__device__ __forceinline__ void put_grad(const WeightGradParams& p, int64_t at, float v) {
     if (p.dw_bf16) {
         uint16_t* d = static_cast<uint16_t*>(p.dw) + at;
         *d = to_bf16(p.accumulate ? __fadd_rn(bf_1(*d), v) : v);
@@ -33,45 +131,360 @@ __device__ __forceinline__ void store_grad(const WeightGradParams& p, int o, int
     }
 }
 
-// 64 x 64 outputs per block, 4 x 4 per thread, 16 rows at a time.
-__global__ void __launch_bounds__(256) weight_grad_any(const __grid_constant__ WeightGradParams p) {
-    __shared__ float a[16][64], b[16][64];
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
+weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kBuffers + 4];
+    __shared__ uint32_t tmem_slot;
+
+    const uint32_t base = (tc::smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t operands = base;                          // [kBuffers], 1024-byte aligned
+    const uint32_t stages = base + kBuffers * kOperandBytes; // [kStages] dY
+    const uint32_t codes = stages + kStages * kDyBytes;      // [kStages] codes
+    const uint32_t steps = codes + kStages * kCodeBytes;     // [kStages] step bytes
+    const uint32_t bar0 = tc::smem_addr(bars);
+    const auto full = [&](int s) { return bar0 + 8u * s; };                         // loads landed
+    const auto free_ = [&](int s) { return bar0 + 8u * (kStages + s); };            // stage consumed
+    const auto ready = [&](int b) { return bar0 + 8u * (2 * kStages + b); };        // restored, both CTAs
+    const auto spent = [&](int b) { return bar0 + 8u * (2 * kStages + kBuffers + b); };
+    const auto summed = [&](int a) { return bar0 + 8u * (2 * kStages + 2 * kBuffers + a); };
+    const auto stored = [&](int a) { return bar0 + 8u * (2 * kStages + 2 * kBuffers + 2 + a); };
+
+    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int pairs = int(gridDim.x) >> 1, pair = int(blockIdx.x) >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tc::mbar_init(full(s), 1);
+            tc::mbar_init(free_(s), 1);
+        }
+        for (int b = 0; b < kBuffers; ++b) {
+            tc::mbar_init(ready(b), 2 * kRestoreWarps);
+            tc::mbar_init(spent(b), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(summed(a), 1);
+            tc::mbar_init(stored(a), 2 * 4);
+        }
+        tc::mbar_init_fence();
+        tc::tma_prefetch_map(&p.dy);
+        tc::tma_prefetch_map(&p.codes);
+        tc::tma_prefetch_map(&p.steps);
+    }
+    if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
     grid_wait();
     grid_release();
-    const int i0 = int(blockIdx.x) * 64, o0 = int(blockIdx.y) * 64;
-    const int tx = int(threadIdx.x) & 15, ty = int(threadIdx.x) >> 4;
-    float acc[4][4] = {};
-    for (int64_t t0 = 0; t0 < p.rows; t0 += 16) {
-        for (int q = int(threadIdx.x); q < 16 * 64; q += 256) {
-            const int64_t t = t0 + q / 64;
-            const int o = o0 + q % 64, i = i0 + q % 64;
-            const bool in = t < p.rows;
-            a[q / 64][q % 64] = in && o < p.out_features ? bf_1(p.dy[t * p.dy_stride + o]) : 0.0f;
-            float v[1] = {0.0f};
-            if (in && i < p.in_features) {
-                CodeRaw<1> code;
-                load_codes<1>(p.x.codes + t * p.x.code_stride + i, code);
-                decode<1>(code, step_value(p.x.steps[t * p.x.step_stride + i / kBlockChannels]), v);
+
+    bool ok = true;
+    Segment s;
+    if (warp == 0) {
+        if (lane == 0) {
+            int st = 0;
+            uint32_t round = 0;
+            for (int n = 0; ok && segment(p, pairs, pair, n, s); ++n) {
+                int o, i;
+                tile_origin(p, s.tile, o, i);
+                o += int(rank) * kHalf;
+                i += int(rank) * kHalf;
+                for (int k = s.first; k < s.last; ++k) {
+                    if (!(ok = tc::mbar_wait(free_(st), (round & 1) ^ 1))) break;
+                    tc::mbar_expect(full(st), kStageBytes);
+                    const int t = k * kTokens;
+                    tc::tma_load(codes + st * kCodeBytes, &p.codes, i, t, full(st));
+                    tc::tma_load(steps + st * kStepBytes, &p.steps, (i / kBlockChannels) & ~15, t,
+                                 full(st));
+                    tc::tma_load(stages + st * kDyBytes, &p.dy, o, t, full(st));
+                    tc::tma_load(stages + st * kDyBytes + kGroupBytes, &p.dy, o + 64, t, full(st));
+                    if (++st == kStages) { st = 0; ++round; }
+                }
             }
-            b[q / 64][q % 64] = v[0];
+            // every load has landed and every signal of the matrix instructions has arrived
+            // here before the CTA may leave: the last use of each stage and buffer
+            const uint32_t total = round * kStages + st;
+            for (int k = 0; k < kStages; ++k) {
+                const uint32_t uses = total / kStages + (uint32_t(k) < total % kStages);
+                if (uses == 0) continue;
+                ok &= tc::mbar_wait(full(k), (uses - 1) & 1);
+                if (ok) ok = tc::mbar_wait(free_(k), (uses - 1) & 1);
+            }
+            for (int b = 0; ok && b < kBuffers; ++b) {
+                const uint32_t uses = total / kBuffers + (uint32_t(b) < total % kBuffers);
+                if (uses > 0) ok = tc::mbar_wait(spent(b), (uses - 1) & 1);
+            }
         }
-        __syncthreads();
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t instruction = tc::bf16_instruction(kTile, kTile);
+            int st = 0, b = 0, acc = 0;
+            uint32_t b_round = 0, acc_round = 0;
+            for (int n = 0; ok && segment(p, pairs, pair, n, s); ++n) {
+                if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
+                tc::fence_after_sync();
+                for (int k = s.first; k < s.last; ++k) {
+                    if (!(ok = tc::mbar_wait(ready(b), b_round & 1))) break;
+                    tc::fence_after_sync();
+                    const uint64_t x =
+                        tc::operand(operands + b * kOperandBytes, kGroupBytes, 1024);
+                    const uint64_t y = tc::operand(stages + st * kDyBytes, kGroupBytes, 1024);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+                    for (int j = 0; j < kTokens / 16; ++j)   // 16 tokens are 2048 bytes of a group
+                        tc::mma(tmem + acc * kTile, x + uint64_t(j * (2048 >> 4)),
+                                y + uint64_t(j * (2048 >> 4)), instruction, k > s.first || j > 0);
+                    tc::commit_both(free_(st));
+                    tc::commit_both(spent(b));
+                    if (++st == kStages) st = 0;
+                    if (++b == kBuffers) { b = 0; ++b_round; }
+                }
+                if (!ok) break;
+                tc::commit_both(summed(acc));
+                if (++acc == 2) { acc = 0; ++acc_round; }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 8) {
+        const int row = (warp - 4) * 32 + lane;     // lane of the accumulator
+        int acc = 0;
+        uint32_t acc_round = 0;
+        for (int n = 0; segment(p, pairs, pair, n, s); ++n) {
+            if (!(ok = tc::mbar_wait_warp(summed(acc), acc_round & 1))) break;
+            tc::fence_after_sync();
+            int o, i;
+            tile_origin(p, s.tile, o, i);
+            const int ci = int(rank) * kHalf + row;
+            i += ci;
+            const uint32_t from = tmem + acc * kTile + (uint32_t(warp - 4) << 21);
+            for (int c = 0; c < kTile; c += 32) {
+                uint32_t v[32];
+                tc::tmem_load32(from + c, v);
+                if (s.whole) {
+                    if (i < p.in_features) {
+                        int64_t at = int64_t(o + c) * p.dw_stride + i;
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+                        for (int j = 0; j < 32; ++j, at += p.dw_stride)
+                            if (o + c + j < p.out_features) put_grad(p, at, __uint_as_float(v[j]));
+                    }
+                } else {
+                    float* d = p.partial + (int64_t(s.slot) * kTile + c) * kTile + ci;
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    acc[m][n] = __fmaf_rn(a[k][ty + 16 * m], b[k][tx + 16 * n], acc[m][n]);
-        __syncthreads();
+                    for (int j = 0; j < 32; ++j) d[j * kTile] = __uint_as_float(v[j]);
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(stored(acc), 0));
+            if (++acc == 2) { acc = 0; ++acc_round; }
+        }
+    } else if (warp >= 8) {
+        const int t = int(threadIdx.x) - 256;
+        const int chunk = t & 7;                    // 16 channels
+        const int group = chunk >> 2;               // of 64
+        int st = 0, b = 0;
+        uint32_t round = 0, b_round = 0;
+        for (int n = 0; ok && segment(p, pairs, pair, n, s); ++n) {
+            int o, i;
+            tile_origin(p, s.tile, o, i);
+            const int block = ((i + int(rank) * kHalf) / kBlockChannels & 15) + (chunk >> 1);
+            for (int k = s.first; k < s.last; ++k) {
+                if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
+                if (!(ok = tc::mbar_wait_warp(spent(b), (b_round & 1) ^ 1))) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = (t >> 3) + 32 * h;   // token
+                    uint32_t w[4], step;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(codes + st * kCodeBytes + row * kHalf + chunk * 16));
+                    asm volatile("ld.shared.u8 %0, [%1];"
+                                 : "=r"(step)
+                                 : "r"(steps + st * kStepBytes + row * 16 + block));
+                    step = (step << 7) * 0x00010001u;
+                    uint32_t v[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[2 * j] = restore_pair(__byte_perm(w[j], 0, 0x4140), step);
+                        v[2 * j + 1] = restore_pair(__byte_perm(w[j], 0, 0x4342), step);
+                    }
+                    // 16-byte pieces of a 128-byte row are permuted by the row's number; the
+                    // second group writes its odd piece first, so that 8 lanes fill 32 banks
+                    const uint32_t at = operands + b * kOperandBytes + group * kGroupBytes + row * 128;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int odd = j ^ group;
+                        const uint32_t piece = uint32_t(((chunk & 3) * 2 + odd) ^ (row & 7));
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + piece * 16),
+                                     "r"(odd ? v[4] : v[0]), "r"(odd ? v[5] : v[1]),
+                                     "r"(odd ? v[6] : v[2]), "r"(odd ? v[7] : v[3])
+                                     : "memory");
+                    }
+                }
+                tc::fence_to_async();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(b), 0));
+                if (++st == kStages) { st = 0; ++round; }
+                if (++b == kBuffers) { b = 0; ++b_round; }
+            }
+        }
     }
+    if (!ok) atomicAdd(&g_wait_failures, 1u);
+    // nobody leaves while the other CTA may still signal or read this one
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_free(tmem, 512);
+}
+
+// Tiles summed in parts: the parts in token order, then as put_grad.  One
+// block of 256 threads per 8 out-features of a dealt-out tile.
+__global__ void __launch_bounds__(256) weight_grad_join(const __grid_constant__ WeightGradParams p,
+                                                        int pairs) {
+    grid_wait();
+    grid_release();
+    const int t = int(blockIdx.x);
+    const int64_t t0 = int64_t(t) * p.blocks;
+    const int first = int(t0 / p.rest_chunk), last = int((t0 + p.blocks - 1) / p.rest_chunk);
+    if (first == last) return;               // one pair summed it all
+    int o, i;
+    tile_origin(p, p.waves * pairs + t, o, i);
+    i += int(threadIdx.x);
+    if (i >= p.in_features) return;
+    float v[8];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    for (int q = first; q <= last; ++q) {
+        const int slot = 2 * q + t - int(int64_t(q) * p.rest_chunk / p.blocks);
+        const float* d = p.partial + (int64_t(slot) * kTile + blockIdx.y * 8) * kTile + threadIdx.x;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int o = o0 + ty + 16 * m, i = i0 + tx + 16 * n;
-            if (o < p.out_features && i < p.in_features) store_grad(p, o, i, acc[m][n]);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], d[j * kTile]);
+    }
+    o += int(blockIdx.y) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (o + j < p.out_features) put_grad(p, int64_t(o + j) * p.dw_stride + i, v[j]);
+}
+
+// Rows copied to 16-byte-aligned ones, for inputs that TMA cannot read.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) repack_rows(const T* from, int64_t from_stride, T* to,
+                                                        int64_t to_stride, int64_t rows, int width) {
+    grid_wait();
+    grid_release();
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int c = int(threadIdx.x); c < width; c += kThreads)
+            to[r * to_stride + c] = from[r * from_stride + c];
+}
+
+// dW = 0, for a call without tokens.
+__global__ void __launch_bounds__(kThreads) zero_rows(const __grid_constant__ WeightGradParams p) {
+    grid_wait();
+    grid_release();
+    for (int o = int(blockIdx.x); o < p.out_features; o += int(gridDim.x))
+        for (int i = int(threadIdx.x); i < p.in_features; i += kThreads)
+            put_grad(p, int64_t(o) * p.dw_stride + i, 0.0f);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encoder(EncodeTiled* fn) {
+    static std::atomic<void*> cached{nullptr};
+    void* f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                               cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+        cached.store(f, std::memory_order_release);
+    }
+    *fn = reinterpret_cast<EncodeTiled>(f);
+    return cudaSuccess;
+}
+
+// A [rows, width] tensor read in boxes of `box` elements by kTokens rows.
+cudaError_t encode(EncodeTiled fn, CUtensorMap* map, CUtensorMapDataType type, int64_t size,
+                   const void* p, int64_t stride, int64_t rows, int64_t width, int box,
+                   CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(stride * size)};
+    const cuuint32_t boxes[2] = {cuuint32_t(box), cuuint32_t(kTokens)};
+    const cuuint32_t ones[2] = {1, 1};
+    const CUresult r = fn(map, type, 2, const_cast<void*>(p), dims, strides, boxes, ones,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+struct Plan {
+    int out_tiles, in_tiles, blocks;
+    int waves, rest_tiles;
+    int64_t rest_chunk;
+    bool join;
+    bool copy_dy, copy_x;            // repacked for TMA
+    int64_t partial_bytes, dy_bytes, code_bytes, step_bytes;
+};
+
+constexpr int kPairs = 76;           // of a GB300's 152 SMs
+
+// Can TMA read these rows where they are?
+bool tma_rows(const void* p, int64_t stride, int64_t size, int64_t rows, int64_t width) {
+    return aligned(p, 16) && (rows <= 1 || (stride >= width && stride * size % 16 == 0));
+}
+
+Plan make_plan(const void* dy, int64_t dy_stride, const dpr_checkpoint* x, int64_t rows,
+               int64_t out_features, int64_t in_features) {
+    Plan q = {};
+    q.out_tiles = int(ceil_div(out_features, kTile));
+    q.in_tiles = int(ceil_div(in_features, kTile));
+    q.blocks = int(ceil_div(rows, kTokens));
+    const int64_t tiles = int64_t(q.out_tiles) * q.in_tiles;
+    q.waves = int(tiles / kPairs);
+    q.rest_tiles = int(tiles % kPairs);
+    // steps of the tiles left over, dealt out evenly; a part is at least 4 steps long
+    const int64_t steps = int64_t(q.rest_tiles) * q.blocks;
+    q.rest_chunk = std::min<int64_t>(q.blocks, std::max<int64_t>(ceil_div(steps, kPairs), 4));
+    q.join = q.rest_tiles > 0 && q.rest_chunk < q.blocks;
+    q.partial_bytes = q.join ? int64_t(2 * kPairs) * kTile * kTile * 4 : 0;
+    q.copy_dy = !tma_rows(dy, dy_stride, 2, rows, out_features);
+    q.dy_bytes = q.copy_dy ? rows * round_up(out_features, 8) * 2 : 0;
+    q.copy_x = !tma_rows(x->codes, x->code_stride, 1, rows, in_features) ||
+               !tma_rows(x->steps, x->step_stride, 1, rows,
+                         ceil_div(in_features, kBlockChannels));
+    if (q.copy_x) {
+        q.code_bytes = rows * round_up(in_features, 16);
+        q.step_bytes = rows * round_up(ceil_div(in_features, kBlockChannels), 16);
+    }
+    return q;
+}
+
+dpr_status check_sizes(int64_t rows, int64_t out_features, int64_t in_features) {
+    dpr_status st = check_matrix_size(rows, out_features);
+    if (st == DPR_OK) st = check_matrix_size(rows, in_features);
+    if (st != DPR_OK) return st;
+    if (rows > DPR_MAX_GRAD_ROWS) return DPR_ERR_UNSUPPORTED;
+    // tiles are counted in 31 bits
+    if (ceil_div(out_features, kTile) * ceil_div(in_features, kTile) > (int64_t(1) << 30))
+        return DPR_ERR_UNSUPPORTED;
+    return DPR_OK;
+}
+
+template <typename T>
+cudaError_t repack(const void* from, int64_t from_stride, void* to, int64_t to_stride, int64_t rows,
+                   int width, cudaStream_t s) {
+    const T* f = static_cast<const T*>(from);
+    T* t = static_cast<T*>(to);
+    void* args[] = {&f, &from_stride, &t, &to_stride, &rows, &width};
+    return launch_grid((const void*)repack_rows<T>, dim3(unsigned(std::min<int64_t>(rows, 152 * 8))),
+                       dim3(kThreads), 0, args, s);
 }
 
 }  // namespace
@@ -81,13 +494,17 @@ using namespace dpr;
 
 extern "C" {
 
-dpr_status dpr_linear_weight_grad_workspace(int64_t rows, int64_t out_features,
-                                            int64_t in_features, int64_t* bytes) {
+dpr_status dpr_linear_weight_grad_workspace(const void* dy, int64_t dy_stride,
+                                            const dpr_checkpoint* x_ckpt, int64_t rows,
+                                            int64_t out_features, int64_t in_features,
+                                            int64_t* bytes) {
     if (!bytes) return DPR_ERR_INVALID_ARG;
     *bytes = 0;
-    dpr_status st = check_matrix_size(rows, out_features);
-    if (st == DPR_OK) st = check_matrix_size(rows, in_features);
-    if (st != DPR_OK) return st;
+    const dpr_status st = check_sizes(rows, out_features, in_features);
+    if (st != DPR_OK || rows == 0) return st;
+    if (!x_ckpt) return DPR_ERR_INVALID_ARG;
+    const Plan q = make_plan(dy, dy_stride, x_ckpt, rows, out_features, in_features);
+    *bytes = q.partial_bytes + round_up(q.dy_bytes, 16) + round_up(q.code_bytes, 16) + q.step_bytes;
     return DPR_OK;
 }
 
@@ -96,7 +513,8 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
                                   void* dweight, int64_t dweight_stride, int dtype, int accumulate,
                                   void* workspace, int64_t workspace_bytes, void* stream) {
     int64_t need = 0;
-    dpr_status st = dpr_linear_weight_grad_workspace(rows, out_features, in_features, &need);
+    dpr_status st = dpr_linear_weight_grad_workspace(dy, dy_stride, x_ckpt, rows, out_features,
+                                                     in_features, &need);
     if (st != DPR_OK) return st;
     if (!dtype_ok(dtype)) return DPR_ERR_INVALID_ARG;
     if ((st = check_matrix(dweight, dweight_stride, in_features, dtype, true)) != DPR_OK) return st;
@@ -105,7 +523,6 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
                                                  dtype_size(dtype))));
     if (rows > 0) {
         if ((st = check_matrix(dy, dy_stride, out_features, DPR_BF16, false)) != DPR_OK) return st;
-        if (!x_ckpt) return DPR_ERR_INVALID_ARG;
         if ((st = check_checkpoint(x_ckpt, in_features)) != DPR_OK) return st;
         if (need > 0) {
             if (!workspace || workspace_bytes < need) return DPR_ERR_INVALID_ARG;
@@ -117,18 +534,85 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
     }
     if (!pairwise_disjoint(outs) || any_overlap(outs, ins)) return DPR_ERR_ALIAS;
 
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     WeightGradParams p = {};
-    p.dy = static_cast<const uint16_t*>(dy); p.dy_stride = dy_stride;
-    if (rows > 0) p.x = *x_ckpt;
-    p.rows = rows; p.out_features = int(out_features); p.in_features = int(in_features);
+    p.out_features = int(out_features); p.in_features = int(in_features);
     p.dw = dweight; p.dw_stride = dweight_stride;
     p.dw_bf16 = dtype == DPR_BF16; p.accumulate = accumulate != 0;
-    if (ceil_div(out_features, 64) > 65535) return DPR_ERR_UNSUPPORTED;
+    if (rows == 0) {
+        if (accumulate) return DPR_OK;
+        void* args[] = {&p};
+        return record_cuda_status(launch_grid((const void*)zero_rows,
+                                              dim3(unsigned(std::min<int64_t>(out_features, 1 << 16))),
+                                              dim3(kThreads), 0, args, s));
+    }
+
+    const Plan q = make_plan(dy, dy_stride, x_ckpt, rows, out_features, in_features);
+    p.out_tiles = q.out_tiles; p.in_tiles = q.in_tiles; p.blocks = q.blocks;
+    p.waves = q.waves; p.rest_tiles = q.rest_tiles; p.rest_chunk = q.rest_chunk;
+    char* ws = static_cast<char*>(workspace);
+    p.partial = reinterpret_cast<float*>(ws);
+    ws += q.partial_bytes;
+    dpr_checkpoint x = *x_ckpt;
+    cudaError_t e = cudaSuccess;
+    if (q.copy_dy) {
+        const int64_t stride = round_up(out_features, 8);
+        e = repack<uint16_t>(dy, dy_stride, ws, stride, rows, int(out_features), s);
+        dy = ws; dy_stride = stride;
+        ws += round_up(q.dy_bytes, 16);
+    }
+    if (q.copy_x && e == cudaSuccess) {
+        const int64_t blocks = ceil_div(in_features, kBlockChannels);
+        const int64_t cs = round_up(in_features, 16), ss = round_up(blocks, 16);
+        e = repack<uint8_t>(x.codes, x.code_stride, ws, cs, rows, int(in_features), s);
+        x.codes = reinterpret_cast<int8_t*>(ws); x.code_stride = cs;
+        ws += round_up(q.code_bytes, 16);
+        if (e == cudaSuccess)
+            e = repack<uint8_t>(x.steps, x.step_stride, ws, ss, rows, int(blocks), s);
+        x.steps = reinterpret_cast<uint8_t*>(ws); x.step_stride = ss;
+    }
+    EncodeTiled fn = nullptr;
+    if (e == cudaSuccess) e = encoder(&fn);
+    // one row's stride is never used, but has to be a multiple of 16 bytes all the same
+    if (rows == 1) {
+        dy_stride = round_up(out_features, 8);
+        x.code_stride = round_up(in_features, 16);
+        x.step_stride = round_up(ceil_div(in_features, kBlockChannels), 16);
+    }
+    if (e == cudaSuccess)
+        e = encode(fn, &p.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, dy_stride, rows,
+                   out_features, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess)
+        e = encode(fn, &p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.codes, x.code_stride, rows,
+                   in_features, kHalf, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess)
+        e = encode(fn, &p.steps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.steps, x.step_stride, rows,
+                   ceil_div(in_features, kBlockChannels), 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute((const void*)weight_grad_pairs,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return record_cuda_status(e);
     void* args[] = {&p};
-    return record_cuda_status(launch_grid(
-        (const void*)weight_grad_any,
-        dim3(unsigned(ceil_div(in_features, 64)), unsigned(ceil_div(out_features, 64))), dim3(256),
-        0, args, static_cast<cudaStream_t>(stream)));
+    // pairs without work are not launched, unless whole waves need all of them
+    const int64_t busy = q.waves > 0 ? kPairs
+                                     : ceil_div(int64_t(q.rest_tiles) * q.blocks, q.rest_chunk);
+    e = launch_grid((const void*)weight_grad_pairs, dim3(unsigned(2 * busy)), dim3(kGradThreads),
+                    kSmemBytes, args, s);
+    if (e == cudaSuccess && q.join) {
+        int pairs = int(busy);
+        void* jargs[] = {&p, &pairs};
+        e = launch_grid((const void*)weight_grad_join, dim3(unsigned(q.rest_tiles), kTile / 8),
+                        dim3(256), 0, jargs, s);
+    }
+    return record_cuda_status(e);
+}
+
+dpr_status dpr_device_wait_failures(uint32_t* count) {
+    if (!count) return DPR_ERR_INVALID_ARG;
+    unsigned int v = 0;
+    const cudaError_t e = cudaMemcpyFromSymbol(&v, g_wait_failures, sizeof(v));
+    *count = v;
+    return record_cuda_status(e);
 }
 
 }  // extern "C"

@@ -33,6 +33,7 @@ typedef enum dpr_dtype { DPR_BF16 = 0, DPR_FP32 = 1 } dpr_dtype;
 
 #define DPR_MAX_ROWS (((int64_t)1) << 30)  /* tokens per call */
 #define DPR_MAX_WIDTH (((int64_t)1) << 20) /* channels */
+#define DPR_MAX_GRAD_ROWS (((int64_t)1) << 22) /* tokens of one weight gradient */
 #define DPR_CHECKPOINT_BLOCK 32            /* channels that share one step */
 
 /*
@@ -114,14 +115,26 @@ dpr_status dpr_checkpoint_load(const dpr_checkpoint* ckpt, int64_t rows, int64_t
  * ([rows, out_features]).  Products are exact and summed in fp32; dweight
  * (bf16 or fp32, `dtype`) is rounded once, after adding the old value when
  * accumulate != 0.  rows == 0 gives zeros.  The workspace is 16-byte aligned
- * and may be reused by the next call on the same stream.
+ * and may be reused by the next call on the same stream; its size depends on
+ * the sizes and, because inputs whose rows are not 16-byte aligned are first
+ * copied into it, on the addresses and strides.
  */
-dpr_status dpr_linear_weight_grad_workspace(int64_t rows, int64_t out_features,
-                                            int64_t in_features, int64_t* bytes);
+dpr_status dpr_linear_weight_grad_workspace(const void* dy, int64_t dy_stride,
+                                            const dpr_checkpoint* x_ckpt, int64_t rows,
+                                            int64_t out_features, int64_t in_features,
+                                            int64_t* bytes);
 dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_checkpoint* x_ckpt,
                                   int64_t rows, int64_t out_features, int64_t in_features,
                                   void* dweight, int64_t dweight_stride, int dtype, int accumulate,
                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * How many waits inside the weight gradient's kernel have run out on the
+ * current device since the library was loaded (each is bounded; 0 unless the
+ * hardware or the library is broken: such a call's result is incomplete).
+ * Waits for the device's work.
+ */
+dpr_status dpr_device_wait_failures(uint32_t* count);
 
 #ifdef __cplusplus
 }

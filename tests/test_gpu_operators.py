@@ -669,3 +669,8 @@ def test_offsets_past_32_bits():
     lin = torch.empty(width, width, device="cuda")
     dpr.dpr_linear_weight_grad(fdy, saved, lin)
     R.check(lin, R.weight_grad(dy, xx), R.weight_grad_bounds(dy, xx, F32), "dweight")
+
+
+def test_no_wait_ran_out():
+    H.device()
+    assert dpr.dpr_device_wait_failures() == 0

@@ -37,7 +37,7 @@ def L():
 def test_exports_every_declared_function(L):
     src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(dpr_[a-z0-9_]+)\s*\(", src)))
-    assert len(names) == 7
+    assert len(names) == 8
     for n in names:
         assert hasattr(L, n), n
 
@@ -175,11 +175,11 @@ def test_weight_grad_refusals(L):
     n = ctypes.c_int64()
 
     def call(dy=X, ds=128, c=None, rows=64, o=128, i=64, dw=DW, dws=64, d=BF16, ws=WS, none=False):
-        st = L.dpr_linear_weight_grad_workspace(rows, o, i, ctypes.byref(n))
+        x = None if none else (c or _ckpt())
+        st = L.dpr_linear_weight_grad_workspace(dy, ds, x, rows, o, i, ctypes.byref(n))
         if st != OK:
             return st
-        return L.dpr_linear_weight_grad(dy, ds, None if none else (c or _ckpt()), rows, o, i, dw, dws,
-                                        d, 0, ws, n.value, None)
+        return L.dpr_linear_weight_grad(dy, ds, x, rows, o, i, dw, dws, d, 0, ws, n.value, None)
     assert call(rows=-1) == INVALID
     assert call(o=0) == INVALID and call(i=0) == INVALID
     assert call(o=1 << 21) == UNSUP and call(rows=1 << 31) == UNSUP
@@ -189,7 +189,15 @@ def test_weight_grad_refusals(L):
     assert call(c=_ckpt(code_stride=63)) == INVALID
     assert call(dy=X + 1) == ALIGN and call(d=FP32, dw=DW + 2) == ALIGN
     assert call(dw=X) == ALIAS and call(dw=CODES) == ALIAS and call(dw=STEPS) == ALIAS
-    assert L.dpr_linear_weight_grad_workspace(1, 1, 1, None) == INVALID
+    assert call(rows=(1 << 22) + 1) == UNSUP
+    assert L.dpr_linear_weight_grad_workspace(X, 64, _ckpt(), 1, 1, 1, None) == INVALID
+    # aligned inputs whose tiles are summed whole need none; odd rows are copied
+    assert L.dpr_linear_weight_grad_workspace(X, 64, _ckpt(), 64, 64, 64, ctypes.byref(n)) == OK
+    assert n.value == 0
+    assert L.dpr_linear_weight_grad_workspace(X, 65, _ckpt(), 64, 65, 64, ctypes.byref(n)) == OK
+    assert n.value == 64 * 72 * 2
+    assert call(dy=X, ds=129, ws=None) == INVALID and call(ds=129, ws=WS + 4) == ALIGN
+    assert call(ds=129, ws=X) == ALIAS
 
 
 def test_binding_refuses_what_is_not_on_the_gpu():
