@@ -13,9 +13,16 @@
 // store writes 32 consecutive elements of a row of dW straight from
 // registers.
 //
+// The tensor core's fp32 accumulation truncates, an error that grows with the
+// length of the sum (5.7e-6 relative after 8192 tokens, against 5.8e-7 for
+// rounded fp32 sums).  So an accumulator runs over 1024 tokens only; then the
+// other one goes on (two of 256 columns fill the tensor memory) while the
+// first is added, rounded to nearest, to the tile's sums in the registers of
+// eight warps.
+//
 // Warps of a CTA: 0 issues the TMA loads, 1 the matrix instructions (first
-// CTA only), 4-7 store finished accumulators while the next tile is summed
-// (two accumulators of 256 columns fill the tensor memory), 8-15 restore.
+// CTA only), 4-11 keep the sums and store them, 12-19 restore: two groups of
+// four warps take turns, so that one group's latencies hide behind the other.
 //
 // Work: whole waves of tiles first, then the tokens of the tiles left over are
 // dealt out evenly to all pairs; parts of a tile are summed in fp32 in the
@@ -34,8 +41,9 @@ namespace {
 constexpr int kTile = 256;               // in-features and out-features of a tile
 constexpr int kHalf = 128;               // of each CTA
 constexpr int kTokens = 64;              // per step of the main loop
-constexpr int kStages = 7;               // TMA ring
-constexpr int kBuffers = 3;              // ring of restored operands
+constexpr int kStages = 6;               // TMA ring
+constexpr int kBuffers = 4;              // ring of restored operands
+constexpr int kChunk = 16;               // main-loop steps per accumulator
 constexpr int kDyBytes = kHalf * kTokens * 2;
 constexpr int kCodeBytes = kHalf * kTokens;
 constexpr int kStepBytes = 16 * kTokens; // 16 step bytes a token, 4 of them used
@@ -43,8 +51,14 @@ constexpr int kStageBytes = kDyBytes + kCodeBytes + kStepBytes;
 constexpr int kOperandBytes = kHalf * kTokens * 2;
 constexpr int kGroupBytes = 64 * kTokens * 2;   // 64 channels of an operand
 constexpr int kSmemBytes = 1024 + kBuffers * kOperandBytes + kStages * kStageBytes;
-constexpr int kGradThreads = 512;
-constexpr int kRestoreWarps = 8;
+constexpr int kGradThreads = 640;
+constexpr int kSumWarps = 8;
+constexpr int kRestoreWarps = 4;         // of each of the two groups
+// Registers per thread after the split (warpgroups: loads and matrix
+// instructions, 2 of sums, 2 of restoring); together no more than the
+// launch's 96 for each of five.
+constexpr int kIssueRegs = 40, kSumRegs = 160, kRestoreRegs = 56;
+static_assert(kIssueRegs + 2 * kSumRegs + 2 * kRestoreRegs <= 5 * 96, "the block's registers");
 
 }  // namespace
 
@@ -131,6 +145,39 @@ __device__ __forceinline__ void put_grad(const WeightGradParams& p, int64_t at, 
     }
 }
 
+// Consecutive rows of dW at one column: `count` of a thread's kN sums, the
+// rows `stride` bytes apart.  The address advances step by step (and is
+// hidden from the compiler, which would otherwise compute all kN at once and
+// spill the sums).
+template <bool kBf16, bool kAdd, int kN>
+__device__ __forceinline__ void store_column(char* d, int64_t stride, int count,
+                                             const float (&sum)[kN]) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        if (j < count) {
+            float v = sum[j];
+            if constexpr (kBf16) {
+                uint16_t h;
+                if constexpr (kAdd) {
+                    asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(d) : "memory");
+                    v = __fadd_rn(bf_1(h), v);
+                }
+                h = to_bf16(v);
+                asm volatile("st.global.u16 [%0], %1;" ::"l"(d), "h"(h) : "memory");
+            } else {
+                if constexpr (kAdd) {
+                    float old;
+                    asm volatile("ld.global.f32 %0, [%1];" : "=f"(old) : "l"(d) : "memory");
+                    v = __fadd_rn(old, v);
+                }
+                asm volatile("st.global.f32 [%0], %1;" ::"l"(d), "f"(v) : "memory");
+            }
+        }
+        d += stride;
+        asm volatile("" : "+l"(d));
+    }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
 weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
     extern __shared__ uint8_t raw[];
@@ -165,7 +212,7 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
         }
         for (int a = 0; a < 2; ++a) {
             tc::mbar_init(summed(a), 1);
-            tc::mbar_init(stored(a), 2 * 4);
+            tc::mbar_init(stored(a), 2 * kSumWarps);
         }
         tc::mbar_init_fence();
         tc::tma_prefetch_map(&p.dy);
@@ -183,6 +230,7 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
 
     bool ok = true;
     Segment s;
+    if (warp < 4) tc::give_registers<kIssueRegs>();
     if (warp == 0) {
         if (lane == 0) {
             int st = 0;
@@ -197,6 +245,8 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
                     tc::mbar_expect(full(st), kStageBytes);
                     const int t = k * kTokens;
                     tc::tma_load(codes + st * kCodeBytes, &p.codes, i, t, full(st));
+                    tc::tma_load(codes + st * kCodeBytes + kCodeBytes / 2, &p.codes, i + 64, t,
+                                 full(st));
                     tc::tma_load(steps + st * kStepBytes, &p.steps, (i / kBlockChannels) & ~15, t,
                                  full(st));
                     tc::tma_load(stages + st * kDyBytes, &p.dy, o, t, full(st));
@@ -225,9 +275,12 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
             int st = 0, b = 0, acc = 0;
             uint32_t b_round = 0, acc_round = 0;
             for (int n = 0; ok && segment(p, pairs, pair, n, s); ++n) {
-                if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
-                tc::fence_after_sync();
                 for (int k = s.first; k < s.last; ++k) {
+                    const int step = (k - s.first) % kChunk;
+                    if (step == 0) {
+                        if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
+                        tc::fence_after_sync();
+                    }
                     if (!(ok = tc::mbar_wait(ready(b), b_round & 1))) break;
                     tc::fence_after_sync();
                     const uint64_t x =
@@ -236,100 +289,130 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
 #pragma unroll
                     for (int j = 0; j < kTokens / 16; ++j)   // 16 tokens are 2048 bytes of a group
                         tc::mma(tmem + acc * kTile, x + uint64_t(j * (2048 >> 4)),
-                                y + uint64_t(j * (2048 >> 4)), instruction, k > s.first || j > 0);
+                                y + uint64_t(j * (2048 >> 4)), instruction, step > 0 || j > 0);
                     tc::commit_both(free_(st));
                     tc::commit_both(spent(b));
                     if (++st == kStages) st = 0;
                     if (++b == kBuffers) { b = 0; ++b_round; }
+                    if (step == kChunk - 1 || k == s.last - 1) {
+                        tc::commit_both(summed(acc));
+                        if (++acc == 2) { acc = 0; ++acc_round; }
+                    }
                 }
-                if (!ok) break;
-                tc::commit_both(summed(acc));
-                if (++acc == 2) { acc = 0; ++acc_round; }
             }
         }
         __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
-        const int row = (warp - 4) * 32 + lane;     // lane of the accumulator
+    } else if (warp >= 4 && warp < 12) {
+        tc::take_registers<kSumRegs>();
+        constexpr int kColumns = kTile / 2;
+        const int quarter = warp & 3;               // the lanes this warp may read
+        const int column = (warp - 4) / 4 * kColumns;
+        const int ci = int(rank) * kHalf + quarter * 32 + lane;
         int acc = 0;
         uint32_t acc_round = 0;
-        for (int n = 0; segment(p, pairs, pair, n, s); ++n) {
-            if (!(ok = tc::mbar_wait_warp(summed(acc), acc_round & 1))) break;
-            tc::fence_after_sync();
-            int o, i;
-            tile_origin(p, s.tile, o, i);
-            const int ci = int(rank) * kHalf + row;
-            i += ci;
-            const uint32_t from = tmem + acc * kTile + (uint32_t(warp - 4) << 21);
-            for (int c = 0; c < kTile; c += 32) {
-                uint32_t v[32];
-                tc::tmem_load32(from + c, v);
-                if (s.whole) {
-                    if (i < p.in_features) {
-                        int64_t at = int64_t(o + c) * p.dw_stride + i;
+        float sum[kColumns];
+        for (int n = 0; ok && segment(p, pairs, pair, n, s); ++n) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j, at += p.dw_stride)
-                            if (o + c + j < p.out_features) put_grad(p, at, __uint_as_float(v[j]));
-                    }
-                } else {
-                    float* d = p.partial + (int64_t(s.slot) * kTile + c) * kTile + ci;
+            for (int j = 0; j < kColumns; ++j) sum[j] = 0.0f;
+            for (int k = s.first; k < s.last; k += kChunk) {
+                if (!(ok = tc::mbar_wait_warp(summed(acc), acc_round & 1))) break;
+                tc::fence_after_sync();
+                const uint32_t from = tmem + acc * kTile + column + (uint32_t(quarter) << 21);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) d[j * kTile] = __uint_as_float(v[j]);
+                for (int c = 0; c < kColumns; c += 16) {
+                    uint32_t v[16];
+                    tc::tmem_load16(from + c, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        sum[c + j] = __fadd_rn(sum[c + j], __uint_as_float(v[j]));
                 }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(stored(acc), 0));
+                if (++acc == 2) { acc = 0; ++acc_round; }
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(stored(acc), 0));
-            if (++acc == 2) { acc = 0; ++acc_round; }
+            if (!ok) break;
+            if (s.whole) {
+                int o, i;
+                tile_origin(p, s.tile, o, i);
+                o += column;
+                i += ci;
+                if (i < p.in_features) {
+                    const int64_t size = p.dw_bf16 ? 2 : 4;
+                    char* d = static_cast<char*>(p.dw) + (int64_t(o) * p.dw_stride + i) * size;
+                    const int64_t stride = p.dw_stride * size;
+                    const int count = p.out_features - o;
+                    if (p.dw_bf16) {
+                        if (p.accumulate) store_column<true, true>(d, stride, count, sum);
+                        else store_column<true, false>(d, stride, count, sum);
+                    } else {
+                        if (p.accumulate) store_column<false, true>(d, stride, count, sum);
+                        else store_column<false, false>(d, stride, count, sum);
+                    }
+                }
+            } else {
+                float* d = p.partial + (int64_t(s.slot) * kTile + column) * kTile + ci;
+                store_column<false, false>(reinterpret_cast<char*>(d), kTile * 4, kColumns, sum);
+            }
         }
-    } else if (warp >= 8) {
-        const int t = int(threadIdx.x) - 256;
-        const int chunk = t & 7;                    // 16 channels
-        const int group = chunk >> 2;               // of 64
-        int st = 0, b = 0;
-        uint32_t round = 0, b_round = 0;
+    } else if (warp >= 12) {
+        tc::give_registers<kRestoreRegs>();
+        const int turn = (warp - 12) >> 2;          // of the two groups
+        const int group = warp & 1;                 // 64 channels of the operand
+        const int chunk = lane & 3;                 // 16 channels of those
+        // 8 neighbouring lanes are 4 chunks of two rows: they read 128 consecutive bytes, and
+        // as the 16-byte pieces of a row are permuted by the row's number, write all 32 banks
+        const int row = ((warp & 2) << 4) + (lane >> 2);
+        const uint32_t read = uint32_t(group * (kCodeBytes / 2) + row * 64 + chunk * 16);
+        const uint32_t write = uint32_t(group * kGroupBytes + row * 128);
+        const uint32_t piece0 = uint32_t((chunk * 2) ^ (row & 7)) * 16;
+        const uint32_t piece1 = uint32_t((chunk * 2 + 1) ^ (row & 7)) * 16;
+        uint32_t step0 = 0;                         // steps of the main loop before this segment
         for (int n = 0; ok && segment(p, pairs, pair, n, s); ++n) {
             int o, i;
             tile_origin(p, s.tile, o, i);
-            const int block = ((i + int(rank) * kHalf) / kBlockChannels & 15) + (chunk >> 1);
-            for (int k = s.first; k < s.last; ++k) {
+            const uint32_t block = uint32_t(((i + int(rank) * kHalf) / kBlockChannels & 15) +
+                                            group * 2 + (chunk >> 1));
+            const uint32_t count = uint32_t(s.last - s.first);
+            for (uint32_t k = (step0 & 1) ^ uint32_t(turn); k < count; k += 2) {
+                const uint32_t st = (step0 + k) % kStages, round = (step0 + k) / kStages;
+                const uint32_t b = (step0 + k) % kBuffers, b_round = (step0 + k) / kBuffers;
                 if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
-                if (!(ok = tc::mbar_wait_warp(spent(b), (b_round & 1) ^ 1))) break;
+                uint32_t w[4][4], step[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = (t >> 3) + 32 * h;   // token
-                    uint32_t w[4], step;
+                for (int h = 0; h < 4; ++h) {
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(codes + st * kCodeBytes + row * kHalf + chunk * 16));
+                                 : "=r"(w[h][0]), "=r"(w[h][1]), "=r"(w[h][2]), "=r"(w[h][3])
+                                 : "r"(codes + st * kCodeBytes + read + h * 8 * 64));
                     asm volatile("ld.shared.u8 %0, [%1];"
-                                 : "=r"(step)
-                                 : "r"(steps + st * kStepBytes + row * 16 + block));
-                    step = (step << 7) * 0x00010001u;
+                                 : "=r"(step[h])
+                                 : "r"(steps + st * kStepBytes + (row + 8 * h) * 16 + block));
+                }
+                if (!(ok = tc::mbar_wait_warp(spent(b), (b_round & 1) ^ 1))) break;
+                const uint32_t at = operands + b * kOperandBytes + write;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t step2 = step[h] * 0x00800080u;   // the byte as a bf16 exponent
                     uint32_t v[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        v[2 * j] = restore_pair(__byte_perm(w[j], 0, 0x4140), step);
-                        v[2 * j + 1] = restore_pair(__byte_perm(w[j], 0, 0x4342), step);
+                        v[2 * j] = restore_pair(__byte_perm(w[h][j], 0, 0x4140), step2);
+                        v[2 * j + 1] = restore_pair(__byte_perm(w[h][j], 0, 0x4342), step2);
                     }
-                    // 16-byte pieces of a 128-byte row are permuted by the row's number; the
-                    // second group writes its odd piece first, so that 8 lanes fill 32 banks
-                    const uint32_t at = operands + b * kOperandBytes + group * kGroupBytes + row * 128;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int odd = j ^ group;
-                        const uint32_t piece = uint32_t(((chunk & 3) * 2 + odd) ^ (row & 7));
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + piece * 16),
-                                     "r"(odd ? v[4] : v[0]), "r"(odd ? v[5] : v[1]),
-                                     "r"(odd ? v[6] : v[2]), "r"(odd ? v[7] : v[3])
-                                     : "memory");
-                    }
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     at + piece0 + h * 8 * 128),
+                                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     at + piece1 + h * 8 * 128),
+                                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                                 : "memory");
                 }
                 tc::fence_to_async();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(b), 0));
-                if (++st == kStages) { st = 0; ++round; }
-                if (++b == kBuffers) { b = 0; ++b_round; }
             }
+            step0 += count;
         }
     }
     if (!ok) atomicAdd(&g_wait_failures, 1u);
@@ -584,7 +667,7 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
                    out_features, 64, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess)
         e = encode(fn, &p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.codes, x.code_stride, rows,
-                   in_features, kHalf, CU_TENSOR_MAP_SWIZZLE_NONE);
+                   in_features, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e == cudaSuccess)
         e = encode(fn, &p.steps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.steps, x.step_stride, rows,
                    ceil_div(in_features, kBlockChannels), 16, CU_TENSOR_MAP_SWIZZLE_NONE);
