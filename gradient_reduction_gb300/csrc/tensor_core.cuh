@@ -25,6 +25,19 @@ __device__ __forceinline__ void cluster_sync() {
                  ::: "memory");
 }
 
+// True in one lane of a converged warp.  Loads and matrix instructions are
+// issued behind this: the compiler knows that one thread is left and feeds
+// them from uniform registers.  Behind `lane == 0` it builds a loop over the
+// active threads around each, which cost the issuing warp about 100 cycles an
+// instruction.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // The address of the same shared-memory location in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -46,8 +59,14 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 }
 
 // Arrives on a barrier of any CTA of the cluster (an address from map_to).
+// What the arrival announces lies in the arriving CTA: operands in its shared
+// memory, which its writers have ordered before the tensor core's reads with
+// fence_to_async, or reads of its tensor memory that have completed.  So the
+// release is at CTA scope; a release at cluster scope also waits for every
+// earlier access of the thread, 1.5 microseconds of a pair's ring each time
+// (8192 tokens, 4096 x 4096: 341 us with it, 230 us without).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
 
@@ -59,7 +78,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
             : "r"(bar), "r"(parity)

@@ -41,8 +41,7 @@ namespace {
 constexpr int kTile = 256;               // in-features and out-features of a tile
 constexpr int kHalf = 128;               // of each CTA
 constexpr int kTokens = 64;              // per step of the main loop
-constexpr int kStages = 6;               // TMA ring
-constexpr int kBuffers = 4;              // ring of restored operands
+constexpr int kStages = 5;               // ring of loaded inputs and restored operands
 constexpr int kChunk = 16;               // main-loop steps per accumulator
 constexpr int kDyBytes = kHalf * kTokens * 2;
 constexpr int kCodeBytes = kHalf * kTokens;
@@ -50,7 +49,7 @@ constexpr int kStepBytes = 16 * kTokens; // 16 step bytes a token, 4 of them use
 constexpr int kStageBytes = kDyBytes + kCodeBytes + kStepBytes;
 constexpr int kOperandBytes = kHalf * kTokens * 2;
 constexpr int kGroupBytes = 64 * kTokens * 2;   // 64 channels of an operand
-constexpr int kSmemBytes = 1024 + kBuffers * kOperandBytes + kStages * kStageBytes;
+constexpr int kSmemBytes = 1024 + kStages * (kOperandBytes + kStageBytes);
 constexpr int kGradThreads = 640;
 constexpr int kSumWarps = 8;
 constexpr int kRestoreWarps = 4;         // of each of the two groups
@@ -181,21 +180,20 @@ __device__ __forceinline__ void store_column(char* d, int64_t stride, int count,
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
 weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kBuffers + 4];
+    __shared__ __align__(8) uint64_t bars[3 * kStages + 4];
     __shared__ uint32_t tmem_slot;
 
     const uint32_t base = (tc::smem_addr(raw) + 1023u) & ~1023u;
-    const uint32_t operands = base;                          // [kBuffers], 1024-byte aligned
-    const uint32_t stages = base + kBuffers * kOperandBytes; // [kStages] dY
+    const uint32_t operands = base;                          // [kStages], 1024-byte aligned
+    const uint32_t stages = base + kStages * kOperandBytes; // [kStages] dY
     const uint32_t codes = stages + kStages * kDyBytes;      // [kStages] codes
     const uint32_t steps = codes + kStages * kCodeBytes;     // [kStages] step bytes
     const uint32_t bar0 = tc::smem_addr(bars);
     const auto full = [&](int s) { return bar0 + 8u * s; };                         // loads landed
     const auto free_ = [&](int s) { return bar0 + 8u * (kStages + s); };            // stage consumed
-    const auto ready = [&](int b) { return bar0 + 8u * (2 * kStages + b); };        // restored, both CTAs
-    const auto spent = [&](int b) { return bar0 + 8u * (2 * kStages + kBuffers + b); };
-    const auto summed = [&](int a) { return bar0 + 8u * (2 * kStages + 2 * kBuffers + a); };
-    const auto stored = [&](int a) { return bar0 + 8u * (2 * kStages + 2 * kBuffers + 2 + a); };
+    const auto ready = [&](int s) { return bar0 + 8u * (2 * kStages + s); };        // restored, both CTAs
+    const auto summed = [&](int a) { return bar0 + 8u * (3 * kStages + a); };
+    const auto stored = [&](int a) { return bar0 + 8u * (3 * kStages + 2 + a); };
 
     const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
     const uint32_t rank = tc::cluster_rank();
@@ -205,10 +203,7 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(full(s), 1);
             tc::mbar_init(free_(s), 1);
-        }
-        for (int b = 0; b < kBuffers; ++b) {
-            tc::mbar_init(ready(b), 2 * kRestoreWarps);
-            tc::mbar_init(spent(b), 1);
+            tc::mbar_init(ready(s), 2 * kRestoreWarps);
         }
         for (int a = 0; a < 2; ++a) {
             tc::mbar_init(summed(a), 1);
@@ -232,7 +227,7 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
     Segment s;
     if (warp < 4) tc::give_registers<kIssueRegs>();
     if (warp == 0) {
-        if (lane == 0) {
+        if (tc::elect_one()) {
             int st = 0;
             uint32_t round = 0;
             for (int n = 0; ok && segment(p, pairs, pair, n, s); ++n) {
@@ -263,41 +258,35 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
                 ok &= tc::mbar_wait(full(k), (uses - 1) & 1);
                 if (ok) ok = tc::mbar_wait(free_(k), (uses - 1) & 1);
             }
-            for (int b = 0; ok && b < kBuffers; ++b) {
-                const uint32_t uses = total / kBuffers + (uint32_t(b) < total % kBuffers);
-                if (uses > 0) ok = tc::mbar_wait(spent(b), (uses - 1) & 1);
-            }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && tc::elect_one()) {
             constexpr uint32_t instruction = tc::bf16_instruction(kTile, kTile);
-            int st = 0, b = 0, acc = 0;
-            uint32_t b_round = 0, acc_round = 0;
+            const uint64_t x0 = tc::operand(operands, kGroupBytes, 1024);
+            const uint64_t y0 = tc::operand(stages, kGroupBytes, 1024);
+            uint32_t st = 0, round = 0, acc = 0, acc_round = 0;
             for (int n = 0; ok && segment(p, pairs, pair, n, s); ++n) {
-                for (int k = s.first; k < s.last; ++k) {
-                    const int step = (k - s.first) % kChunk;
-                    if (step == 0) {
-                        if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
+                for (int left = s.last - s.first; ok && left > 0; left -= kChunk) {
+                    if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
+                    const uint32_t d = tmem + acc * kTile;
+                    bool add = false;
+                    for (int k = min(left, kChunk); k > 0; --k) {
+                        if (!(ok = tc::mbar_wait(ready(st), round & 1))) break;
                         tc::fence_after_sync();
-                    }
-                    if (!(ok = tc::mbar_wait(ready(b), b_round & 1))) break;
-                    tc::fence_after_sync();
-                    const uint64_t x =
-                        tc::operand(operands + b * kOperandBytes, kGroupBytes, 1024);
-                    const uint64_t y = tc::operand(stages + st * kDyBytes, kGroupBytes, 1024);
+                        const uint64_t x = x0 + st * (kOperandBytes >> 4);
+                        const uint64_t y = y0 + st * (kDyBytes >> 4);
 #pragma unroll
-                    for (int j = 0; j < kTokens / 16; ++j)   // 16 tokens are 2048 bytes of a group
-                        tc::mma(tmem + acc * kTile, x + uint64_t(j * (2048 >> 4)),
-                                y + uint64_t(j * (2048 >> 4)), instruction, step > 0 || j > 0);
-                    tc::commit_both(free_(st));
-                    tc::commit_both(spent(b));
-                    if (++st == kStages) st = 0;
-                    if (++b == kBuffers) { b = 0; ++b_round; }
-                    if (step == kChunk - 1 || k == s.last - 1) {
-                        tc::commit_both(summed(acc));
-                        if (++acc == 2) { acc = 0; ++acc_round; }
+                        for (int j = 0; j < kTokens / 16; ++j) {  // 16 tokens: 2048 bytes of a group
+                            tc::mma(d, x + j * (2048 >> 4), y + j * (2048 >> 4), instruction, add);
+                            add = true;
+                        }
+                        tc::commit_both(free_(st));
+                        if (++st == kStages) { st = 0; ++round; }
                     }
+                    if (!ok) break;
+                    tc::commit_both(summed(acc));
+                    if (++acc == 2) { acc = 0; ++acc_round; }
                 }
             }
         }
@@ -376,7 +365,6 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
             const uint32_t count = uint32_t(s.last - s.first);
             for (uint32_t k = (step0 & 1) ^ uint32_t(turn); k < count; k += 2) {
                 const uint32_t st = (step0 + k) % kStages, round = (step0 + k) / kStages;
-                const uint32_t b = (step0 + k) % kBuffers, b_round = (step0 + k) / kBuffers;
                 if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
                 uint32_t w[4][4], step[4];
 #pragma unroll
@@ -388,34 +376,37 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
                                  : "=r"(step[h])
                                  : "r"(steps + st * kStepBytes + (row + 8 * h) * 16 + block));
                 }
-                if (!(ok = tc::mbar_wait_warp(spent(b), (b_round & 1) ^ 1))) break;
-                const uint32_t at = operands + b * kOperandBytes + write;
+                uint32_t v[4][8];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     const uint32_t step2 = step[h] * 0x00800080u;   // the byte as a bf16 exponent
-                    uint32_t v[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        v[2 * j] = restore_pair(__byte_perm(w[h][j], 0, 0x4140), step2);
-                        v[2 * j + 1] = restore_pair(__byte_perm(w[h][j], 0, 0x4342), step2);
+                        v[h][2 * j] = restore_pair(__byte_perm(w[h][j], 0, 0x4140), step2);
+                        v[h][2 * j + 1] = restore_pair(__byte_perm(w[h][j], 0, 0x4342), step2);
                     }
+                }
+                const uint32_t at = operands + st * kOperandBytes + write;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
                                      at + piece0 + h * 8 * 128),
-                                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                 "r"(v[h][0]), "r"(v[h][1]), "r"(v[h][2]), "r"(v[h][3])
                                  : "memory");
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
                                      at + piece1 + h * 8 * 128),
-                                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                                 "r"(v[h][4]), "r"(v[h][5]), "r"(v[h][6]), "r"(v[h][7])
                                  : "memory");
                 }
                 tc::fence_to_async();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(b), 0));
+                if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(st), 0));
             }
             step0 += count;
         }
     }
     if (!ok) atomicAdd(&g_wait_failures, 1u);
+    __syncwarp();
     // nobody leaves while the other CTA may still signal or read this one
     tc::fence_before_sync();
     __syncthreads();
