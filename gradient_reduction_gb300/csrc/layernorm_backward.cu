@@ -1,5 +1,11 @@
 // Layer norm, backward: dx needs two sums along every row, dweight and dbias
 // one sum each down every column.
+//
+// Rows of up to 8192 channels take one pass (norm_grad_fused): the threads of
+// a block own columns, keep their sums in registers over all of the block's
+// rows, and load the next row while they work on one.  The blocks' column
+// sums are joined by a second, small kernel in a fixed order.  Longer rows
+// take two passes, row sums first, then columns.
 #include <algorithm>
 
 #include "ops_device.cuh"
@@ -19,11 +25,13 @@ struct NormGradParams {
     void* dx;
     int64_t dx_stride;
     float2* row_avg;          // [rows]: avg(g), avg(g * xhat)
-    float* partial;           // [slices][2][width]: dweight and dbias of a slice of the rows
+    float* partial;           // [slices][2][partial_width]: dweight and dbias of a slice of the
+                              // rows; NULL when neither is wanted
     int64_t rows;
     int width;
+    int partial_width;        // width rounded up to 4
     int slices;
-    int64_t slice_rows;       // rows per slice
+    int64_t slice_rows;       // rows per slice (two passes)
     float inv_width;
     int param_bf16;
     int param_vec;
@@ -34,6 +42,7 @@ struct JoinParams {
     void* dweight;            // NULL: not wanted
     void* dbias;
     int width;
+    int partial_width;
     int slices;
     int grad_bf16;
     int accumulate;
@@ -56,11 +65,172 @@ struct Source {
             load_raw(static_cast<const T*>(p.x) + row * p.x_stride + c, raw);
         }
     }
+    __device__ __forceinline__ void zero() {
+        if constexpr (kSaved) {
+#pragma unroll
+            for (int i = 0; i < int(sizeof(codes.w) / 4); ++i) codes.w[i] = 0;
+            step = 0.0f;
+        } else {
+            zero_raw(raw);
+        }
+    }
     __device__ __forceinline__ void get(float (&f)[V]) const {
         if constexpr (kSaved) decode<V>(codes, step, f);
         else unpack(raw, f);
     }
 };
+
+// The sums of `a` and `b` over the blockDim.x threads that share threadIdx.y.
+// `s` has 32 entries per threadIdx.y; calls in a row alternate between two of
+// them (one barrier, none behind the reads).
+__device__ __forceinline__ void row_sums(float& a, float& b, float2 (*s)[32]) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if (blockDim.x == 32) return;
+    const int lane = int(threadIdx.x) & 31, nw = int(blockDim.x) >> 5;
+    if (lane == 0) s[threadIdx.y][threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const float2 v = lane < nw ? s[threadIdx.y][lane] : make_float2(0.0f, 0.0f);
+    a = warp_sum(v.x);
+    b = warp_sum(v.y);
+}
+
+// One pass: blockDim.x threads (a multiple of 32, at most 512) share a row,
+// NV vectors of V channels each, vector i at (i * blockDim.x + threadIdx.x) *
+// V; blockDim.y rows at a time per block, the blocks' rows interleaved.
+template <typename T, int V, int NV, bool kSaved>
+__global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ NormGradParams p) {
+    constexpr int E = V * NV;
+    __shared__ float2 s[2][8][32];
+    extern __shared__ float columns[];           // [blockDim.y - 1][2][threads * E]
+    grid_wait();
+    grid_release();
+    const int tx = int(threadIdx.x), threads = int(blockDim.x);
+    float w[E], dw[E], db[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) { w[k] = 1.0f; dw[k] = 0.0f; db[k] = 0.0f; }
+    if (p.weight) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + tx) * V;
+            float f[V];
+            if (c < p.width) {
+                load_params<V>(p.weight, p.param_bf16, p.param_vec, c, f);
+#pragma unroll
+                for (int k = 0; k < V; ++k) w[i * V + k] = f[k];
+            }
+        }
+    }
+    const int64_t stride = int64_t(gridDim.x) * blockDim.y;
+    int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    Raw<T, V> dy[NV];
+    Source<T, V, kSaved> x[NV];
+    float mean = 0.0f, rstd = 0.0f;
+    const auto load = [&](int64_t r) {
+        const bool live = r < p.rows;
+        mean = live ? p.mean[r] : 0.0f;
+        rstd = live ? p.rstd[r] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + tx) * V;
+            zero_raw(dy[i]);
+            x[i].zero();
+            if (live && c < p.width) {
+                load_raw(static_cast<const T*>(p.dy) + r * p.dy_stride + c, dy[i]);
+                x[i].load(p, r, c);
+            }
+        }
+    };
+    load(row);
+    // the same number of turns for every row of a block: the barriers are shared
+    int turn = 0;
+    for (int64_t first = int64_t(blockIdx.x) * blockDim.y; first < p.rows;
+         first += stride, row += stride, turn ^= 1) {
+        float g[E], h[E];
+        float a = 0.0f, b = 0.0f;
+        const float r = rstd;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float d[V], f[V];
+            unpack(dy[i], d);
+            x[i].get(f);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int e = i * V + k;
+                // a channel past the row's end has d = 0
+                h[e] = __fmul_rn(__fsub_rn(f[k], mean), r);
+                g[e] = __fmul_rn(d[k], w[e]);
+                a = __fadd_rn(a, g[e]);
+                b = __fmaf_rn(g[e], h[e], b);
+                dw[e] = __fmaf_rn(d[k], h[e], dw[e]);
+                db[e] = __fadd_rn(db[e], d[k]);
+            }
+        }
+        load(row + stride);
+        row_sums(a, b, s[turn]);
+        a = __fmul_rn(a, p.inv_width);
+        b = __fmul_rn(b, p.inv_width);
+        if (row < p.rows) {
+            T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * threads + tx) * V;
+                if (c < p.width) {
+                    float d[V];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        const int e = i * V + k;
+                        d[k] = __fmul_rn(r, __fmaf_rn(-h[e], b, __fsub_rn(g[e], a)));
+                    }
+                    Raw<T, V> out;
+                    pack(d, out);
+                    store_raw(dx + c, out);
+                }
+            }
+        }
+    }
+    if (!p.partial) return;
+    // the block's rows-at-a-time, added in order by the first
+    if (blockDim.y > 1) {
+        __syncthreads();
+        float* mine = columns + (int(threadIdx.y) - 1) * 2 * threads * E;
+        if (threadIdx.y > 0) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                mine[k * threads + tx] = dw[k];
+                mine[(E + k) * threads + tx] = db[k];
+            }
+        }
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+        for (int y = 0; y + 1 < int(blockDim.y); ++y) {
+            const float* other = columns + y * 2 * threads * E;
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                dw[k] = __fadd_rn(dw[k], other[k * threads + tx]);
+                db[k] = __fadd_rn(db[k], other[(E + k) * threads + tx]);
+            }
+        }
+    }
+    float* to = p.partial + int64_t(blockIdx.x) * 2 * p.partial_width;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * threads + tx) * V;
+        if (c < p.width) {
+            if constexpr (V >= 8) {
+#pragma unroll
+                for (int k = 0; k < V; k += 4) {
+                    const int e = i * V + k;
+                    st_f4(to + c + k, dw[e], dw[e + 1], dw[e + 2], dw[e + 3]);
+                    st_f4(to + p.partial_width + c + k, db[e], db[e + 1], db[e + 2], db[e + 3]);
+                }
+            } else {
+                to[c] = dw[i];
+                to[p.partial_width + c] = db[i];
+            }
+        }
+    }
+}
 
 // avg(g) and avg(g * xhat) of every row: blockDim.x threads per row.
 template <typename T, int V, bool kSaved>
@@ -148,15 +318,16 @@ __global__ void __launch_bounds__(256) norm_grad_columns(const __grid_constant__
             float t = 0.0f;
 #pragma unroll
             for (int y = 0; y < 8; ++y) t = __fadd_rn(t, s[y][i]);
-            if (base + i < width)
-                p.partial[(int64_t(blockIdx.y) * 2 + pass) * width + base + i] = t;
+            if (p.partial && base + i < width)
+                p.partial[(int64_t(blockIdx.y) * 2 + pass) * p.partial_width + base + i] = t;
         }
         __syncthreads();
     }
 }
 
-// dweight and dbias from the slices' partial sums, added in slice order:
-// 32 columns by 8 groups of slices per block; blockIdx.y picks the gradient.
+// dweight and dbias from the slices' partial sums, in a fixed order: 32
+// columns by 8 groups of slices per block, a group's loads eight at a time;
+// blockIdx.y picks the gradient.
 __global__ void __launch_bounds__(256) norm_grad_join(const __grid_constant__ JoinParams p) {
     __shared__ float s[8][33];
     grid_wait();
@@ -165,9 +336,17 @@ __global__ void __launch_bounds__(256) norm_grad_join(const __grid_constant__ Jo
     if (!out) return;
     const int c = int(blockIdx.x) * 32 + int(threadIdx.x);
     float t = 0.0f;
-    if (c < p.width)
-        for (int i = int(threadIdx.y); i < p.slices; i += 8)
-            t = __fadd_rn(t, p.partial[(int64_t(i) * 2 + blockIdx.y) * p.width + c]);
+    if (c < p.width) {
+        const float* from = p.partial + int64_t(blockIdx.y) * p.partial_width + c;
+        for (int i = int(threadIdx.y); i < p.slices; i += 64) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = i + 8 * j < p.slices ? from[int64_t(i + 8 * j) * 2 * p.partial_width] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t = __fadd_rn(t, v[j]);
+        }
+    }
     s[threadIdx.y][threadIdx.x] = t;
     __syncthreads();
     if (threadIdx.y != 0 || c >= p.width) return;
@@ -183,7 +362,8 @@ __global__ void __launch_bounds__(256) norm_grad_join(const __grid_constant__ Jo
     }
 }
 
-// Slices of the rows: enough blocks for the GPU, at least 16 rows each.
+// Two passes: slices of the rows, enough blocks for the GPU, at least 16 rows
+// each.
 constexpr int kMaxSlices = 256;
 int slice_count(int64_t rows, int64_t width) {
     const int64_t tiles = ceil_div(width, 512);
@@ -191,8 +371,47 @@ int slice_count(int64_t rows, int64_t width) {
     return int(std::max<int64_t>(1, std::min<int64_t>({want, ceil_div(rows, 16), kMaxSlices})));
 }
 
+// One pass: 16 channels a thread (8 for short fp32 rows), 512 threads a row at
+// the most, blocks of at least 256 threads, 512 threads per SM (its 128
+// registers a thread are the whole register file).
+constexpr int kFusedWidth = 8192;
+constexpr int kSms = 152;
+struct FusedShape {
+    int threads, per_block;
+    int64_t blocks;
+};
+FusedShape fused_shape(int64_t rows, int64_t width, int v, int nv) {
+    FusedShape f;
+    f.threads = int(round_up(ceil_div(width, int64_t(v) * nv), 32));
+    f.per_block = std::max(1, 256 / f.threads);
+    const int64_t resident = int64_t(kSms) * (512 / (f.threads * f.per_block));
+    f.blocks = std::max<int64_t>(1, std::min(resident, ceil_div(rows, f.per_block)));
+    return f;
+}
+
+template <typename T, int V, int NV, bool kSaved>
+cudaError_t launch_fused(NormGradParams& p, cudaStream_t s) {
+    const FusedShape f = fused_shape(p.rows, p.width, V, NV);
+    p.slices = int(f.blocks);
+    void* args[] = {&p};
+    const size_t smem = size_t(f.per_block - 1) * 2 * f.threads * V * NV * 4;
+    // at most 7 * 2 * 32 * 16 floats: within the 48 KB every kernel may have
+    return launch_grid((const void*)norm_grad_fused<T, V, NV, kSaved>, dim3(unsigned(f.blocks)),
+                       dim3(f.threads, f.per_block), smem, args, s);
+}
+
 template <typename T, int V, bool kSaved>
 cudaError_t launch_backward(NormGradParams& p, cudaStream_t s) {
+    if (p.width <= kFusedWidth) {
+        if constexpr (V == 16) return launch_fused<T, 16, 1, kSaved>(p, s);
+        else if constexpr (V == 8 && sizeof(T) == 4)
+            return p.width <= 4096 ? launch_fused<T, 8, 1, kSaved>(p, s)
+                                   : launch_fused<T, 8, 2, kSaved>(p, s);
+        else if constexpr (V == 8) return launch_fused<T, 8, 2, kSaved>(p, s);
+        else return launch_fused<T, 1, 16, kSaved>(p, s);
+    }
+    p.slices = slice_count(p.rows, p.width);
+    p.slice_rows = ceil_div(p.rows, p.slices);
     void* args[] = {&p};
     const int64_t vecs = ceil_div(p.width, V);
     const int threads = int(std::min<int64_t>(256, round_up(vecs, 32)));
@@ -223,7 +442,13 @@ dpr_status dpr_layernorm_backward_workspace(int64_t rows, int64_t width, int64_t
     *bytes = 0;
     const dpr_status st = check_matrix_size(rows, width);
     if (st != DPR_OK) return st;
-    *bytes = round_up(rows * 8, 16) + int64_t(slice_count(rows, width)) * 2 * width * 4;
+    // the most that any access width asks for: 32 threads upward share a row
+    int64_t slices = slice_count(rows, width), sums = round_up(rows * 8, 16);
+    if (width <= kFusedWidth) {
+        slices = std::max(fused_shape(rows, width, 16, 1).blocks, fused_shape(rows, width, 8, 1).blocks);
+        sums = 0;
+    }
+    *bytes = sums + slices * 2 * round_up(width, 4) * 4;
     return DPR_OK;
 }
 
@@ -287,10 +512,11 @@ dpr_status dpr_layernorm_backward(const void* dy, int64_t dy_stride, const void*
         p.mean = mean; p.rstd = rstd;
         p.dx = dx; p.dx_stride = dx_stride;
         p.row_avg = static_cast<float2*>(workspace);
-        p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(rows * 8, 16));
+        const int64_t sums = width <= kFusedWidth ? 0 : round_up(rows * 8, 16);
+        if (dweight || dbias)
+            p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums);
+        p.partial_width = int(round_up(width, 4));
         p.rows = rows; p.width = int(width);
-        p.slices = slice_count(rows, width);
-        p.slice_rows = ceil_div(rows, p.slices);
         p.inv_width = 1.0f / float(width);
         p.param_bf16 = param_dtype == DPR_BF16;
         p.param_vec = aligned(weight, 16);
@@ -315,7 +541,7 @@ dpr_status dpr_layernorm_backward(const void* dy, int64_t dy_stride, const void*
                                       : launch_source<float, 1>(p, s);
         }
         if (e != cudaSuccess) return record_cuda_status(e);
-        j.partial = p.partial; j.slices = p.slices;
+        j.partial = p.partial; j.slices = p.slices; j.partial_width = p.partial_width;
     }
     if (dweight || dbias) {
         void* args[] = {&j};

@@ -415,10 +415,14 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
     if (warp == 1) tc::tmem_free(tmem, 512);
 }
 
-// Tiles summed in parts: the parts in token order, then as put_grad.  One
-// block of 256 threads per 8 out-features of a dealt-out tile.
-__global__ void __launch_bounds__(256) weight_grad_join(const __grid_constant__ WeightGradParams p,
-                                                        int pairs) {
+// Tiles summed in parts: the parts in token order, then as put_grad.  A block
+// joins two out-features of a dealt-out tile, 64 threads and 4 in-features a
+// thread for each, so that a single tile still spreads over 128 SMs; the
+// parts are loaded eight at a time (one by one the loads' latency made the
+// join of 32 parts take 24 us).
+constexpr int kJoinThreads = 128, kJoinRows = 2, kJoinAhead = 8;
+__global__ void __launch_bounds__(kJoinThreads)
+weight_grad_join(const __grid_constant__ WeightGradParams p, int pairs) {
     grid_wait();
     grid_release();
     const int t = int(blockIdx.x);
@@ -427,21 +431,34 @@ __global__ void __launch_bounds__(256) weight_grad_join(const __grid_constant__ 
     if (first == last) return;               // one pair summed it all
     int o, i;
     tile_origin(p, p.waves * pairs + t, o, i);
-    i += int(threadIdx.x);
-    if (i >= p.in_features) return;
-    float v[8];
+    const int row = int(blockIdx.y) * kJoinRows + (int(threadIdx.x) >> 6);
+    const int column = int(threadIdx.x) & 63;
+    if (o + row >= p.out_features) return;
+    // the first pair's part may be its second piece, every later one's is its first
+    const int slot0 = 2 * first + t - int(int64_t(first) * p.rest_chunk / p.blocks);
+    const float* d = p.partial + int64_t(row) * kTile + column;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q = first; q <= last; q += kJoinAhead) {
+        float w[kJoinAhead][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    for (int q = first; q <= last; ++q) {
-        const int slot = 2 * q + t - int(int64_t(q) * p.rest_chunk / p.blocks);
-        const float* d = p.partial + (int64_t(slot) * kTile + blockIdx.y * 8) * kTile + threadIdx.x;
+        for (int a = 0; a < kJoinAhead; ++a) {
+            if (q + a > last) break;
+            const int slot = q + a == first ? slot0 : 2 * (q + a);
+            const float* f = d + int64_t(slot) * kTile * kTile;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], d[j * kTile]);
+            for (int j = 0; j < 4; ++j) w[a][j] = f[64 * j];
+        }
+#pragma unroll
+        for (int a = 0; a < kJoinAhead; ++a) {
+            if (q + a > last) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __fadd_rn(v[j], w[a][j]);
+        }
     }
-    o += int(blockIdx.y) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (o + j < p.out_features) put_grad(p, int64_t(o + j) * p.dw_stride + i, v[j]);
+    for (int j = 0; j < 4; ++j)
+        if (i + column + 64 * j < p.in_features)
+            put_grad(p, int64_t(o + row) * p.dw_stride + i + column + 64 * j, v[j]);
 }
 
 // Rows copied to 16-byte-aligned ones, for inputs that TMA cannot read.
@@ -675,8 +692,9 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
     if (e == cudaSuccess && q.join) {
         int pairs = int(busy);
         void* jargs[] = {&p, &pairs};
-        e = launch_grid((const void*)weight_grad_join, dim3(unsigned(q.rest_tiles), kTile / 8),
-                        dim3(256), 0, jargs, s);
+        e = launch_grid((const void*)weight_grad_join,
+                        dim3(unsigned(q.rest_tiles), kTile / kJoinRows), dim3(kJoinThreads), 0,
+                        jargs, s);
     }
     return record_cuda_status(e);
 }
