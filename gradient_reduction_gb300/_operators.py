@@ -50,74 +50,105 @@ def dpr_checkpoint_empty(rows: int, width: int, device=None) -> Checkpoint:
     return Checkpoint(codes[:, :width], steps[:, :blocks])
 
 
-def _on_device(t: torch.Tensor, what: str) -> None:
+def _wrong_device(t: torch.Tensor, what: str):
     if not t.is_cuda:
         raise ValueError(f"{what}: need a CUDA tensor")
-    dev = torch.cuda.current_device()
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: tensor on cuda:{t.get_device()}, current device is cuda:{dev}")
+    raise ValueError(f"{what}: tensor on cuda:{t.get_device()}, current device is "
+                     f"cuda:{torch.cuda.current_device()}")
 
 
-def _matrix(t: torch.Tensor, what: str, dtypes=_DTYPES):
+# The current device without torch.cuda.current_device()'s lazy initialisation
+# checks (0.3 us a call); a CUDA tensor at hand means that CUDA is up.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _device(t: torch.Tensor, what: str) -> int:
+    """The current device, on which the call's tensors have to be: the kernels
+    would fault on another's memory."""
+    dev = t.get_device()
+    if dev < 0 or dev != _get_device():
+        _wrong_device(t, what)
+    return dev
+
+
+def _matrix(t: torch.Tensor, what: str, dev: int):
     """(address, rows, width, row stride) of a tensor as a matrix."""
-    _on_device(t, what)
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what}: {t.dtype} is not among {', '.join(map(str, dtypes))}")
+    if t.get_device() != dev:
+        _wrong_device(t, what)
     if t.dim() != 2:
-        if t.dim() == 0:
-            raise ValueError(f"{what}: need at least one dimension")
-        try:
-            t = t.view(-1, t.shape[-1]) if t.numel() else t.new_empty(
-                (t.shape[:-1].numel(), t.shape[-1]))
-        except RuntimeError:
-            raise ValueError(f"{what}: the leading dimensions do not merge into one row stride, "
-                             f"shape {tuple(t.shape)} strides {t.stride()}") from None
+        t = _merge(t, what)
     rows, width = t.shape
     stride, inner = t.stride()
-    if width > 1 and inner != 1:
+    if inner != 1 and width > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return t.data_ptr(), rows, width, stride if rows > 1 else max(stride, width)
+    return t.data_ptr(), rows, width, stride if rows > 1 or stride > width else width
 
 
-def _same(what: str, got, want) -> None:
-    if tuple(got) != tuple(want):
-        raise ValueError(f"{what}: need {want[0]} rows of {want[1]}, got {got[0]} of {got[1]}")
+def _merge(t: torch.Tensor, what: str) -> torch.Tensor:
+    if t.dim() == 0:
+        raise ValueError(f"{what}: need at least one dimension")
+    if t.numel() == 0:
+        return t.new_empty((t.shape[:-1].numel(), t.shape[-1]))
+    try:
+        return t.view(-1, t.shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{what}: the leading dimensions do not merge into one row stride, "
+                         f"shape {tuple(t.shape)} strides {t.stride()}") from None
 
 
-def _checkpoint_arg(c, what: str):
-    """(C struct, rows, width) of a Checkpoint."""
+def _code(t: torch.Tensor, what: str) -> int:
+    """The type code of a bf16 or fp32 tensor."""
+    c = _DTYPES.get(t.dtype)
+    if c is None:
+        raise ValueError(f"{what}: {t.dtype} is neither torch.bfloat16 nor torch.float32")
+    return c
+
+
+def _checkpoint_arg(c, what: str, rows: int, width: int, dev: int):
+    """The C struct of a Checkpoint of `rows` x `width`."""
     if not isinstance(c, Checkpoint):
         raise ValueError(f"{what}: need a Checkpoint, got {type(c).__name__}")
-    pc, rows, width, sc = _matrix(c.codes, what + ".codes", (torch.int8,))
-    ps, srows, blocks, ss = _matrix(c.steps, what + ".steps", (torch.uint8,))
-    if srows != rows or blocks < -(-width // CHECKPOINT_BLOCK):
+    codes, steps = c.codes, c.steps
+    if codes.dtype != torch.int8 or steps.dtype != torch.uint8:
+        raise ValueError(f"{what}: need int8 codes and uint8 steps, got {codes.dtype} and {steps.dtype}")
+    pc, r, w, sc = _matrix(codes, what, dev)
+    ps, sr, blocks, ss = _matrix(steps, what, dev)
+    if r != rows or w != width:
+        _wrong_shape(what, r, w, rows, width)
+    if sr != rows or blocks * CHECKPOINT_BLOCK < width:
         raise ValueError(f"{what}: {rows} rows of {width} codes need as many rows of "
-                         f"{-(-width // CHECKPOINT_BLOCK)} steps, got {srows} of {blocks}")
-    return _CheckpointArg(pc, sc, ps, ss), rows, width
+                         f"{-(-width // CHECKPOINT_BLOCK)} steps, got {sr} of {blocks}")
+    return _CheckpointArg(pc, sc, ps, ss)
 
 
-def _vector(t, n: int, what: str, dtypes=_DTYPES):
+def _wrong_shape(what: str, rows: int, width: int, want_rows: int, want_width: int):
+    raise ValueError(f"{what}: need {want_rows} rows of {want_width}, got {rows} of {width}")
+
+
+def _vector(t, n: int, what: str, dev: int) -> int:
     """Address of a contiguous vector of n elements; 0 for None."""
     if t is None:
         return 0
-    _on_device(t, what)
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what}: {t.dtype} is not among {', '.join(map(str, dtypes))}")
+    if t.get_device() != dev:
+        _wrong_device(t, what)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what}: need {n} contiguous elements")
     return t.data_ptr()
 
 
-_FP32 = (torch.float32,)
+def _statistic(t, n: int, what: str, dev: int) -> int:
+    if t is not None and t.dtype != torch.float32:
+        raise ValueError(f"{what}: need torch.float32, got {t.dtype}")
+    return _vector(t, n, what, dev)
 
 
-def _pair_dtype(a, b, what: str) -> int:
+def _pair_code(a, b, what: str) -> int:
     """The common type code of two optional tensors."""
-    if a is None and b is None:
-        return 0
-    if a is not None and b is not None and a.dtype != b.dtype:
+    if a is None:
+        return 0 if b is None else _code(b, what)
+    if b is not None and a.dtype != b.dtype:
         raise ValueError(f"{what} must have one dtype, got {a.dtype} and {b.dtype}")
-    return _DTYPES[(b if a is None else a).dtype]
+    return _code(a, what)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -127,11 +158,12 @@ def _workspace_bytes(fn: str, *sizes: int) -> int:
     return n.value
 
 
-def _workspace(t, nbytes: int, stream):
+def _workspace(t, nbytes: int, stream, dev: int):
     """The caller's scratch memory, or some from PyTorch's allocator, taken on
     the stream that uses it so that it is not handed out again too early."""
     if t is not None:
-        _on_device(t, "workspace")
+        if t.get_device() != dev:
+            _wrong_device(t, "workspace")
         if not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
             raise ValueError(f"workspace: need {nbytes} contiguous bytes")
         return t
@@ -151,25 +183,25 @@ def dpr_layernorm_forward(x: torch.Tensor, weight, bias, eps: float, y: torch.Te
     and bias (bf16 or fp32) may be None.  mean and rstd ([rows] fp32) are what
     the backward pass needs.  The checkpoints, where given, are written in
     the same pass as dpr_checkpoint_save(x) and (y) would.  y may be x."""
-    px, rows, width, sx = _matrix(x, "x")
-    py, *shape, sy = _matrix(y, "y")
-    _same("y", shape, (rows, width))
+    dev = _device(x, "x")
+    px, rows, width, sx = _matrix(x, "x", dev)
+    py, r, w, sy = _matrix(y, "y", dev)
+    if r != rows or w != width:
+        _wrong_shape("y", r, w, rows, width)
     if y.dtype != x.dtype:
         raise ValueError(f"y: {y.dtype}, but x is {x.dtype}")
-    refs = []
-    for c, what in ((x_checkpoint, "x_checkpoint"), (y_checkpoint, "y_checkpoint")):
-        if c is None:
-            refs.append(None)
-            continue
-        arg, *shape = _checkpoint_arg(c, what)
-        _same(what, shape, (rows, width))
-        refs.append(ctypes.byref(arg))
+    cx = cy = None
+    if x_checkpoint is not None:
+        cx = ctypes.byref(_checkpoint_arg(x_checkpoint, "x_checkpoint", rows, width, dev))
+    if y_checkpoint is not None:
+        cy = ctypes.byref(_checkpoint_arg(y_checkpoint, "y_checkpoint", rows, width, dev))
     st = lib().dpr_layernorm_forward(
-        px, sx, rows, width, _DTYPES[x.dtype], _vector(weight, width, "weight"),
-        _vector(bias, width, "bias"), _pair_dtype(weight, bias, "weight and bias"), eps, py, sy,
-        _vector(mean, rows, "mean", _FP32), _vector(rstd, rows, "rstd", _FP32), refs[0], refs[1],
+        px, sx, rows, width, _code(x, "x"), _vector(weight, width, "weight", dev),
+        _vector(bias, width, "bias", dev), _pair_code(weight, bias, "weight and bias"), eps, py, sy,
+        _statistic(mean, rows, "mean", dev), _statistic(rstd, rows, "rstd", dev), cx, cy,
         _stream(stream))
-    _check("dpr_layernorm_forward", st)
+    if st:
+        _check("dpr_layernorm_forward", st)
 
 
 def dpr_layernorm_backward(dy: torch.Tensor, x, weight, mean: torch.Tensor, rstd: torch.Tensor,
@@ -178,50 +210,57 @@ def dpr_layernorm_backward(dy: torch.Tensor, x, weight, mean: torch.Tensor, rstd
     """dx, dweight and dbias of dpr_layernorm_forward.  `x` is the forward's
     input or its Checkpoint.  dweight and dbias (bf16 or fp32 [width], None
     where not wanted) are added to with `accumulate`.  dx may be dy or x."""
-    pd, rows, width, sd = _matrix(dy, "dy")
-    po, *shape, so = _matrix(dx, "dx")
-    _same("dx", shape, (rows, width))
+    dev = _device(dy, "dy")
+    pd, rows, width, sd = _matrix(dy, "dy", dev)
+    po, r, w, so = _matrix(dx, "dx", dev)
+    if r != rows or w != width:
+        _wrong_shape("dx", r, w, rows, width)
     if dx.dtype != dy.dtype:
         raise ValueError(f"dx: {dx.dtype}, but dy is {dy.dtype}")
     px = sx = 0
     ref = None
     if isinstance(x, torch.Tensor):
-        px, *shape, sx = _matrix(x, "x")
+        px, r, w, sx = _matrix(x, "x", dev)
+        if r != rows or w != width:
+            _wrong_shape("x", r, w, rows, width)
         if x.dtype != dy.dtype:
             raise ValueError(f"x: {x.dtype}, but dy is {dy.dtype}")
     else:
-        arg, *shape = _checkpoint_arg(x, "x")
-        ref = ctypes.byref(arg)
-    _same("x", shape, (rows, width))
+        ref = ctypes.byref(_checkpoint_arg(x, "x", rows, width, dev))
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward pass are needed")
     nbytes = _workspace_bytes("dpr_layernorm_backward_workspace", rows, width)
-    ws = _workspace(workspace, nbytes, stream)
+    ws = _workspace(workspace, nbytes, stream, dev)
     st = lib().dpr_layernorm_backward(
-        pd, sd, px, sx, ref, rows, width, _DTYPES[dy.dtype], _vector(weight, width, "weight"),
-        0 if weight is None else _DTYPES[weight.dtype], _vector(mean, rows, "mean", _FP32),
-        _vector(rstd, rows, "rstd", _FP32), po, so, _vector(dweight, width, "dweight"),
-        _vector(dbias, width, "dbias"), _pair_dtype(dweight, dbias, "dweight and dbias"),
-        int(bool(accumulate)), 0 if ws is None else ws.data_ptr(), nbytes, _stream(stream))
-    _check("dpr_layernorm_backward", st)
+        pd, sd, px, sx, ref, rows, width, _code(dy, "dy"), _vector(weight, width, "weight", dev),
+        0 if weight is None else _code(weight, "weight"), _statistic(mean, rows, "mean", dev),
+        _statistic(rstd, rows, "rstd", dev), po, so, _vector(dweight, width, "dweight", dev),
+        _vector(dbias, width, "dbias", dev), _pair_code(dweight, dbias, "dweight and dbias"),
+        1 if accumulate else 0, 0 if ws is None else ws.data_ptr(), nbytes, _stream(stream))
+    if st:
+        _check("dpr_layernorm_backward", st)
 
 
 def dpr_checkpoint_save(x: torch.Tensor, checkpoint: Checkpoint, stream=None) -> None:
     """Saves x ([..., width] bf16 or fp32) in 8 bits."""
-    px, rows, width, sx = _matrix(x, "x")
-    arg, *shape = _checkpoint_arg(checkpoint, "checkpoint")
-    _same("checkpoint", shape, (rows, width))
-    _check("dpr_checkpoint_save", lib().dpr_checkpoint_save(
-        px, sx, rows, width, _DTYPES[x.dtype], ctypes.byref(arg), _stream(stream)))
+    dev = _device(x, "x")
+    px, rows, width, sx = _matrix(x, "x", dev)
+    arg = _checkpoint_arg(checkpoint, "checkpoint", rows, width, dev)
+    st = lib().dpr_checkpoint_save(px, sx, rows, width, _code(x, "x"), ctypes.byref(arg),
+                                   _stream(stream))
+    if st:
+        _check("dpr_checkpoint_save", st)
 
 
 def dpr_checkpoint_load(checkpoint: Checkpoint, out: torch.Tensor, stream=None) -> None:
     """Restores a checkpoint into out ([..., width] bf16 or fp32)."""
-    po, rows, width, so = _matrix(out, "out")
-    arg, *shape = _checkpoint_arg(checkpoint, "checkpoint")
-    _same("checkpoint", shape, (rows, width))
-    _check("dpr_checkpoint_load", lib().dpr_checkpoint_load(
-        ctypes.byref(arg), rows, width, po, so, _DTYPES[out.dtype], _stream(stream)))
+    dev = _device(out, "out")
+    po, rows, width, so = _matrix(out, "out", dev)
+    arg = _checkpoint_arg(checkpoint, "checkpoint", rows, width, dev)
+    st = lib().dpr_checkpoint_load(ctypes.byref(arg), rows, width, po, so, _code(out, "out"),
+                                   _stream(stream))
+    if st:
+        _check("dpr_checkpoint_load", st)
 
 
 def dpr_linear_weight_grad(dy: torch.Tensor, x_checkpoint: Checkpoint, dweight: torch.Tensor,
@@ -229,23 +268,29 @@ def dpr_linear_weight_grad(dy: torch.Tensor, x_checkpoint: Checkpoint, dweight: 
     """dweight = dy^T x with dy bf16 [..., out_features] and the checkpoint
     of x [rows, in_features]; dweight bf16 or fp32 [out_features,
     in_features], added to with `accumulate`."""
-    pd, rows, out_features, sd = _matrix(dy, "dy", (torch.bfloat16,))
-    arg, xrows, in_features = _checkpoint_arg(x_checkpoint, "x_checkpoint")
-    if xrows != rows:
-        raise ValueError(f"x_checkpoint: {xrows} rows, but dy has {rows}")
+    dev = _device(dy, "dy")
+    pd, rows, out_features, sd = _matrix(dy, "dy", dev)
+    if dy.dtype != torch.bfloat16:
+        raise ValueError(f"dy: need torch.bfloat16, got {dy.dtype}")
     if dweight.dim() != 2:
         raise ValueError("dweight: need a matrix")
-    pw, *shape, sw = _matrix(dweight, "dweight")
-    _same("dweight", shape, (out_features, in_features))
-    ref = ctypes.byref(arg)
+    pw, r, in_features, sw = _matrix(dweight, "dweight", dev)
+    if r != out_features:
+        raise ValueError(f"dweight: {r} rows, but dy has {out_features} out-features")
+    ref = ctypes.byref(_checkpoint_arg(x_checkpoint, "x_checkpoint", rows, in_features, dev))
     need = ctypes.c_int64()
-    _check("dpr_linear_weight_grad", lib().dpr_linear_weight_grad_workspace(
-        pd, sd, ref, rows, out_features, in_features, ctypes.byref(need)))
+    L = lib()
+    st = L.dpr_linear_weight_grad_workspace(pd, sd, ref, rows, out_features, in_features,
+                                            ctypes.byref(need))
+    if st:
+        _check("dpr_linear_weight_grad", st)
     nbytes = need.value
-    ws = _workspace(workspace, nbytes, stream)
-    _check("dpr_linear_weight_grad", lib().dpr_linear_weight_grad(
-        pd, sd, ref, rows, out_features, in_features, pw, sw, _DTYPES[dweight.dtype],
-        int(bool(accumulate)), 0 if ws is None else ws.data_ptr(), nbytes, _stream(stream)))
+    ws = _workspace(workspace, nbytes, stream, dev)
+    st = L.dpr_linear_weight_grad(
+        pd, sd, ref, rows, out_features, in_features, pw, sw, _code(dweight, "dweight"),
+        1 if accumulate else 0, 0 if ws is None else ws.data_ptr(), nbytes, _stream(stream))
+    if st:
+        _check("dpr_linear_weight_grad", st)
 
 
 def dpr_device_wait_failures() -> int:

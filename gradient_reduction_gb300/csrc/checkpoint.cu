@@ -34,9 +34,7 @@ __global__ void __launch_bounds__(kThreads) checkpoint_save(const __grid_constan
     Raw<T, V> raw;
     zero_raw(raw);
     if (on) load_raw(static_cast<const T*>(p.x) + row * p.stride + c, raw);
-    float f[V];
-    unpack(raw, f);
-    save_vector<V>(f, c, on, p.c.codes + row * p.c.code_stride, p.c.steps + row * p.c.step_stride);
+    save_vector(raw, c, on, p.c.codes + row * p.c.code_stride, p.c.steps + row * p.c.step_stride);
 }
 
 template <typename T, int V>
@@ -76,10 +74,10 @@ dpr_status run(void* x, int64_t stride, int64_t rows, int64_t width, int dtype,
     if ((st = check_matrix(x, stride, width, dtype, !save)) != DPR_OK) return st;
     if ((st = check_checkpoint(c, width)) != DPR_OK) return st;
     const int64_t es = dtype_size(dtype);
-    std::vector<Span> v;
-    v.push_back(span_of(x, matrix_bytes(rows, width, stride, es)));
-    add_spans(*c, rows, width, &v);
-    if (!pairwise_disjoint(v)) return DPR_ERR_ALIAS;
+    SpanList v;
+    v.add(x, matrix_bytes(rows, width, stride, es));
+    v.add(*c, rows, width);
+    if (!v.disjoint()) return DPR_ERR_ALIAS;
     // a grid's blocks are counted in 31 bits
     if (rows * round_up(width, kBlockChannels) / kThreads > (int64_t(1) << 30))
         return DPR_ERR_UNSUPPORTED;

@@ -80,21 +80,6 @@ struct Source {
     }
 };
 
-// The sums of `a` and `b` over the blockDim.x threads that share threadIdx.y.
-// `s` has 32 entries per threadIdx.y; calls in a row alternate between two of
-// them (one barrier, none behind the reads).
-__device__ __forceinline__ void row_sums(float& a, float& b, float2 (*s)[32]) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if (blockDim.x == 32) return;
-    const int lane = int(threadIdx.x) & 31, nw = int(blockDim.x) >> 5;
-    if (lane == 0) s[threadIdx.y][threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const float2 v = lane < nw ? s[threadIdx.y][lane] : make_float2(0.0f, 0.0f);
-    a = warp_sum(v.x);
-    b = warp_sum(v.y);
-}
-
 // One pass: blockDim.x threads (a multiple of 32, at most 512) share a row,
 // NV vectors of V channels each, vector i at (i * blockDim.x + threadIdx.x) *
 // V; blockDim.y rows at a time per block, the blocks' rows interleaved.
@@ -106,19 +91,29 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
     grid_wait();
     grid_release();
     const int tx = int(threadIdx.x), threads = int(blockDim.x);
-    float w[E], dw[E], db[E];
+    // element i * V + k is half (i * V + k) & 1 of pair (i * V + k) / 2
+    F2 w[E / 2], dw[E / 2], db[E / 2];
+    {
+        float f[E];
 #pragma unroll
-    for (int k = 0; k < E; ++k) { w[k] = 1.0f; dw[k] = 0.0f; db[k] = 0.0f; }
-    if (p.weight) {
+        for (int k = 0; k < E; ++k) f[k] = 1.0f;
+        if (p.weight) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * threads + tx) * V;
-            float f[V];
-            if (c < p.width) {
-                load_params<V>(p.weight, p.param_bf16, p.param_vec, c, f);
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * threads + tx) * V;
+                float v[V];
+                if (c < p.width) {
+                    load_params<V>(p.weight, p.param_bf16, p.param_vec, c, v);
 #pragma unroll
-                for (int k = 0; k < V; ++k) w[i * V + k] = f[k];
+                    for (int k = 0; k < V; ++k) f[i * V + k] = v[k];
+                }
             }
+        }
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+            w[k] = f2(f[2 * k], f[2 * k + 1]);
+            dw[k] = f2(0.0f);
+            db[k] = f2(0.0f);
         }
     }
     const int64_t stride = int64_t(gridDim.x) * blockDim.y;
@@ -146,44 +141,54 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
     int turn = 0;
     for (int64_t first = int64_t(blockIdx.x) * blockDim.y; first < p.rows;
          first += stride, row += stride, turn ^= 1) {
-        float g[E], h[E];
-        float a = 0.0f, b = 0.0f;
+        F2 g[E / 2], h[E / 2];
+        F2 sum_g = f2(0.0f), sum_gh = f2(0.0f);
         const float r = rstd;
+        {
+            float d[E], f[E];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float d[V], f[V];
-            unpack(dy[i], d);
-            x[i].get(f);
+            for (int i = 0; i < NV; ++i) {
+                float v[V];
+                unpack(dy[i], v);
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const int e = i * V + k;
+                for (int k = 0; k < V; ++k) d[i * V + k] = v[k];
+                x[i].get(v);
+#pragma unroll
+                for (int k = 0; k < V; ++k) f[i * V + k] = v[k];
+            }
+            const F2 minus_mean = f2(-mean), r2 = f2(r);
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k) {
                 // a channel past the row's end has d = 0
-                h[e] = __fmul_rn(__fsub_rn(f[k], mean), r);
-                g[e] = __fmul_rn(d[k], w[e]);
-                a = __fadd_rn(a, g[e]);
-                b = __fmaf_rn(g[e], h[e], b);
-                dw[e] = __fmaf_rn(d[k], h[e], dw[e]);
-                db[e] = __fadd_rn(db[e], d[k]);
+                const F2 dk = f2(d[2 * k], d[2 * k + 1]);
+                h[k] = mul2(add2(f2(f[2 * k], f[2 * k + 1]), minus_mean), r2);
+                g[k] = mul2(dk, w[k]);
+                sum_g = add2(sum_g, g[k]);
+                sum_gh = fma2(g[k], h[k], sum_gh);
+                dw[k] = fma2(dk, h[k], dw[k]);
+                db[k] = add2(db[k], dk);
             }
         }
         load(row + stride);
+        float a = total(sum_g), b = total(sum_gh);
         row_sums(a, b, s[turn]);
-        a = __fmul_rn(a, p.inv_width);
-        b = __fmul_rn(b, p.inv_width);
         if (row < p.rows) {
+            const F2 minus_a = f2(-__fmul_rn(a, p.inv_width)), r2 = f2(r);
+            const F2 minus_b = f2(-__fmul_rn(b, p.inv_width));
+            float d[E];
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k)
+                halves(mul2(r2, fma2(h[k], minus_b, add2(g[k], minus_a))), d[2 * k], d[2 * k + 1]);
             T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * threads + tx) * V;
                 if (c < p.width) {
-                    float d[V];
+                    float v[V];
 #pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const int e = i * V + k;
-                        d[k] = __fmul_rn(r, __fmaf_rn(-h[e], b, __fsub_rn(g[e], a)));
-                    }
+                    for (int k = 0; k < V; ++k) v[k] = d[i * V + k];
                     Raw<T, V> out;
-                    pack(d, out);
+                    pack(v, out);
                     store_raw(dx + c, out);
                 }
             }
@@ -194,39 +199,48 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
     if (blockDim.y > 1) {
         __syncthreads();
         float* mine = columns + (int(threadIdx.y) - 1) * 2 * threads * E;
+        float2* const mine2 = reinterpret_cast<float2*>(mine);
         if (threadIdx.y > 0) {
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                mine[k * threads + tx] = dw[k];
-                mine[(E + k) * threads + tx] = db[k];
+            for (int k = 0; k < E / 2; ++k) {
+                halves(dw[k], mine2[k * threads + tx].x, mine2[k * threads + tx].y);
+                float2& t = mine2[(E / 2 + k) * threads + tx];
+                halves(db[k], t.x, t.y);
             }
         }
         __syncthreads();
         if (threadIdx.y > 0) return;
         for (int y = 0; y + 1 < int(blockDim.y); ++y) {
-            const float* other = columns + y * 2 * threads * E;
+            const float2* other = reinterpret_cast<const float2*>(columns + y * 2 * threads * E);
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                dw[k] = __fadd_rn(dw[k], other[k * threads + tx]);
-                db[k] = __fadd_rn(db[k], other[(E + k) * threads + tx]);
+            for (int k = 0; k < E / 2; ++k) {
+                const float2 u = other[k * threads + tx], v = other[(E / 2 + k) * threads + tx];
+                dw[k] = add2(dw[k], f2(u.x, u.y));
+                db[k] = add2(db[k], f2(v.x, v.y));
             }
         }
     }
     float* to = p.partial + int64_t(blockIdx.x) * 2 * p.partial_width;
+    float out_w[E], out_b[E];
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+        halves(dw[k], out_w[2 * k], out_w[2 * k + 1]);
+        halves(db[k], out_b[2 * k], out_b[2 * k + 1]);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * threads + tx) * V;
         if (c < p.width) {
             if constexpr (V >= 8) {
 #pragma unroll
-                for (int k = 0; k < V; k += 4) {
-                    const int e = i * V + k;
-                    st_f4(to + c + k, dw[e], dw[e + 1], dw[e + 2], dw[e + 3]);
-                    st_f4(to + p.partial_width + c + k, db[e], db[e + 1], db[e + 2], db[e + 3]);
+                for (int k = i * V; k < i * V + V; k += 4) {
+                    float* at = to + c + k - i * V;
+                    st_f4(at, out_w[k], out_w[k + 1], out_w[k + 2], out_w[k + 3]);
+                    st_f4(at + p.partial_width, out_b[k], out_b[k + 1], out_b[k + 2], out_b[k + 3]);
                 }
             } else {
-                to[c] = dw[i];
-                to[p.partial_width + c] = db[i];
+                to[c] = out_w[i];
+                to[p.partial_width + c] = out_b[i];
             }
         }
     }
@@ -468,10 +482,10 @@ dpr_status dpr_layernorm_backward(const void* dy, int64_t dy_stride, const void*
     if (!aligned(weight, uintptr_t(ps)) || !aligned(dweight, uintptr_t(gs)) ||
         !aligned(dbias, uintptr_t(gs)))
         return DPR_ERR_ALIGNMENT;
-    std::vector<Span> outs, ins;
-    if (dweight) outs.push_back(span_of(dweight, uint64_t(width * gs)));
-    if (dbias) outs.push_back(span_of(dbias, uint64_t(width * gs)));
-    if (weight) ins.push_back(span_of(weight, uint64_t(width * ps)));
+    SpanList outs, ins;
+    if (dweight) outs.add(dweight, uint64_t(width * gs));
+    if (dbias) outs.add(dbias, uint64_t(width * gs));
+    if (weight) ins.add(weight, uint64_t(width * ps));
     if (rows > 0) {
         if ((st = check_matrix(dy, dy_stride, width, dtype, false)) != DPR_OK) return st;
         if ((st = check_matrix(dx, dx_stride, width, dtype, true)) != DPR_OK) return st;
@@ -481,23 +495,23 @@ dpr_status dpr_layernorm_backward(const void* dy, int64_t dy_stride, const void*
         if (!mean || !rstd || !workspace || workspace_bytes < need) return DPR_ERR_INVALID_ARG;
         if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(workspace, 16))
             return DPR_ERR_ALIGNMENT;
-        outs.push_back(span_of(workspace, uint64_t(need)));
-        ins.push_back(span_of(mean, uint64_t(rows) * 4));
-        ins.push_back(span_of(rstd, uint64_t(rows) * 4));
-        if (x_ckpt) add_spans(*x_ckpt, rows, width, &ins);
+        outs.add(workspace, uint64_t(need));
+        ins.add(mean, uint64_t(rows) * 4);
+        ins.add(rstd, uint64_t(rows) * 4);
+        if (x_ckpt) ins.add(*x_ckpt, rows, width);
         // dx may be dy or x itself; nothing else may overlap them
         const Span dxs = span_of(dx, matrix_bytes(rows, width, dx_stride, es));
         const Span dys = span_of(dy, matrix_bytes(rows, width, dy_stride, es));
         if (!(dx == dy && dx_stride == dy_stride) && overlaps(dxs, dys)) return DPR_ERR_ALIAS;
-        if (!pairwise_disjoint(outs) || any_overlap(outs, {dys})) return DPR_ERR_ALIAS;
+        if (outs.meets(dys)) return DPR_ERR_ALIAS;
         if (!x_ckpt) {
             const Span xs = span_of(x, matrix_bytes(rows, width, x_stride, es));
             if (!(dx == x && dx_stride == x_stride) && overlaps(dxs, xs)) return DPR_ERR_ALIAS;
-            if (any_overlap(outs, {xs})) return DPR_ERR_ALIAS;
+            if (outs.meets(xs)) return DPR_ERR_ALIAS;
         }
-        outs.push_back(dxs);
+        outs.add(dx, dxs.hi - dxs.lo);
     }
-    if (!pairwise_disjoint(outs) || any_overlap(outs, ins)) return DPR_ERR_ALIAS;
+    if (!outs.disjoint() || outs.meets(ins)) return DPR_ERR_ALIAS;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     JoinParams j = {};

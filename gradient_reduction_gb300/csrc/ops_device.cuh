@@ -12,6 +12,42 @@ namespace dpr {
 
 constexpr int kBlockChannels = 32;   // channels that share a step
 
+// --- two fp32 numbers per instruction (sm_100 and later) -----------------------
+// Each half is rounded as the single operation is.
+
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void halves(F2 p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float total(F2 p) {
+    float a, b;
+    halves(p, a, b);
+    return __fadd_rn(a, b);
+}
+
 // --- V consecutive elements of a row ----------------------------------------
 // T is uint16_t (bf16 bits) or float.  V = 16 (bf16) and V = 8 (fp32) are
 // 32-byte accesses, V = 8 (bf16) 16-byte ones, V = 1 single elements.
@@ -132,6 +168,15 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Sum over the first lanes of each aligned group of `n` (a power of two).
+__device__ __forceinline__ float group_sum(float v, int n) {
+    for (int d = n >> 1; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
+// The smallest power of two that is at least n (n = 1 .. 32).
+__device__ __forceinline__ int power_of_two(int n) { return n <= 1 ? 1 : 2 << (31 - __clz(n - 1)); }
+
 // Sum of `v` over the blockDim.x (a multiple of 32, at most 1024) threads
 // that share threadIdx.y; every one of them gets it.  `s` has one row of 32
 // floats per threadIdx.y.  Every thread of the block calls it.  Two calls in
@@ -139,20 +184,31 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ float row_sum(float v, float (*s)[32]) {
     v = warp_sum(v);
     if (blockDim.x == 32) return v;
-    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const int nw = int(blockDim.x) >> 5, n = power_of_two(nw);
+    const int lane = int(threadIdx.x) & 31, at = lane & (n - 1);
     if (lane == 0) s[threadIdx.y][threadIdx.x >> 5] = v;
     __syncthreads();
-    v = lane < nw ? s[threadIdx.y][lane] : 0.0f;
-    return warp_sum(v);
+    return group_sum(at < nw ? s[threadIdx.y][at] : 0.0f, n);
+}
+
+// The same for two sums at once.
+__device__ __forceinline__ void row_sums(float& a, float& b, float2 (*s)[32]) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if (blockDim.x == 32) return;
+    const int nw = int(blockDim.x) >> 5, n = power_of_two(nw);
+    const int lane = int(threadIdx.x) & 31, at = lane & (n - 1);
+    if (lane == 0) s[threadIdx.y][threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const float2 v = at < nw ? s[threadIdx.y][at] : make_float2(0.0f, 0.0f);
+    a = group_sum(v.x, n);
+    b = group_sum(v.y, n);
 }
 
 // --- the 8-bit format -----------------------------------------------------------
 
-// |x| as bits: integer order is magnitude order, with infinities and NaN
-// above every finite value.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
-// The step byte of a block whose largest |x| has these bits.  For a peak in
+// The step byte of a block whose largest |x| has these fp32 bits (integer
+// order is magnitude order, infinities and NaN above the rest).  For a peak in
 // [2^k, 2^(k+1)) the smallest step keeping peak / step below 127.5 is
 // 2^(k-6), or 2^(k-5) when the mantissa puts the peak at 127.5 * 2^(k-6) or
 // above; steps are kept in [2^-126, 2^121] (the byte in [1, 248]).
@@ -160,7 +216,7 @@ __device__ __forceinline__ uint32_t step_byte(uint32_t peak) {
     if (peak >= 0x7F800000u) return 255u;
     if (peak == 0) return 0u;
     int b = int((peak + 0x00010000u) >> 23) - 6;   // carries into the exponent from 127.5/128 up
-    return uint32_t(min(max(b, 1), 248));
+    return uint32_t(min(max(b, 1), 248));   // kTopByte
 }
 
 __device__ __forceinline__ float step_value(uint32_t byte) { return __uint_as_float(byte << 23); }
@@ -171,43 +227,72 @@ __device__ __forceinline__ float step_inverse(uint32_t byte) {
 }
 
 // x / step rounded to the nearest integer (ties to even), as the low byte of
-// the result.  x * inverse is exact or far below 1/2, and adding 1.5 * 2^23
-// rounds it to an integer whose two's complement is the sum's low bits.  The
-// limits bind only where the step is at its largest.
-__device__ __forceinline__ uint32_t encode(float x, float inverse) {
-    const float v = fminf(fmaxf(__fmul_rn(x, inverse), -127.0f), 127.0f);
-    return __float_as_uint(__fadd_rn(v, 12582912.0f));
-}
+// the result: x * inverse is exact or far below 1/2, and adding 1.5 * 2^23
+// rounds it (once: a fused multiply-add) to an integer whose two's complement
+// is the sum's low bits.
+constexpr float kRoundInteger = 12582912.0f;
+constexpr uint32_t kTopByte = 248;   // the largest step: codes may need limiting
 
-// The low bytes of four encode() results.
+// The low bytes of four such numbers.
 __device__ __forceinline__ uint32_t pack_codes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// The largest |x| of V elements, as fp32 bits.
+template <typename T, int V>
+__device__ __forceinline__ uint32_t peak_bits(const Raw<T, V>& r) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t peak = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) peak = max(peak, r.w[i] & 0x7FFFFFFFu);
+        return peak;
+    } else if constexpr (V == 1) {
+        return (r.w[0] & 0x7FFFu) << 16;
+    } else {
+        uint32_t peak = 0;   // two bf16 magnitudes at a time
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) peak = __vmaxu2(peak, r.w[i] & 0x7FFF7FFFu);
+        return max(peak << 16, peak & 0xFFFF0000u);
+    }
 }
 
 // Saves V channels starting at channel c (a multiple of V) of one row.  The
 // 32 / V threads of a block of channels are neighbouring lanes and all call
 // it; channels at or past `width` are zeros (`on` false: nothing stored).
 // `codes` and `steps` point at the row's start.
-template <int V>
-__device__ __forceinline__ void save_vector(const float (&x)[V], int64_t c, bool on, int8_t* codes,
+template <typename T, int V>
+__device__ __forceinline__ void save_vector(const Raw<T, V>& raw, int64_t c, bool on, int8_t* codes,
                                             uint8_t* steps) {
-    uint32_t peak = 0;
+    uint32_t peak = peak_bits(raw);
+    if constexpr (V == 1) {
+        peak = __reduce_max_sync(0xFFFFFFFFu, peak);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) peak = max(peak, abs_bits(x[i]));
-#pragma unroll
-    for (int d = 1; d < kBlockChannels / V; d <<= 1)
-        peak = max(peak, __shfl_xor_sync(0xFFFFFFFFu, peak, d));
+        for (int d = 1; d < kBlockChannels / V; d <<= 1)
+            peak = max(peak, __shfl_xor_sync(0xFFFFFFFFu, peak, d));
+    }
     const uint32_t byte = step_byte(peak);
     if (!on) return;
     const float inv = step_inverse(byte);
+    float x[V];
+    unpack(raw, x);
+    if (byte == kTopByte) {
+        const float top = __fmul_rn(127.0f, step_value(kTopByte));
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = fminf(fmaxf(x[i], -top), top);
+    }
     if constexpr (V == 1) {
-        codes[c] = byte == 255u ? int8_t(0) : int8_t(encode(x[0], inv) & 0xFFu);
+        const uint32_t q = __float_as_uint(__fmaf_rn(x[0], inv, kRoundInteger));
+        codes[c] = byte == 255u ? int8_t(0) : int8_t(q & 0xFFu);
     } else {
         uint32_t w[V / 4];
 #pragma unroll
         for (int i = 0; i < V / 4; ++i) {
-            w[i] = pack_codes(encode(x[4 * i], inv), encode(x[4 * i + 1], inv),
-                              encode(x[4 * i + 2], inv), encode(x[4 * i + 3], inv));
+            float q[4];
+            halves(fma2(f2(x[4 * i], x[4 * i + 1]), f2(inv), f2(kRoundInteger)), q[0], q[1]);
+            halves(fma2(f2(x[4 * i + 2], x[4 * i + 3]), f2(inv), f2(kRoundInteger)), q[2], q[3]);
+            w[i] = pack_codes(__float_as_uint(q[0]), __float_as_uint(q[1]), __float_as_uint(q[2]),
+                              __float_as_uint(q[3]));
             if (byte == 255u) w[i] = 0;
         }
         if constexpr (V == 16)
@@ -244,11 +329,18 @@ __device__ __forceinline__ void load_codes(const int8_t* p, CodeRaw<V>& r) {
 // low byte of 2^23's bits is the float 2^23 + 128 + code.
 template <int V>
 __device__ __forceinline__ void decode(const CodeRaw<V>& r, float step, float (&f)[V]) {
+    float q[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t u = r.w[i / 4] ^ 0x80808080u;
-        const uint32_t bits = __byte_perm(u, 0x4B000000u, 0x7650 + (i & 3));
-        f[i] = __fmul_rn(__fadd_rn(__uint_as_float(bits), -8388736.0f), step);
+        q[i] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7650 + (i & 3)));
+    }
+    if constexpr (V == 1) {
+        f[0] = __fmul_rn(__fadd_rn(q[0], -8388736.0f), step);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            halves(mul2(add2(f2(q[i], q[i + 1]), f2(-8388736.0f)), f2(step)), f[i], f[i + 1]);
     }
 }
 

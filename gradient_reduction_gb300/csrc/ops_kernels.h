@@ -3,8 +3,6 @@
 #pragma once
 
 #include <cstdint>
-#include <vector>
-
 #include <cuda_runtime.h>
 
 #include "../../include/dpr_ops.h"
@@ -18,9 +16,6 @@ cudaError_t launch_grid(const void* kernel, dim3 grid, dim3 block, size_t smem, 
                         cudaStream_t s);
 
 bool programmatic_launch_enabled();   // defined beside launch_kernel
-
-// SMs of the current device (0 and an error on failure).
-cudaError_t current_sm_count(int* sms);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -43,8 +38,34 @@ dpr_status check_matrix_size(int64_t rows, int64_t width);
 // a broadcast row).
 dpr_status check_matrix(const void* p, int64_t stride, int64_t width, int dtype, bool written);
 dpr_status check_checkpoint(const dpr_checkpoint* c, int64_t width);
-// Appends the spans of a checkpoint's codes and steps.
-void add_spans(const dpr_checkpoint& c, int64_t rows, int64_t width, std::vector<Span>* v);
+
+// The few buffers of one call, without allocating.
+struct SpanList {
+    Span v[12];
+    int n = 0;
+    void add(const void* p, uint64_t bytes) { v[n++] = span_of(p, bytes); }
+    // a checkpoint's codes and steps
+    void add(const dpr_checkpoint& c, int64_t rows, int64_t width) {
+        add(c.codes, matrix_bytes(rows, width, c.code_stride, 1));
+        add(c.steps, matrix_bytes(rows, ceil_div(width, DPR_CHECKPOINT_BLOCK), c.step_stride, 1));
+    }
+    bool meets(const Span& s) const {
+        for (int i = 0; i < n; ++i)
+            if (overlaps(v[i], s)) return true;
+        return false;
+    }
+    bool meets(const SpanList& o) const {
+        for (int i = 0; i < o.n; ++i)
+            if (meets(o.v[i])) return true;
+        return false;
+    }
+    bool disjoint() const {
+        for (int i = 0; i < n; ++i)
+            for (int j = 0; j < i; ++j)
+                if (overlaps(v[i], v[j])) return false;
+        return true;
+    }
+};
 
 // Elements per access for an activation of `dtype` whose rows are `width`
 // long: 32-byte accesses (16 bf16 or 8 fp32 elements) or 16-byte ones (8

@@ -501,6 +501,19 @@ cudaError_t encoder(EncodeTiled* fn) {
     return cudaSuccess;
 }
 
+// weight_grad_pairs' shared memory, allowed once per device.
+cudaError_t allow_shared_memory() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) & bit))) return e;
+    e = cudaFuncSetAttribute((const void*)weight_grad_pairs,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 // A [rows, width] tensor read in boxes of `box` elements by kTokens rows.
 cudaError_t encode(EncodeTiled fn, CUtensorMap* map, CUtensorMapDataType type, int64_t size,
                    const void* p, int64_t stride, int64_t rows, int64_t width, int box,
@@ -609,21 +622,20 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
     if (st != DPR_OK) return st;
     if (!dtype_ok(dtype)) return DPR_ERR_INVALID_ARG;
     if ((st = check_matrix(dweight, dweight_stride, in_features, dtype, true)) != DPR_OK) return st;
-    std::vector<Span> outs, ins;
-    outs.push_back(span_of(dweight, matrix_bytes(out_features, in_features, dweight_stride,
-                                                 dtype_size(dtype))));
+    SpanList outs, ins;
+    outs.add(dweight, matrix_bytes(out_features, in_features, dweight_stride, dtype_size(dtype)));
     if (rows > 0) {
         if ((st = check_matrix(dy, dy_stride, out_features, DPR_BF16, false)) != DPR_OK) return st;
         if ((st = check_checkpoint(x_ckpt, in_features)) != DPR_OK) return st;
         if (need > 0) {
             if (!workspace || workspace_bytes < need) return DPR_ERR_INVALID_ARG;
             if (!aligned(workspace, 16)) return DPR_ERR_ALIGNMENT;
-            outs.push_back(span_of(workspace, uint64_t(need)));
+            outs.add(workspace, uint64_t(need));
         }
-        ins.push_back(span_of(dy, matrix_bytes(rows, out_features, dy_stride, 2)));
-        add_spans(*x_ckpt, rows, in_features, &ins);
+        ins.add(dy, matrix_bytes(rows, out_features, dy_stride, 2));
+        ins.add(*x_ckpt, rows, in_features);
     }
-    if (!pairwise_disjoint(outs) || any_overlap(outs, ins)) return DPR_ERR_ALIAS;
+    if (!outs.disjoint() || outs.meets(ins)) return DPR_ERR_ALIAS;
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     WeightGradParams p = {};
@@ -679,9 +691,7 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
     if (e == cudaSuccess)
         e = encode(fn, &p.steps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.steps, x.step_stride, rows,
                    ceil_div(in_features, kBlockChannels), 16, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute((const void*)weight_grad_pairs,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e == cudaSuccess) e = allow_shared_memory();
     if (e != cudaSuccess) return record_cuda_status(e);
     void* args[] = {&p};
     // pairs without work are not launched, unless whole waves need all of them
