@@ -294,8 +294,8 @@ def dpr_linear_weight_grad(dy: torch.Tensor, x_checkpoint: Checkpoint, dweight: 
 
 
 def dpr_device_wait_failures() -> int:
-    """Waits inside the weight gradient's kernel that have run out (0 in
-    working order); waits for the device."""
+    """Waits inside the operators' kernels that have run out (0 in working
+    order); waits for the device."""
     n = ctypes.c_uint32()
     _check("dpr_device_wait_failures", lib().dpr_device_wait_failures(ctypes.byref(n)))
     return n.value

@@ -13,56 +13,79 @@ struct CkptParams {
     dpr_checkpoint c;
     int64_t rows;
     int width;
-    uint32_t per_row;       // thread slots per row, a multiple of the lanes of a block of channels
-    uint64_t slots;
 };
 
 namespace {
 
-// Slot q is V channels of row q / per_row.  A block of channels is 32 / V
-// neighbouring slots, and slots come in order of lanes, so its lanes meet in
-// one warp.
-template <typename T, int V>
+// blockDim.x threads along a row (a multiple of the lanes that hold a block
+// of channels, so that its peak is found within a warp), NV vectors of V
+// channels each per thread, blockDim.y rows per block; blockIdx.y counts
+// along the row.
+template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads) checkpoint_save(const __grid_constant__ CkptParams p) {
     grid_wait();
     grid_release();
-    const uint64_t q = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
-    const bool in = q < p.slots;
-    const int64_t row = in ? int64_t(q / p.per_row) : 0;
-    const int c = in ? int(q % p.per_row) * V : 0;
-    const bool on = in && c < p.width;
-    Raw<T, V> raw;
-    zero_raw(raw);
-    if (on) load_raw(static_cast<const T*>(p.x) + row * p.stride + c, raw);
-    save_vector(raw, c, on, p.c.codes + row * p.c.code_stride, p.c.steps + row * p.c.step_stride);
+    const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int first = int(blockIdx.y) * int(blockDim.x) * V * NV;
+    const bool live = row < p.rows;
+    const int64_t r = live ? row : 0;
+    const T* x = static_cast<const T*>(p.x) + r * p.stride + first;
+    const int width = live ? p.width - first : 0;   // may be short of this block's end
+    Raw<T, V> raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+        zero_raw(raw[i]);
+        if (c < width) load_raw(x + c, raw[i]);
+    }
+    save_row<T, V, NV>(raw, width, p.c.codes + r * p.c.code_stride + first,
+                       p.c.steps + r * p.c.step_stride + first / kBlockChannels);
 }
 
-template <typename T, int V>
+template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads) checkpoint_load(const __grid_constant__ CkptParams p) {
     grid_wait();
     grid_release();
-    const uint64_t q = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
-    if (q >= p.slots) return;
-    const int64_t row = int64_t(q / p.per_row);
-    const int c = int(q % p.per_row) * V;
-    if (c >= p.width) return;
-    CodeRaw<V> codes;
-    load_codes<V>(p.c.codes + row * p.c.code_stride + c, codes);
-    const float step = step_value(p.c.steps[row * p.c.step_stride + c / kBlockChannels]);
-    float f[V];
-    decode<V>(codes, step, f);
-    Raw<T, V> raw;
-    pack(f, raw);
-    store_raw(static_cast<T*>(p.x) + row * p.stride + c, raw);
+    const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (row >= p.rows) return;
+    const int first = int(blockIdx.y) * int(blockDim.x) * V * NV;
+    const int width = p.width - first;
+    const int8_t* from = p.c.codes + row * p.c.code_stride + first;
+    const uint8_t* steps = p.c.steps + row * p.c.step_stride + first / kBlockChannels;
+    T* x = static_cast<T*>(p.x) + row * p.stride + first;
+    CodeRaw<V> codes[NV];
+    float step[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+        if (c >= width) continue;
+        load_codes<V>(from + c, codes[i]);
+        step[i] = step_value(steps[c / kBlockChannels]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+        if (c >= width) continue;
+        float f[V];
+        decode<V>(codes[i], step[i], f);
+        Raw<T, V> raw;
+        pack(f, raw);
+        store_raw(x + c, raw);
+    }
 }
 
-template <int V>
-cudaError_t launch(CkptParams& p, const void* kernel, cudaStream_t s) {
-    p.per_row = uint32_t(round_up(ceil_div(p.width, V), kBlockChannels / V));
-    p.slots = uint64_t(p.rows) * p.per_row;
+template <typename T, int V, int NV>
+cudaError_t launch(CkptParams& p, bool save, cudaStream_t s) {
+    const void* k = save ? (const void*)checkpoint_save<T, V, NV>
+                         : (const void*)checkpoint_load<T, V, NV>;
+    const int lanes = V == 1 ? 32 : kBlockChannels / V;
+    // the fewest pieces of a row that fit a block, of even size
+    const int64_t pieces = ceil_div(p.width, int64_t(kThreads) * V * NV);
+    const RowShape f = row_shape(ceil_div(p.width, pieces), V * NV, lanes, kThreads);
     void* args[] = {&p};
-    return launch_grid(kernel, dim3(unsigned((p.slots + kThreads - 1) / kThreads)), dim3(kThreads),
-                       0, args, s);
+    return launch_grid(k, dim3(unsigned(ceil_div(p.rows, f.per_block)),
+                               unsigned(ceil_div(p.width, int64_t(f.threads) * V * NV))),
+                       dim3(f.threads, f.per_block), 0, args, s);
 }
 
 dpr_status run(void* x, int64_t stride, int64_t rows, int64_t width, int dtype,
@@ -78,9 +101,6 @@ dpr_status run(void* x, int64_t stride, int64_t rows, int64_t width, int dtype,
     v.add(x, matrix_bytes(rows, width, stride, es));
     v.add(*c, rows, width);
     if (!v.disjoint()) return DPR_ERR_ALIAS;
-    // a grid's blocks are counted in 31 bits
-    if (rows * round_up(width, kBlockChannels) / kThreads > (int64_t(1) << 30))
-        return DPR_ERR_UNSUPPORTED;
 
     CkptParams p = {};
     p.x = x; p.stride = stride; p.c = *c; p.rows = rows; p.width = int(width);
@@ -90,21 +110,9 @@ dpr_status run(void* x, int64_t stride, int64_t rows, int64_t width, int dtype,
     cudaError_t e;
     const bool bf = dtype == DPR_BF16;
     switch (vector_elems(dtype, width, a32, a16)) {
-        case 16:
-            e = launch<16>(p, save ? (const void*)checkpoint_save<uint16_t, 16>
-                                   : (const void*)checkpoint_load<uint16_t, 16>, s);
-            break;
-        case 8:
-            e = launch<8>(p, save ? (bf ? (const void*)checkpoint_save<uint16_t, 8>
-                                        : (const void*)checkpoint_save<float, 8>)
-                                  : (bf ? (const void*)checkpoint_load<uint16_t, 8>
-                                        : (const void*)checkpoint_load<float, 8>), s);
-            break;
-        default:
-            e = launch<1>(p, save ? (bf ? (const void*)checkpoint_save<uint16_t, 1>
-                                        : (const void*)checkpoint_save<float, 1>)
-                                  : (bf ? (const void*)checkpoint_load<uint16_t, 1>
-                                        : (const void*)checkpoint_load<float, 1>), s);
+        case 16: e = launch<uint16_t, 16, 1>(p, save, s); break;
+        case 8: e = bf ? launch<uint16_t, 8, 1>(p, save, s) : launch<float, 8, 1>(p, save, s); break;
+        default: e = bf ? launch<uint16_t, 1, 8>(p, save, s) : launch<float, 1, 8>(p, save, s);
     }
     return record_cuda_status(e);
 }

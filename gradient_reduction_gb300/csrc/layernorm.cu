@@ -40,205 +40,156 @@ __device__ __forceinline__ void load_affine(const NormParams& p, int c, float (&
     if (p.bias) load_params<V>(p.bias, p.param_bf16, p.param_vec, c, b);
 }
 
-// One block of up to 1024 threads (a multiple of 32) per row; each thread
-// holds NV vectors of V elements, vector i at (i * blockDim.x + threadIdx.x) *
-// V.
+// Vector accesses.  blockDim.x threads share a row (see row_sum), blockDim.y
+// rows at a time per block, the blocks' rows interleaved; each thread holds NV
+// vectors of V elements, vector i at (i * blockDim.x + threadIdx.x) * V, and
+// loads those of its next row while it works on one.
 template <typename T, int V, int NV, bool kCkpt>
-__global__ void __launch_bounds__(1024) norm_rows(const __grid_constant__ NormParams p) {
-    __shared__ float s[2][1][32];
+__global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormParams p) {
+    __shared__ float s[2][2][8][32];
     grid_wait();
     grid_release();
-    const int64_t row = blockIdx.x;
-    const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
-
-    Raw<T, V> raw[NV];
+    const int tx = int(threadIdx.x), threads = int(blockDim.x);
+    const int64_t stride = int64_t(gridDim.x) * blockDim.y;
+    int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const T* x = static_cast<const T*>(p.x) + row * p.x_stride + tx * V;
+    T* y = static_cast<T*>(p.y) + row * p.y_stride + tx * V;
+    const int64_t x_step = stride * p.x_stride, y_step = stride * p.y_stride;
+    Raw<T, V> next[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
-        zero_raw(raw[i]);
-        if (c < p.width) load_raw(x + c, raw[i]);
+        zero_raw(next[i]);
+        if (row < p.rows && (i * threads + tx) * V < p.width) load_raw(x + i * threads * V, next[i]);
     }
-    float sum = 0.0f;
+    int turn = 0;
+    // rows that share a warp take the same number of turns: their lanes work together
+    const int64_t end = threads < 32 ? p.rows + (threadIdx.y & (32 / threads - 1)) : p.rows;
+    for (; row < end; row += stride, y += y_step, turn ^= 1) {
+        const bool live = row < p.rows;
+        F2 d[NV][V / 2];
+        F2 part = f2(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            unpack2(next[i], d[i]);
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) part = add2(part, d[i][k]);
+            if (kCkpt && p.x_ckpt.codes) {
+                const int64_t r = live ? row : 0;
+                const int c = (i * threads + tx) * V;
+                save_vector(next[i], d[i], c, live && c < p.width,
+                            p.x_ckpt.codes + r * p.x_ckpt.code_stride,
+                            p.x_ckpt.steps + r * p.x_ckpt.step_stride);
+            }
+        }
+        x += x_step;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            zero_raw(next[i]);
+            if (row + stride < p.rows && (i * threads + tx) * V < p.width)
+                load_raw(x + i * threads * V, next[i]);
+        }
+        const float mean = __fmul_rn(row_sum(total(part), s[turn][0]), p.inv_width);
+        part = f2(0.0f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((i * threads + tx) * V < p.width) {
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k) {
+                    d[i][k] = add2(d[i][k], f2(-mean));
+                    part = fma2(d[i][k], d[i][k], part);
+                }
+            }
+        const float var = __fmul_rn(row_sum(total(part), s[turn][1]), p.inv_width);
+        const float rstd = inverse_sqrt(__fadd_rn(var, p.eps));
+        if (tx == 0 && live) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + tx) * V;
+            const bool on = live && c < p.width;
+            Raw<T, V> raw;
+            zero_raw(raw);
+            if (on) {
+                float w[V], b[V];
+                load_affine<V>(p, c, w, b);
+#pragma unroll
+                for (int k = 0; k < V / 2; ++k)
+                    d[i][k] = fma2(mul2(d[i][k], f2(rstd)), f2(w[2 * k], w[2 * k + 1]),
+                                   f2(b[2 * k], b[2 * k + 1]));
+                pack2(d[i], raw);
+                store_raw(y + i * threads * V, raw);
+            }
+            if (kCkpt && p.y_ckpt.codes) {
+                const int64_t r = live ? row : 0;
+                save_vector(raw, c, on, p.y_ckpt.codes + r * p.y_ckpt.code_stride,
+                            p.y_ckpt.steps + r * p.y_ckpt.step_stride);
+            }
+        }
+    }
+}
+
+// Single elements: as above, one row (or blockDim.y of them) per block, NV
+// elements a thread in registers.
+template <typename T, int NV, bool kCkpt>
+__global__ void __launch_bounds__(1024) norm_rows_any(const __grid_constant__ NormParams p) {
+    __shared__ float s[2][8][32];
+    grid_wait();
+    grid_release();
+    const int tx = int(threadIdx.x), threads = int(blockDim.x);
+    const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const bool live = row < p.rows;   // the barriers below are for the whole block
+    const int64_t r = live ? row : 0;
+    const int width = live ? p.width : 0;
+    const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
+    Raw<T, 1> raw[NV];
+    float d[NV], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float f[V];
-        unpack(raw[i], f);
+        const int c = i * threads + tx;
+        zero_raw(raw[i]);
+        if (c < width) load_raw(x + c, raw[i]);
+    }
 #pragma unroll
-        for (int k = 0; k < V; ++k) sum = __fadd_rn(sum, f[k]);
+    for (int i = 0; i < NV; ++i) {
+        float f[1];
+        unpack(raw[i], f);
+        d[i] = f[0];
+        sum = __fadd_rn(sum, d[i]);
     }
     const float mean = __fmul_rn(row_sum(sum, s[0]), p.inv_width);
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
-        if (c < p.width) {
-            float f[V];
-            unpack(raw[i], f);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float d = __fsub_rn(f[k], mean);
-                sq = __fmaf_rn(d, d, sq);
-            }
-        }
+        d[i] = i * threads + tx < width ? __fsub_rn(d[i], mean) : 0.0f;
+        sq = __fmaf_rn(d[i], d[i], sq);
     }
     const float var = __fmul_rn(row_sum(sq, s[1]), p.inv_width);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, p.eps)));
-    if (threadIdx.x == 0) {
+    const float rstd = inverse_sqrt(__fadd_rn(var, p.eps));
+    if (tx == 0 && live) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-
-    T* y = static_cast<T*>(p.y) + row * p.y_stride;
+    if (kCkpt && p.x_ckpt.codes)
+        save_row<T, 1, NV>(raw, width, p.x_ckpt.codes + r * p.x_ckpt.code_stride,
+                           p.x_ckpt.steps + r * p.x_ckpt.step_stride);
+    T* y = static_cast<T*>(p.y) + r * p.y_stride;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
-        const bool on = c < p.width;
-        float f[V], w[V], b[V];
-        unpack(raw[i], f);
-        if (kCkpt && p.x_ckpt.codes)
-            save_vector(raw[i], c, on, p.x_ckpt.codes + row * p.x_ckpt.code_stride,
-                        p.x_ckpt.steps + row * p.x_ckpt.step_stride);
-        Raw<T, V> out;
-        zero_raw(out);
-        if (on) {
-            load_affine<V>(p, c, w, b);
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-                f[k] = __fmaf_rn(__fmul_rn(__fsub_rn(f[k], mean), rstd), w[k], b[k]);
-            pack(f, out);
-            store_raw(y + c, out);
-        }
-        if (kCkpt && p.y_ckpt.codes)
-            save_vector(out, c, on, p.y_ckpt.codes + row * p.y_ckpt.code_stride,
-                        p.y_ckpt.steps + row * p.y_ckpt.step_stride);
-    }
-}
-
-// Rows of up to 512 threads x 16 channels: as norm_rows, but each block keeps
-// its channels' weight and bias in registers over many rows (the blocks' rows
-// are interleaved) and loads the next row while it works on one.
-template <typename T, int V, int NV, bool kCkpt>
-__global__ void __launch_bounds__(512) norm_many_rows(const __grid_constant__ NormParams p) {
-    constexpr int E = V * NV;
-    __shared__ float s[2][2][8][32];
-    grid_wait();
-    grid_release();
-    const int tx = int(threadIdx.x), threads = int(blockDim.x);
-    F2 w[E / 2], b[E / 2];
-    {
-        float fw[E], fb[E];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * threads + tx) * V;
-            float v[V], u[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) { v[k] = 1.0f; u[k] = 0.0f; }
-            if (c < p.width) load_affine<V>(p, c, v, u);
-#pragma unroll
-            for (int k = 0; k < V; ++k) { fw[i * V + k] = v[k]; fb[i * V + k] = u[k]; }
-        }
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k) {
-            w[k] = f2(fw[2 * k], fw[2 * k + 1]);
-            b[k] = f2(fb[2 * k], fb[2 * k + 1]);
+        const int c = i * threads + tx;
+        zero_raw(raw[i]);
+        if (c < width) {
+            float f[1], w[1], b[1];
+            load_affine<1>(p, c, w, b);
+            f[0] = __fmaf_rn(__fmul_rn(d[i], rstd), w[0], b[0]);
+            pack(f, raw[i]);
+            store_raw(y + c, raw[i]);
         }
     }
-    const int64_t stride = int64_t(gridDim.x) * blockDim.y;
-    int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-    Raw<T, V> next[NV];
-    const auto load = [&](int64_t r) {
-        const T* x = static_cast<const T*>(p.x) + r * p.x_stride;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * threads + tx) * V;
-            zero_raw(next[i]);
-            if (r < p.rows && c < p.width) load_raw(x + c, next[i]);
-        }
-    };
-    load(row);
-    int turn = 0;
-    // the same number of turns for every row of a block: the barriers are shared
-    for (int64_t first = int64_t(blockIdx.x) * blockDim.y; first < p.rows;
-         first += stride, row += stride, turn ^= 1) {
-        const bool live = row < p.rows;
-        Raw<T, V> raw[NV];
-        F2 d[E / 2];
-        F2 sum = f2(0.0f);
-        {
-            float f[E];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                raw[i] = next[i];
-                float v[V];
-                unpack(raw[i], v);
-#pragma unroll
-                for (int k = 0; k < V; ++k) f[i * V + k] = v[k];
-            }
-#pragma unroll
-            for (int k = 0; k < E / 2; ++k) {
-                d[k] = f2(f[2 * k], f[2 * k + 1]);
-                sum = add2(sum, d[k]);
-            }
-        }
-        load(row + stride);
-        if (kCkpt && p.x_ckpt.codes) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * threads + tx) * V;
-                save_vector(raw[i], c, live && c < p.width,
-                            p.x_ckpt.codes + (live ? row : 0) * p.x_ckpt.code_stride,
-                            p.x_ckpt.steps + (live ? row : 0) * p.x_ckpt.step_stride);
-            }
-        }
-        const float mean = __fmul_rn(row_sum(total(sum), s[turn][0]), p.inv_width);
-        F2 sq = f2(0.0f);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool on = (i * threads + tx) * V < p.width;
-            if constexpr (V == 1) {
-                // a pair is two vectors: the centred value of a channel past the end is 0
-                if (i & 1) {
-                    float lo, hi;
-                    halves(add2(d[i / 2], f2(-mean)), lo, hi);
-                    if (!on) hi = 0.0f;
-                    if ((i - 1) * threads + tx >= p.width) lo = 0.0f;
-                    d[i / 2] = f2(lo, hi);
-                    sq = fma2(d[i / 2], d[i / 2], sq);
-                }
-            } else if (on) {
-#pragma unroll
-                for (int k = i * V / 2; k < (i + 1) * V / 2; ++k) {
-                    d[k] = add2(d[k], f2(-mean));
-                    sq = fma2(d[k], d[k], sq);
-                }
-            }
-        }
-        const float var = __fmul_rn(row_sum(total(sq), s[turn][1]), p.inv_width);
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, p.eps)));
-        if (tx == 0 && live) {
-            if (p.mean) p.mean[row] = mean;
-            if (p.rstd) p.rstd[row] = rstd;
-        }
-        float f[E];
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k)
-            halves(fma2(mul2(d[k], f2(rstd)), w[k], b[k]), f[2 * k], f[2 * k + 1]);
-        T* y = static_cast<T*>(p.y) + (live ? row : 0) * p.y_stride;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * threads + tx) * V;
-            const bool on = live && c < p.width;
-            float v[V];
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = on ? f[i * V + k] : 0.0f;
-            Raw<T, V> out;
-            pack(v, out);
-            if (on) store_raw(y + c, out);
-            if (kCkpt && p.y_ckpt.codes)
-                save_vector(out, c, on, p.y_ckpt.codes + (live ? row : 0) * p.y_ckpt.code_stride,
-                            p.y_ckpt.steps + (live ? row : 0) * p.y_ckpt.step_stride);
-        }
-    }
+    if (kCkpt && p.y_ckpt.codes)
+        save_row<T, 1, NV>(raw, width, p.y_ckpt.codes + r * p.y_ckpt.code_stride,
+                           p.y_ckpt.steps + r * p.y_ckpt.step_stride);
 }
 
 // Rows too long for registers: one block of 1024 threads per row, which
@@ -273,7 +224,7 @@ __global__ void __launch_bounds__(1024) norm_long_rows(const __grid_constant__ N
         }
     }
     const float var = __fmul_rn(row_sum(sq, s[1]), p.inv_width);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, p.eps)));
+    const float rstd = inverse_sqrt(__fadd_rn(var, p.eps));
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -286,9 +237,11 @@ __global__ void __launch_bounds__(1024) norm_long_rows(const __grid_constant__ N
         zero_raw(raw);
         if (on) load_raw(x + c, raw);
         unpack(raw, f);
-        if (p.x_ckpt.codes)
-            save_vector(raw, c, on, p.x_ckpt.codes + row * p.x_ckpt.code_stride,
-                        p.x_ckpt.steps + row * p.x_ckpt.step_stride);
+        if (p.x_ckpt.codes) {
+            const Raw<T, V> one[1] = {raw};
+            save_row<T, V, 1>(one, p.width - c0, p.x_ckpt.codes + row * p.x_ckpt.code_stride + c0,
+                              p.x_ckpt.steps + row * p.x_ckpt.step_stride + c0 / kBlockChannels);
+        }
         zero_raw(raw);
         if (on) {
             load_affine<V>(p, c, w, b);
@@ -298,19 +251,37 @@ __global__ void __launch_bounds__(1024) norm_long_rows(const __grid_constant__ N
             pack(f, raw);
             store_raw(y + c, raw);
         }
-        if (p.y_ckpt.codes)
-            save_vector(raw, c, on, p.y_ckpt.codes + row * p.y_ckpt.code_stride,
-                        p.y_ckpt.steps + row * p.y_ckpt.step_stride);
+        if (p.y_ckpt.codes) {
+            const Raw<T, V> one[1] = {raw};
+            save_row<T, V, 1>(one, p.width - c0, p.y_ckpt.codes + row * p.y_ckpt.code_stride + c0,
+                              p.y_ckpt.steps + row * p.y_ckpt.step_stride + c0 / kBlockChannels);
+        }
     }
 }
 
+constexpr int kBlock = 128;              // threads of a block, or one row's if more
+constexpr int kBlockAny = 256;           // the same for single elements
 template <typename T, int V, int NV>
-cudaError_t launch_rows(const NormParams& p, int threads, cudaStream_t s) {
-    const bool ckpt = p.x_ckpt.codes || p.y_ckpt.codes;
-    const void* k = ckpt ? (const void*)norm_rows<T, V, NV, true>
-                         : (const void*)norm_rows<T, V, NV, false>;
+cudaError_t launch_rows(const NormParams& p, cudaStream_t s) {
+    const RowShape f = row_shape(p.width, V * NV, kBlockChannels / V, kBlock);
+    const void* k = p.x_ckpt.codes || p.y_ckpt.codes ? (const void*)norm_rows<T, V, NV, true>
+                                                     : (const void*)norm_rows<T, V, NV, false>;
+    int64_t resident = 0;
+    const cudaError_t e = resident_blocks(k, f.threads * f.per_block, &resident);
+    if (e != cudaSuccess) return e;
     void* args[] = {const_cast<NormParams*>(&p)};
-    return launch_grid(k, dim3(unsigned(p.rows)), dim3(threads), 0, args, s);
+    return launch_grid(k, dim3(unsigned(std::min(resident, ceil_div(p.rows, f.per_block)))),
+                       dim3(f.threads, f.per_block), 0, args, s);
+}
+
+template <typename T, int NV>
+cudaError_t launch_rows_any(const NormParams& p, cudaStream_t s) {
+    const RowShape f = row_shape(p.width, NV, 32, kBlockAny);
+    const void* k = p.x_ckpt.codes || p.y_ckpt.codes ? (const void*)norm_rows_any<T, NV, true>
+                                                     : (const void*)norm_rows_any<T, NV, false>;
+    void* args[] = {const_cast<NormParams*>(&p)};
+    return launch_grid(k, dim3(unsigned(ceil_div(p.rows, f.per_block))),
+                       dim3(f.threads, f.per_block), 0, args, s);
 }
 
 template <typename T, int V>
@@ -320,28 +291,28 @@ cudaError_t launch_long(const NormParams& p, cudaStream_t s) {
                        args, s);
 }
 
-// 16 channels a thread up to 512 threads a row (norm_many_rows, blocks of at
-// least 256 threads, 512 threads per SM); beyond that N1, then N2 vectors a
-// thread of 1024 (norm_rows); then rows read three times.
-constexpr int64_t kSms = 152;
-template <typename T, int V, int N1, int N2>
+// Channels per thread: 32, so that a row's sums cross few threads; 48 where
+// that lets an SM hold twice as many rows (8192 x 11008 bf16: 69 us against 89);
+// one vector while 32 would leave the GPU short of threads.
+template <typename T, int V>
 cudaError_t launch_forward(const NormParams& p, cudaStream_t s) {
-    constexpr int NV = 16 / V;
-    if (p.width <= 512 * 16) {
-        const int threads = int(round_up(ceil_div(p.width, V * NV), 32));
-        const int per_block = std::max(1, 256 / threads);
-        const int64_t resident = kSms * (512 / (threads * per_block));
-        const int64_t blocks = std::min(resident, ceil_div(p.rows, per_block));
-        const void* k = p.x_ckpt.codes || p.y_ckpt.codes ? (const void*)norm_many_rows<T, V, NV, true>
-                                                         : (const void*)norm_many_rows<T, V, NV, false>;
-        void* args[] = {const_cast<NormParams*>(&p)};
-        return launch_grid(k, dim3(unsigned(blocks)), dim3(threads, per_block), 0, args, s);
-    }
     const int64_t vecs = ceil_div(p.width, V);
-    if (vecs > 1024 * N2) return launch_long<T, V>(p, s);
-    const int nv = vecs > 1024 * N1 ? N2 : N1;
-    const int threads = int(round_up(ceil_div(vecs, nv), 32));
-    return nv == N1 ? launch_rows<T, V, N1>(p, threads, s) : launch_rows<T, V, N2>(p, threads, s);
+    if (vecs <= 512 && p.rows * p.width < (1 << 22)) return launch_rows<T, V, 1>(p, s);
+    const auto rows_per_sm = [&](int elems) {
+        return 512 / std::max(row_shape(p.width, elems, kBlockChannels / V, 1).threads, 1);
+    };
+    if (p.width > 512 * 32 || (p.width > 4096 && rows_per_sm(48) >= 2 * rows_per_sm(32))) {
+        if (p.width <= 512 * 48) return launch_rows<T, V, 48 / V>(p, s);
+        return launch_long<T, V>(p, s);
+    }
+    return launch_rows<T, V, 32 / V>(p, s);
+}
+
+template <typename T>
+cudaError_t launch_forward_any(const NormParams& p, cudaStream_t s) {
+    if (p.width <= 1024 * 8) return launch_rows_any<T, 8>(p, s);
+    if (p.width <= 1024 * 16) return launch_rows_any<T, 16>(p, s);
+    return launch_long<T, 1>(p, s);
 }
 
 }  // namespace
@@ -402,15 +373,11 @@ extern "C" dpr_status dpr_layernorm_forward(const void* x, int64_t x_stride, int
     p.param_vec = aligned(weight, 16) && aligned(bias, 16);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
+    const bool bf = dtype == DPR_BF16;
     switch (vector_elems(dtype, width, a32, a16)) {
-        case 16: e = launch_forward<uint16_t, 16, 1, 2>(p, s); break;
-        case 8:
-            e = dtype == DPR_BF16 ? launch_forward<uint16_t, 8, 2, 4>(p, s)
-                                  : launch_forward<float, 8, 2, 4>(p, s);
-            break;
-        default:
-            e = dtype == DPR_BF16 ? launch_forward<uint16_t, 1, 16, 16>(p, s)
-                                  : launch_forward<float, 1, 16, 16>(p, s);
+        case 16: e = launch_forward<uint16_t, 16>(p, s); break;
+        case 8: e = bf ? launch_forward<uint16_t, 8>(p, s) : launch_forward<float, 8>(p, s); break;
+        default: e = bf ? launch_forward_any<uint16_t>(p, s) : launch_forward_any<float>(p, s);
     }
     return record_cuda_status(e);
 }

@@ -10,6 +10,7 @@
 
 #include "ops_device.cuh"
 #include "ops_kernels.h"
+#include "tensor_core.cuh"
 
 namespace dpr {
 
@@ -32,6 +33,7 @@ struct NormGradParams {
     int partial_width;        // width rounded up to 4
     int slices;
     int64_t slice_rows;       // rows per slice (two passes)
+    int depth;                // rows of a group in flight (one pass, staged)
     float inv_width;
     int param_bf16;
     int param_vec;
@@ -51,6 +53,20 @@ struct JoinParams {
 namespace {
 
 // V elements of the row's x: the stored activation or its checkpoint.
+constexpr int kMaxDepth = 6;
+__device__ unsigned int g_wait_failures;
+
+__device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&w)[4]) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+}
+__device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&w)[2]) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+}
+__device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&w)[1]) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+}
+
 template <typename T, int V, bool kSaved>
 struct Source {
     Raw<T, V> raw;
@@ -79,6 +95,66 @@ struct Source {
         else unpack(raw, f);
     }
 };
+
+// A block's column sums, first over its rows-at-a-time through `columns`
+// ([blockDim.y - 1][2][threads * V * NV] floats of shared memory), to its
+// place among the partial sums.
+template <int V, int NV>
+__device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[V * NV / 2],
+                                              F2 (&db)[V * NV / 2], float* columns) {
+    constexpr int E = V * NV;
+    const int tx = int(threadIdx.x), threads = int(blockDim.x);
+    if (!p.partial) return;
+    // the block's rows-at-a-time, added in order by the first
+    if (blockDim.y > 1) {
+        __syncthreads();
+        float* mine = columns + (int(threadIdx.y) - 1) * 2 * threads * E;
+        float2* const mine2 = reinterpret_cast<float2*>(mine);
+        if (threadIdx.y > 0) {
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k) {
+                halves(dw[k], mine2[k * threads + tx].x, mine2[k * threads + tx].y);
+                float2& t = mine2[(E / 2 + k) * threads + tx];
+                halves(db[k], t.x, t.y);
+            }
+        }
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+        for (int y = 0; y + 1 < int(blockDim.y); ++y) {
+            const float2* other = reinterpret_cast<const float2*>(columns + y * 2 * threads * E);
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k) {
+                const float2 u = other[k * threads + tx], v = other[(E / 2 + k) * threads + tx];
+                dw[k] = add2(dw[k], f2(u.x, u.y));
+                db[k] = add2(db[k], f2(v.x, v.y));
+            }
+        }
+    }
+    float* to = p.partial + int64_t(blockIdx.x) * 2 * p.partial_width;
+    float out_w[E], out_b[E];
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+        halves(dw[k], out_w[2 * k], out_w[2 * k + 1]);
+        halves(db[k], out_b[2 * k], out_b[2 * k + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * threads + tx) * V;
+        if (c < p.width) {
+            if constexpr (V >= 4) {
+#pragma unroll
+                for (int k = i * V; k < i * V + V; k += 4) {
+                    float* at = to + c + k - i * V;
+                    st_f4(at, out_w[k], out_w[k + 1], out_w[k + 2], out_w[k + 3]);
+                    st_f4(at + p.partial_width, out_b[k], out_b[k + 1], out_b[k + 2], out_b[k + 3]);
+                }
+            } else {
+                to[c] = out_w[i];
+                to[p.partial_width + c] = out_b[i];
+            }
+        }
+    }
+}
 
 // One pass: blockDim.x threads (a multiple of 32, at most 512) share a row,
 // NV vectors of V channels each, vector i at (i * blockDim.x + threadIdx.x) *
@@ -194,56 +270,158 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
             }
         }
     }
-    if (!p.partial) return;
-    // the block's rows-at-a-time, added in order by the first
-    if (blockDim.y > 1) {
-        __syncthreads();
-        float* mine = columns + (int(threadIdx.y) - 1) * 2 * threads * E;
-        float2* const mine2 = reinterpret_cast<float2*>(mine);
-        if (threadIdx.y > 0) {
+    store_partial<V, NV>(p, dw, db, columns);
+}
+
+// As norm_grad_fused for rows of 513 channels up whose parts are 16-byte
+// aligned: one thread of each group of blockDim.x (at least 64) has its rows
+// bulk-copied into shared memory, p.depth of them ahead, so a row's loads cost
+// the threads no registers and no address arithmetic.  A thread owns 16
+// channels in 16-byte pieces, piece i at i * blockDim.x + threadIdx.x, which
+// neighbouring threads read without bank conflicts.
+template <typename T, bool kSaved>
+__global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ NormGradParams p) {
+    constexpr int V = 16 / int(sizeof(T)), NV = 16 / V, E = 16;
+    __shared__ float2 s[2][4][32];
+    __shared__ __align__(8) uint64_t bars[4][kMaxDepth];
+    extern __shared__ __align__(16) uint8_t ring[];
+    const int tx = int(threadIdx.x), threads = int(blockDim.x);
+    const uint32_t full = tc::smem_addr(bars[threadIdx.y]);
+    if (tx == 0) {
+        for (int k = 0; k < p.depth; ++k) tc::mbar_init(full + 8 * k, 1);
+        tc::mbar_init_fence();
+    }
+    __syncthreads();
+    grid_wait();
+    grid_release();
+    const uint32_t dy_bytes = uint32_t(p.width) * sizeof(T);
+    const uint32_t x_bytes = kSaved ? uint32_t(p.width) : dy_bytes;
+    const uint32_t stage = dy_bytes + x_bytes;
+    const uint32_t mine = tc::smem_addr(ring) + threadIdx.y * p.depth * stage;
+    const int64_t stride = int64_t(gridDim.x) * blockDim.y;
+    int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const auto fetch = [&](int64_t r, int k) {
+        const void* x = kSaved ? static_cast<const void*>(p.ckpt.codes + r * p.ckpt.code_stride)
+                               : static_cast<const T*>(p.x) + r * p.x_stride;
+        tc::mbar_expect(full + 8 * k, stage);
+        tc::bulk_load(mine + k * stage, static_cast<const T*>(p.dy) + r * p.dy_stride, dy_bytes,
+                      full + 8 * k);
+        tc::bulk_load(mine + k * stage + dy_bytes, x, x_bytes, full + 8 * k);
+    };
+    if (tx == 0)
+        for (int k = 0; k < p.depth; ++k)
+            if (row + k * stride < p.rows) fetch(row + k * stride, k);
+
+    F2 w[E / 2], dw[E / 2], db[E / 2];
+    {
+        float f[E];
 #pragma unroll
-            for (int k = 0; k < E / 2; ++k) {
-                halves(dw[k], mine2[k * threads + tx].x, mine2[k * threads + tx].y);
-                float2& t = mine2[(E / 2 + k) * threads + tx];
-                halves(db[k], t.x, t.y);
-            }
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + tx) * V;
+            float v[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = 1.0f;
+            if (p.weight && c < p.width) load_params<V>(p.weight, p.param_bf16, p.param_vec, c, v);
+#pragma unroll
+            for (int k = 0; k < V; ++k) f[i * V + k] = v[k];
         }
-        __syncthreads();
-        if (threadIdx.y > 0) return;
-        for (int y = 0; y + 1 < int(blockDim.y); ++y) {
-            const float2* other = reinterpret_cast<const float2*>(columns + y * 2 * threads * E);
 #pragma unroll
-            for (int k = 0; k < E / 2; ++k) {
-                const float2 u = other[k * threads + tx], v = other[(E / 2 + k) * threads + tx];
-                dw[k] = add2(dw[k], f2(u.x, u.y));
-                db[k] = add2(db[k], f2(v.x, v.y));
-            }
+        for (int k = 0; k < E / 2; ++k) {
+            w[k] = f2(f[2 * k], f[2 * k + 1]);
+            dw[k] = f2(0.0f);
+            db[k] = f2(0.0f);
         }
     }
-    float* to = p.partial + int64_t(blockIdx.x) * 2 * p.partial_width;
-    float out_w[E], out_b[E];
+    // what does not come in 16-byte rows is loaded a row ahead
+    float mean = 0.0f, rstd = 0.0f, step[NV];
+    const auto load_small = [&](int64_t r) {
+        if (r >= p.rows) return;
+        mean = p.mean[r];
+        rstd = p.rstd[r];
+        if constexpr (kSaved) {
 #pragma unroll
-    for (int k = 0; k < E / 2; ++k) {
-        halves(dw[k], out_w[2 * k], out_w[2 * k + 1]);
-        halves(db[k], out_b[2 * k], out_b[2 * k + 1]);
-    }
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * threads + tx) * V;
+                step[i] = c < p.width
+                              ? step_value(p.ckpt.steps[r * p.ckpt.step_stride + c / kBlockChannels])
+                              : 0.0f;
+            }
+        }
+    };
+    load_small(row);
+    T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
+    int k = 0, turn = 0;
+    uint32_t parity = 0, turns = 0;
+    bool ok = true;
+    for (; row < p.rows; row += stride, dx += stride * p.dx_stride, turn ^= 1, ++turns) {
+        if (ok) ok = tc::mbar_wait(full + 8 * k, parity);
+        F2 g[E / 2], h[E / 2];
+        F2 sum_g = f2(0.0f), sum_gh = f2(0.0f);
+        const F2 minus_mean = f2(-mean), r2 = f2(rstd);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * threads + tx) * V;
-        if (c < p.width) {
-            if constexpr (V >= 8) {
+        for (int i = 0; i < NV; ++i) {
+            F2 d[V / 2], x[V / 2];
+            Raw<T, V> raw;
+            zero_raw(raw);
+            const uint32_t at = mine + k * stage + uint32_t(i * threads + tx) * 16;
+            const bool on = (i * threads + tx) * V < p.width;
+            if (on) load_shared(at, raw.w);
+            unpack2(raw, d);
+            if constexpr (kSaved) {
+                CodeRaw<V> codes;
 #pragma unroll
-                for (int k = i * V; k < i * V + V; k += 4) {
-                    float* at = to + c + k - i * V;
-                    st_f4(at, out_w[k], out_w[k + 1], out_w[k + 2], out_w[k + 3]);
-                    st_f4(at + p.partial_width, out_b[k], out_b[k + 1], out_b[k + 2], out_b[k + 3]);
-                }
+                for (int j = 0; j < V / 4; ++j) codes.w[j] = 0;
+                if (on) load_shared(mine + k * stage + dy_bytes + uint32_t(i * threads + tx) * V, codes.w);
+                decode2<V>(codes, step[i], x);
             } else {
-                to[c] = out_w[i];
-                to[p.partial_width + c] = out_b[i];
+                if (on) load_shared(at + dy_bytes, raw.w);
+                unpack2(raw, x);
+            }
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                // a channel past the row's end has d = 0
+                const int e = i * V / 2 + j;
+                h[e] = mul2(add2(x[j], minus_mean), r2);
+                g[e] = mul2(d[j], w[e]);
+                sum_g = add2(sum_g, g[e]);
+                sum_gh = fma2(g[e], h[e], sum_gh);
+                dw[e] = fma2(d[j], h[e], dw[e]);
+                db[e] = add2(db[e], d[j]);
+            }
+        }
+        load_small(row + stride);
+        float a = total(sum_g), b = total(sum_gh);
+        row_sums(a, b, s[turn]);
+        // the whole group has read the stage: the next row may have it
+        if (tx == 0 && row + p.depth * stride < p.rows) fetch(row + p.depth * stride, k);
+        if (++k == p.depth) { k = 0; parity ^= 1; }
+        const F2 minus_a = f2(-__fmul_rn(a, p.inv_width)), minus_b = f2(-__fmul_rn(b, p.inv_width));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + tx) * V;
+            if (c < p.width) {
+                F2 o[V / 2];
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    const int e = i * V / 2 + j;
+                    o[j] = mul2(r2, fma2(h[e], minus_b, add2(g[e], minus_a)));
+                }
+                Raw<T, V> out;
+                pack2(o, out);
+                st_v4(dx + c, make_uint4(out.w[0], out.w[1], out.w[2], out.w[3]));
             }
         }
     }
+    if (!ok && tx == 0) {
+        // a wait ran out: count it, and let what is still in flight land first
+        atomicAdd(&g_wait_failures, 1u);
+        for (int j = 0; j < p.depth; ++j) {
+            const uint32_t uses = turns / p.depth + (uint32_t(j) < turns % p.depth);
+            if (uses > 0) tc::mbar_wait(full + 8 * j, (uses - 1) & 1);
+        }
+    }
+    __syncthreads();    // the ring is free: the blocks' sums go through it
+    store_partial<V, NV>(p, dw, db, reinterpret_cast<float*>(ring));
 }
 
 // avg(g) and avg(g * xhat) of every row: blockDim.x threads per row.
@@ -439,8 +617,33 @@ cudaError_t launch_backward(NormGradParams& p, cudaStream_t s) {
                        s);
 }
 
+// Rows in shared memory: as many ahead as leave room for all of an SM's groups.
+template <typename T, bool kSaved>
+cudaError_t launch_staged(NormGradParams& p, cudaStream_t s) {
+    constexpr int64_t kShared = 200 * 1024;
+    const FusedShape f = fused_shape(p.rows, p.width, 16, 1);
+    p.slices = int(f.blocks);
+    const int64_t stage = int64_t(p.width) * (sizeof(T) + (kSaved ? 1 : sizeof(T)));
+    const int64_t groups = std::max(1, 512 / (f.threads * f.per_block)) * f.per_block;
+    p.depth = int(std::max<int64_t>(2, std::min<int64_t>(kMaxDepth, kShared / (groups * stage))));
+    const size_t sums = size_t(f.per_block - 1) * 2 * f.threads * 16 * 4;
+    const size_t smem = std::max(size_t(f.per_block) * p.depth * stage, sums);
+    const void* k = (const void*)norm_grad_staged<T, kSaved>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(kShared));
+    if (e != cudaSuccess) return e;
+    void* args[] = {&p};
+    return launch_grid(k, dim3(unsigned(f.blocks)), dim3(f.threads, f.per_block), smem, args, s);
+}
+
 template <typename T, int V>
 cudaError_t launch_source(NormGradParams& p, cudaStream_t s) {
+    // bulk copies take whole 16-byte pieces
+    if (V > 1 && p.width > 512 && p.width <= kFusedWidth) {
+        if (!p.ckpt.codes) return launch_staged<T, false>(p, s);
+        if (p.width % 16 == 0 && rows_aligned(p.ckpt.codes, p.ckpt.code_stride, 1, 16))
+            return launch_staged<T, true>(p, s);
+    }
     return p.ckpt.codes ? launch_backward<T, V, true>(p, s) : launch_backward<T, V, false>(p, s);
 }
 
@@ -566,3 +769,7 @@ dpr_status dpr_layernorm_backward(const void* dy, int64_t dy_stride, const void*
 }
 
 }  // extern "C"
+
+cudaError_t dpr::norm_wait_failures(unsigned int* count) {
+    return cudaMemcpyFromSymbol(count, g_wait_failures, sizeof(*count));
+}

@@ -125,6 +125,22 @@ __device__ __forceinline__ void store_raw(T* p, const Raw<T, V>& r) {
     }
 }
 
+// V elements as pairs.
+template <typename T, int V>
+__device__ __forceinline__ void unpack2(const Raw<T, V>& r, F2 (&f)[V / 2]) {
+    float v[V];
+    unpack(r, v);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[i] = f2(v[2 * i], v[2 * i + 1]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void pack2(const F2 (&f)[V / 2], Raw<T, V>& r) {
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) halves(f[i], v[2 * i], v[2 * i + 1]);
+    pack(v, r);
+}
+
 // V parameter values (weight, bias), bf16 or fp32 by `is_bf16`; `vec`:
 // 16-byte accesses are allowed.
 template <int V>
@@ -168,7 +184,7 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the first lanes of each aligned group of `n` (a power of two).
+// Sum over each aligned group of `n` (a power of two) lanes.
 __device__ __forceinline__ float group_sum(float v, int n) {
     for (int d = n >> 1; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
     return v;
@@ -177,32 +193,53 @@ __device__ __forceinline__ float group_sum(float v, int n) {
 // The smallest power of two that is at least n (n = 1 .. 32).
 __device__ __forceinline__ int power_of_two(int n) { return n <= 1 ? 1 : 2 << (31 - __clz(n - 1)); }
 
-// Sum of `v` over the blockDim.x (a multiple of 32, at most 1024) threads
-// that share threadIdx.y; every one of them gets it.  `s` has one row of 32
-// floats per threadIdx.y.  Every thread of the block calls it.  Two calls in
-// a row need different `s` (one barrier, none behind the reads).
+// Barrier of the blockDim.x (a multiple of 32) threads that share threadIdx.y;
+// at most 15 of them.
+__device__ __forceinline__ void row_barrier() {
+    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+}
+
+// Sum of `v` over the blockDim.x threads that share threadIdx.y (a power of
+// two below 32, or a multiple of 32 up to 1024); every one of them gets it.
+// `s` has one row of 32 floats per threadIdx.y where that is a multiple.
+// All of them call it.  Two calls in a row need different `s` (one barrier,
+// none behind the reads).
 __device__ __forceinline__ float row_sum(float v, float (*s)[32]) {
+    if (blockDim.x < 32) return group_sum(v, int(blockDim.x));
     v = warp_sum(v);
     if (blockDim.x == 32) return v;
     const int nw = int(blockDim.x) >> 5, n = power_of_two(nw);
     const int lane = int(threadIdx.x) & 31, at = lane & (n - 1);
     if (lane == 0) s[threadIdx.y][threadIdx.x >> 5] = v;
-    __syncthreads();
+    row_barrier();
     return group_sum(at < nw ? s[threadIdx.y][at] : 0.0f, n);
 }
 
 // The same for two sums at once.
 __device__ __forceinline__ void row_sums(float& a, float& b, float2 (*s)[32]) {
+    if (blockDim.x < 32) {
+        a = group_sum(a, int(blockDim.x));
+        b = group_sum(b, int(blockDim.x));
+        return;
+    }
     a = warp_sum(a);
     b = warp_sum(b);
     if (blockDim.x == 32) return;
     const int nw = int(blockDim.x) >> 5, n = power_of_two(nw);
     const int lane = int(threadIdx.x) & 31, at = lane & (n - 1);
     if (lane == 0) s[threadIdx.y][threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
+    row_barrier();
     const float2 v = at < nw ? s[threadIdx.y][at] : make_float2(0.0f, 0.0f);
     a = group_sum(v.x, n);
     b = group_sum(v.y, n);
+}
+
+// 1 / sqrt(v) for v >= 0, within one unit in the last place or so: the
+// hardware's approximation and one Newton step.  (0 gives infinity.)
+__device__ __forceinline__ float inverse_sqrt(float v) {
+    const float r = rsqrtf(v);
+    const float better = __fmul_rn(r, __fmaf_rn(__fmul_rn(-0.5f, v), __fmul_rn(r, r), 1.5f));
+    return v > 1e-30f && v < 1e30f ? better : r;
 }
 
 // --- the 8-bit format -----------------------------------------------------------
@@ -256,51 +293,100 @@ __device__ __forceinline__ uint32_t peak_bits(const Raw<T, V>& r) {
     }
 }
 
-// Saves V channels starting at channel c (a multiple of V) of one row.  The
-// 32 / V threads of a block of channels are neighbouring lanes and all call
-// it; channels at or past `width` are zeros (`on` false: nothing stored).
-// `codes` and `steps` point at the row's start.
+// The code of x in a block with a step byte of kTopByte (limited to 127) or
+// 255 (0), in the low byte.
+__device__ __forceinline__ uint32_t encode_limited(float x, uint32_t byte) {
+    const float top = __fmul_rn(127.0f, step_value(kTopByte));
+    const float v = fminf(fmaxf(x, -top), top);
+    const uint32_t q = __float_as_uint(__fmaf_rn(v, step_inverse(kTopByte), kRoundInteger));
+    return byte == 255u ? 0u : q & 0xFFu;
+}
+
+// The code of one element in a block with this step byte, in the low byte.
+template <typename T>
+__device__ __forceinline__ uint32_t encode_one(const Raw<T, 1>& r, uint32_t byte) {
+    float x[1];
+    unpack(r, x);
+    if (byte >= kTopByte) return encode_limited(x[0], byte);
+    return __float_as_uint(__fmaf_rn(x[0], step_inverse(byte), kRoundInteger)) & 0xFFu;
+}
+
+// Saves V channels starting at channel c (a multiple of V) of one row, given
+// as stored and as pairs.  The 32 / V threads of a block of channels are
+// neighbouring lanes and all call it; channels at or past the row's end are
+// zeros (`on` false: nothing stored).  `codes` and `steps` point at the row's
+// start.
 template <typename T, int V>
-__device__ __forceinline__ void save_vector(const Raw<T, V>& raw, int64_t c, bool on, int8_t* codes,
-                                            uint8_t* steps) {
+__device__ __forceinline__ void save_vector(const Raw<T, V>& raw, const F2 (&f)[V / 2], int c,
+                                            bool on, int8_t* codes, uint8_t* steps) {
     uint32_t peak = peak_bits(raw);
-    if constexpr (V == 1) {
-        peak = __reduce_max_sync(0xFFFFFFFFu, peak);
-    } else {
 #pragma unroll
-        for (int d = 1; d < kBlockChannels / V; d <<= 1)
-            peak = max(peak, __shfl_xor_sync(0xFFFFFFFFu, peak, d));
-    }
+    for (int d = 1; d < kBlockChannels / V; d <<= 1)
+        peak = max(peak, __shfl_xor_sync(0xFFFFFFFFu, peak, d));
     const uint32_t byte = step_byte(peak);
     if (!on) return;
-    const float inv = step_inverse(byte);
-    float x[V];
-    unpack(raw, x);
-    if (byte == kTopByte) {
-        const float top = __fmul_rn(127.0f, step_value(kTopByte));
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = fminf(fmaxf(x[i], -top), top);
-    }
-    if constexpr (V == 1) {
-        const uint32_t q = __float_as_uint(__fmaf_rn(x[0], inv, kRoundInteger));
-        codes[c] = byte == 255u ? int8_t(0) : int8_t(q & 0xFFu);
-    } else {
-        uint32_t w[V / 4];
+    uint32_t w[V / 4];
+    if (byte < kTopByte) {
+        const F2 inv = f2(step_inverse(byte)), round = f2(kRoundInteger);
 #pragma unroll
         for (int i = 0; i < V / 4; ++i) {
             float q[4];
-            halves(fma2(f2(x[4 * i], x[4 * i + 1]), f2(inv), f2(kRoundInteger)), q[0], q[1]);
-            halves(fma2(f2(x[4 * i + 2], x[4 * i + 3]), f2(inv), f2(kRoundInteger)), q[2], q[3]);
+            halves(fma2(f[2 * i], inv, round), q[0], q[1]);
+            halves(fma2(f[2 * i + 1], inv, round), q[2], q[3]);
             w[i] = pack_codes(__float_as_uint(q[0]), __float_as_uint(q[1]), __float_as_uint(q[2]),
                               __float_as_uint(q[3]));
-            if (byte == 255u) w[i] = 0;
         }
-        if constexpr (V == 16)
-            st_v4(codes + c, make_uint4(w[0], w[1], w[2], w[3]));
-        else
-            *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+    } else {   // numbers near the type's largest, or not finite
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            float x[4];
+            halves(f[2 * i], x[0], x[1]);
+            halves(f[2 * i + 1], x[2], x[3]);
+            w[i] = pack_codes(encode_limited(x[0], byte), encode_limited(x[1], byte),
+                              encode_limited(x[2], byte), encode_limited(x[3], byte));
+        }
     }
+    if constexpr (V == 16)
+        st_v4(codes + c, make_uint4(w[0], w[1], w[2], w[3]));
+    else
+        *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
     if ((c & (kBlockChannels - 1)) == 0) steps[c / kBlockChannels] = uint8_t(byte);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void save_vector(const Raw<T, V>& raw, int c, bool on, int8_t* codes,
+                                            uint8_t* steps) {
+    F2 f[V / 2];
+    unpack2(raw, f);
+    save_vector(raw, f, c, on, codes, steps);
+}
+
+// Saves a thread's NV vectors of a row, vector i at (i * blockDim.x +
+// threadIdx.x) * V; nothing from `width` on.  Every thread calls it.
+template <typename T, int V, int NV>
+__device__ __forceinline__ void save_row(const Raw<T, V> (&raw)[NV], int width, int8_t* codes,
+                                         uint8_t* steps) {
+    const int tx = int(threadIdx.x), threads = int(blockDim.x);
+    if constexpr (V == 1) {
+        // a warp's 32 lanes are a block of channels: all peaks first, for their latencies
+        uint32_t byte[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            byte[i] = step_byte(__reduce_max_sync(0xFFFFFFFFu, peak_bits(raw[i])));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = i * threads + tx;
+            const uint32_t q = encode_one(raw[i], byte[i]);
+            if (c < width) codes[c] = int8_t(q);
+            if (c < width && (tx & 31) == 0) steps[c / kBlockChannels] = uint8_t(byte[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * threads + tx) * V;
+            save_vector(raw[i], c, c < width, codes, steps);
+        }
+    }
 }
 
 // V codes of a row.
@@ -328,19 +414,25 @@ __device__ __forceinline__ void load_codes(const int8_t* p, CodeRaw<V>& r) {
 // code * step: flipping the code's sign bit gives code + 128, which as the
 // low byte of 2^23's bits is the float 2^23 + 128 + code.
 template <int V>
-__device__ __forceinline__ void decode(const CodeRaw<V>& r, float step, float (&f)[V]) {
+__device__ __forceinline__ void decode2(const CodeRaw<V>& r, float step, F2 (&f)[V / 2]) {
     float q[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const uint32_t u = r.w[i / 4] ^ 0x80808080u;
-        q[i] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7650 + (i & 3)));
-    }
-    if constexpr (V == 1) {
-        f[0] = __fmul_rn(__fadd_rn(q[0], -8388736.0f), step);
-    } else {
+    for (int i = 0; i < V; ++i)
+        q[i] = __uint_as_float(__byte_perm(r.w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7650 + (i & 3)));
 #pragma unroll
-        for (int i = 0; i < V; i += 2)
-            halves(mul2(add2(f2(q[i], q[i + 1]), f2(-8388736.0f)), f2(step)), f[i], f[i + 1]);
+    for (int i = 0; i < V / 2; ++i)
+        f[i] = mul2(add2(f2(q[2 * i], q[2 * i + 1]), f2(-8388736.0f)), f2(step));
+}
+template <int V>
+__device__ __forceinline__ void decode(const CodeRaw<V>& r, float step, float (&f)[V]) {
+    if constexpr (V == 1) {
+        const uint32_t bits = __byte_perm(r.w[0] ^ 0x80u, 0x4B000000u, 0x7650);
+        f[0] = __fmul_rn(__fadd_rn(__uint_as_float(bits), -8388736.0f), step);
+    } else {
+        F2 p[V / 2];
+        decode2<V>(r, step, p);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) halves(p[i], f[2 * i], f[2 * i + 1]);
     }
 }
 

@@ -1,4 +1,8 @@
 // Launch and argument checks shared by the backward-pass operators.
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "ops_kernels.h"
 
 namespace dpr {
@@ -17,6 +21,27 @@ cudaError_t launch_grid(const void* kernel, dim3 grid, dim3 block, size_t smem, 
     cfg.attrs = attr;
     cfg.numAttrs = (!legacy && programmatic_launch_enabled()) ? 1 : 0;
     return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+cudaError_t resident_blocks(const void* kernel, int threads, int64_t* blocks) {
+    static std::mutex mu;
+    static std::map<std::tuple<const void*, int, int>, int64_t> cache;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_tuple(kernel, threads, dev);
+    auto it = cache.find(key);
+    if (it == cache.end()) {
+        int sms = 0, per_sm = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+        if (e != cudaSuccess) return e;
+        it = cache.emplace(key, int64_t(sms) * (per_sm < 1 ? 1 : per_sm)).first;
+    }
+    *blocks = it->second;
+    return cudaSuccess;
 }
 
 dpr_status check_matrix_size(int64_t rows, int64_t width) {

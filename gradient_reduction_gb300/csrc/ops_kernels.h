@@ -17,6 +17,9 @@ cudaError_t launch_grid(const void* kernel, dim3 grid, dim3 block, size_t smem, 
 
 bool programmatic_launch_enabled();   // defined beside launch_kernel
 
+// Waits that have run out in the layer norm's backward kernels.
+cudaError_t norm_wait_failures(unsigned int* count);
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
@@ -66,6 +69,25 @@ struct SpanList {
         return true;
     }
 };
+
+// Blocks of `threads` threads (no dynamic shared memory) that are resident on
+// the current device at once; remembered per kernel and size.
+cudaError_t resident_blocks(const void* kernel, int threads, int64_t* blocks);
+
+// Threads that share a row of `width` channels at `elems` per thread, and rows
+// per block of at least `block` threads: a power of two below 32 (at least
+// `least`, the lanes that hold a block of channels), else a multiple of 32.
+struct RowShape {
+    int threads, per_block;
+};
+inline RowShape row_shape(int64_t width, int elems, int least, int block) {
+    const int64_t need = ceil_div(width, elems);
+    int threads = 1;
+    if (need > 16 || least > 16) threads = int(round_up(need, 32));
+    else
+        while (threads < need || threads < least) threads *= 2;
+    return RowShape{threads, threads >= block ? 1 : block / threads};
+}
 
 // Elements per access for an activation of `dtype` whose rows are `width`
 // long: 32-byte accesses (16 bf16 or 8 fp32 elements) or 16-byte ones (8

@@ -1,5 +1,5 @@
-// PTX of the Blackwell tensor-core path: mbarriers with bounded waits, TMA
-// tile loads, tcgen05 matrix instructions over a pair of CTAs (cta_group::2)
+// PTX of asynchronous loads and of the Blackwell tensor-core path: mbarriers
+// with bounded waits, TMA tile loads and bulk copies, tcgen05 matrix instructions over a pair of CTAs (cta_group::2)
 // with their accumulators in tensor memory.
 #pragma once
 
@@ -101,6 +101,15 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Bulk copy of `bytes` (a multiple of 16) from a 16-byte aligned address.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
 

@@ -711,9 +711,10 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
 
 dpr_status dpr_device_wait_failures(uint32_t* count) {
     if (!count) return DPR_ERR_INVALID_ARG;
-    unsigned int v = 0;
-    const cudaError_t e = cudaMemcpyFromSymbol(&v, g_wait_failures, sizeof(v));
-    *count = v;
+    unsigned int v = 0, w = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_wait_failures, sizeof(v));
+    if (e == cudaSuccess) e = norm_wait_failures(&w);
+    *count = v + w;
     return record_cuda_status(e);
 }
 

@@ -129,8 +129,8 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
- * How many waits inside the weight gradient's kernel have run out on the
- * current device since the library was loaded (each is bounded; 0 unless the
+ * How many waits inside these operators' kernels have run out on the current
+ * device since the library was loaded (each is bounded; 0 unless the
  * hardware or the library is broken: such a call's result is incomplete).
  * Waits for the device's work.
  */
