@@ -273,16 +273,41 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
     store_partial<V, NV>(p, dw, db, columns);
 }
 
+// Four sums over the blockDim.x threads (64 to 512) that share threadIdx.y;
+// lane l of a warp ends up with sum l / 8 of the warp after six exchanges, and
+// all four come back after one barrier.  `s` as for row_sums.
+__device__ __forceinline__ void row_sums4(float (&v)[4], float (*s)[16][4]) {
+    const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5, nw = int(blockDim.x) >> 5;
+    const bool upper = lane & 16, odd = lane & 8;
+    const float k0 = __fadd_rn(upper ? v[2] : v[0],
+                               __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[2], 16));
+    const float k1 = __fadd_rn(upper ? v[3] : v[1],
+                               __shfl_xor_sync(0xFFFFFFFFu, upper ? v[1] : v[3], 16));
+    float t = __fadd_rn(odd ? k1 : k0, __shfl_xor_sync(0xFFFFFFFFu, odd ? k0 : k1, 8));
+    t = group_sum8(t);
+    if ((lane & 7) == 0) s[threadIdx.y][warp][lane >> 3] = t;
+    row_barrier();
+    const int w = lane & 7;
+    t = w < nw ? s[threadIdx.y][w][lane >> 3] : 0.0f;
+    if (nw > 8) t = __fadd_rn(t, w + 8 < nw ? s[threadIdx.y][w + 8][lane >> 3] : 0.0f);
+    t = group_sum8(t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, t, 8 * i);
+}
+
 // As norm_grad_fused for rows of 513 channels up whose parts are 16-byte
-// aligned: one thread of each group of blockDim.x (at least 64) has its rows
-// bulk-copied into shared memory, p.depth of them ahead, so a row's loads cost
-// the threads no registers and no address arithmetic.  A thread owns 16
-// channels in 16-byte pieces, piece i at i * blockDim.x + threadIdx.x, which
-// neighbouring threads read without bank conflicts.
+// aligned.  One thread of each group of blockDim.x (at least 64) has its rows
+// bulk-copied into shared memory, p.depth of them in all, so a row's loads
+// cost the threads no registers and no address arithmetic.  The group takes
+// two rows a turn: their sums share one barrier and most exchanges, and their
+// chains of dependent instructions overlap.  Rows are read from shared memory
+// twice, for the sums and for the rest, which leaves the registers to the
+// column sums.  A thread owns 16 channels in 16-byte pieces, piece i at
+// i * blockDim.x + threadIdx.x, which neighbours read without bank conflicts.
 template <typename T, bool kSaved>
 __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ NormGradParams p) {
     constexpr int V = 16 / int(sizeof(T)), NV = 16 / V, E = 16;
-    __shared__ float2 s[2][4][32];
+    __shared__ float s[2][4][16][4];
     __shared__ __align__(8) uint64_t bars[4][kMaxDepth];
     extern __shared__ __align__(16) uint8_t ring[];
     const int tx = int(threadIdx.x), threads = int(blockDim.x);
@@ -299,18 +324,23 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
     const uint32_t stage = dy_bytes + x_bytes;
     const uint32_t mine = tc::smem_addr(ring) + threadIdx.y * p.depth * stage;
     const int64_t stride = int64_t(gridDim.x) * blockDim.y;
-    int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-    const auto fetch = [&](int64_t r, int k) {
+    const int64_t row0 = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const auto fetch = [&](int64_t r, uint32_t k) {
         const void* x = kSaved ? static_cast<const void*>(p.ckpt.codes + r * p.ckpt.code_stride)
                                : static_cast<const T*>(p.x) + r * p.x_stride;
         tc::mbar_expect(full + 8 * k, stage);
         tc::bulk_load(mine + k * stage, static_cast<const T*>(p.dy) + r * p.dy_stride, dy_bytes,
                       full + 8 * k);
         tc::bulk_load(mine + k * stage + dy_bytes, x, x_bytes, full + 8 * k);
+        // a row's step bytes are a DRAM access of their own: asked for as early
+        if constexpr (kSaved)
+            for (int at = 0; at * kBlockChannels < p.width; at += 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.ckpt.steps +
+                                                              r * p.ckpt.step_stride + at));
     };
+    int64_t asked = row0;               // the next row to be fetched, by the first thread
     if (tx == 0)
-        for (int k = 0; k < p.depth; ++k)
-            if (row + k * stride < p.rows) fetch(row + k * stride, k);
+        for (int k = 0; k < p.depth && asked < p.rows; ++k, asked += stride) fetch(asked, k);
 
     F2 w[E / 2], dw[E / 2], db[E / 2];
     {
@@ -332,85 +362,123 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
             db[k] = f2(0.0f);
         }
     }
-    // what does not come in 16-byte rows is loaded a row ahead
-    float mean = 0.0f, rstd = 0.0f, step[NV];
-    const auto load_small = [&](int64_t r) {
+    // what does not come in 16-byte rows is loaded a turn ahead
+    struct Small {
+        float mean, rstd, step[NV];
+    };
+    Small now[2], next[2];
+    const uint8_t* steps = kSaved ? p.ckpt.steps + row0 * p.ckpt.step_stride + tx * V / kBlockChannels
+                                  : nullptr;
+    const int64_t step_turn = 2 * stride * p.ckpt.step_stride;
+    const auto load_small = [&](int64_t r, int j, Small& m) {   // steps: of row r - j * stride
         if (r >= p.rows) return;
-        mean = p.mean[r];
-        rstd = p.rstd[r];
+        m.mean = p.mean[r];
+        m.rstd = p.rstd[r];
         if constexpr (kSaved) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * threads + tx) * V;
-                step[i] = c < p.width
-                              ? step_value(p.ckpt.steps[r * p.ckpt.step_stride + c / kBlockChannels])
-                              : 0.0f;
-            }
+            for (int i = 0; i < NV; ++i)
+                if ((i * threads + tx) * V < p.width)
+                    m.step[i] = step_value(
+                        steps[j * stride * p.ckpt.step_stride + i * threads * V / kBlockChannels]);
         }
     };
-    load_small(row);
-    T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
-    int k = 0, turn = 0;
-    uint32_t parity = 0, turns = 0;
-    bool ok = true;
-    for (; row < p.rows; row += stride, dx += stride * p.dx_stride, turn ^= 1, ++turns) {
-        if (ok) ok = tc::mbar_wait(full + 8 * k, parity);
-        F2 g[E / 2], h[E / 2];
-        F2 sum_g = f2(0.0f), sum_gh = f2(0.0f);
-        const F2 minus_mean = f2(-mean), r2 = f2(rstd);
+    // a piece's dy and xhat from the stage at `at`
+    const auto read = [&](uint32_t at, int i, const Small& m, F2 (&d)[V / 2], F2 (&h)[V / 2]) {
+        Raw<T, V> raw;
+        const uint32_t piece = uint32_t(i * threads + tx);
+        load_shared(at + piece * 16, raw.w);
+        unpack2(raw, d);
+        const F2 minus_mean = f2(-m.mean), r2 = f2(m.rstd);
+        if constexpr (kSaved) {
+            CodeRaw<V> codes;
+            load_shared(at + dy_bytes + piece * V, codes.w);
+            codes2<V>(codes, h);
+            // code * step is exact: one rounding, as subtracting from it
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            F2 d[V / 2], x[V / 2];
-            Raw<T, V> raw;
-            zero_raw(raw);
-            const uint32_t at = mine + k * stage + uint32_t(i * threads + tx) * 16;
-            const bool on = (i * threads + tx) * V < p.width;
-            if (on) load_shared(at, raw.w);
-            unpack2(raw, d);
-            if constexpr (kSaved) {
-                CodeRaw<V> codes;
+            for (int j = 0; j < V / 2; ++j) h[j] = mul2(fma2(h[j], f2(m.step[i]), minus_mean), r2);
+        } else {
+            load_shared(at + dy_bytes + piece * 16, raw.w);
+            unpack2(raw, h);
 #pragma unroll
-                for (int j = 0; j < V / 4; ++j) codes.w[j] = 0;
-                if (on) load_shared(mine + k * stage + dy_bytes + uint32_t(i * threads + tx) * V, codes.w);
-                decode2<V>(codes, step[i], x);
-            } else {
-                if (on) load_shared(at + dy_bytes, raw.w);
-                unpack2(raw, x);
-            }
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-                // a channel past the row's end has d = 0
-                const int e = i * V / 2 + j;
-                h[e] = mul2(add2(x[j], minus_mean), r2);
-                g[e] = mul2(d[j], w[e]);
-                sum_g = add2(sum_g, g[e]);
-                sum_gh = fma2(g[e], h[e], sum_gh);
-                dw[e] = fma2(d[j], h[e], dw[e]);
-                db[e] = add2(db[e], d[j]);
-            }
+            for (int j = 0; j < V / 2; ++j) h[j] = mul2(add2(h[j], minus_mean), r2);
         }
-        load_small(row + stride);
-        float a = total(sum_g), b = total(sum_gh);
-        row_sums(a, b, s[turn]);
-        // the whole group has read the stage: the next row may have it
-        if (tx == 0 && row + p.depth * stride < p.rows) fetch(row + p.depth * stride, k);
-        if (++k == p.depth) { k = 0; parity ^= 1; }
-        const F2 minus_a = f2(-__fmul_rn(a, p.inv_width)), minus_b = f2(-__fmul_rn(b, p.inv_width));
+    };
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * threads + tx) * V;
-            if (c < p.width) {
-                F2 o[V / 2];
+    for (int j = 0; j < 2; ++j) load_small(row0 + j * stride, j, now[j]);
+    T* dx = static_cast<T*>(p.dx) + row0 * p.dx_stride + tx * V;
+    const int64_t dx_row = stride * p.dx_stride;
+    uint32_t k = 0, parity = 0, turns = 0, last = 0;    // `last`: the first stage of the turn before
+    int turn = 0;
+    bool ok = true;
+    for (int64_t row = row0; row < p.rows; row += 2 * stride, dx += 2 * dx_row, turn ^= 1) {
+        uint32_t at[2];
+        float sums[4];
+        const uint32_t first = k;
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    const int e = i * V / 2 + j;
-                    o[j] = mul2(r2, fma2(h[e], minus_b, add2(g[e], minus_a)));
+        for (int j = 0; j < 2; ++j) {
+            F2 sum_g = f2(0.0f), sum_gh = f2(0.0f);
+            at[j] = mine + k * stage;
+            if (row + j * stride < p.rows) {
+                if (ok) ok = tc::mbar_wait(full + 8 * k, parity);
+                if (++k == uint32_t(p.depth)) { k = 0; parity ^= 1; }
+                ++turns;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    if ((i * threads + tx) * V >= p.width) continue;
+                    F2 d[V / 2], h[V / 2];
+                    read(at[j], i, now[j], d, h);
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) {
+                        const F2 g = mul2(d[e], w[i * V / 2 + e]);
+                        sum_g = add2(sum_g, g);
+                        sum_gh = fma2(g, h[e], sum_gh);
+                    }
+                }
+            }
+            sums[2 * j] = total(sum_g);
+            sums[2 * j + 1] = total(sum_gh);
+        }
+        if constexpr (kSaved) steps += step_turn;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) load_small(row + (2 + j) * stride, j, next[j]);
+        row_sums4(sums, s[turn]);
+        // the whole group is past the turn before: its two stages are free
+        if (tx == 0 && row != row0) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (asked < p.rows) {
+                    fetch(asked, last);
+                    asked += stride;
+                    if (++last == uint32_t(p.depth)) last = 0;
+                }
+        }
+        last = first;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (row + j * stride >= p.rows) break;
+            const F2 minus_a = f2(-__fmul_rn(sums[2 * j], p.inv_width));
+            const F2 minus_b = f2(-__fmul_rn(sums[2 * j + 1], p.inv_width));
+            const F2 r2 = f2(now[j].rstd);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if ((i * threads + tx) * V >= p.width) continue;
+                F2 d[V / 2], h[V / 2];
+                read(at[j], i, now[j], d, h);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) {
+                    const int q = i * V / 2 + e;
+                    dw[q] = fma2(d[e], h[e], dw[q]);
+                    db[q] = add2(db[q], d[e]);
+                    d[e] = mul2(r2, fma2(h[e], minus_b, fma2(d[e], w[q], minus_a)));
                 }
                 Raw<T, V> out;
-                pack2(o, out);
-                st_v4(dx + c, make_uint4(out.w[0], out.w[1], out.w[2], out.w[3]));
+                pack2(d, out);
+                st_v4(dx + j * dx_row + i * threads * V,
+                      make_uint4(out.w[0], out.w[1], out.w[2], out.w[3]));
             }
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) now[j] = next[j];
     }
     if (!ok && tx == 0) {
         // a wait ran out: count it, and let what is still in flight land first
@@ -617,32 +685,40 @@ cudaError_t launch_backward(NormGradParams& p, cudaStream_t s) {
                        s);
 }
 
-// Rows in shared memory: as many ahead as leave room for all of an SM's groups.
+// Rows of a group in shared memory, with all of an SM's groups in 200 KB; two
+// turns' worth (4) at least, or the staged kernel is not for this width.
+constexpr int64_t kShared = 200 * 1024;
+int staged_depth(int64_t width, int64_t row_bytes) {
+    const FusedShape f = fused_shape(1 << 20, width, 16, 1);
+    const int64_t groups = 512 / (f.threads * f.per_block) * f.per_block;
+    return int(std::min<int64_t>(kMaxDepth, kShared / (groups * row_bytes)));
+}
+
 template <typename T, bool kSaved>
-cudaError_t launch_staged(NormGradParams& p, cudaStream_t s) {
-    constexpr int64_t kShared = 200 * 1024;
+cudaError_t launch_staged(NormGradParams& p, int depth, cudaStream_t s) {
     const FusedShape f = fused_shape(p.rows, p.width, 16, 1);
     p.slices = int(f.blocks);
-    const int64_t stage = int64_t(p.width) * (sizeof(T) + (kSaved ? 1 : sizeof(T)));
-    const int64_t groups = std::max(1, 512 / (f.threads * f.per_block)) * f.per_block;
-    p.depth = int(std::max<int64_t>(2, std::min<int64_t>(kMaxDepth, kShared / (groups * stage))));
+    p.depth = depth;
     const size_t sums = size_t(f.per_block - 1) * 2 * f.threads * 16 * 4;
-    const size_t smem = std::max(size_t(f.per_block) * p.depth * stage, sums);
+    const size_t rows = size_t(f.per_block) * depth * p.width * (sizeof(T) + (kSaved ? 1 : sizeof(T)));
     const void* k = (const void*)norm_grad_staged<T, kSaved>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                int(kShared));
     if (e != cudaSuccess) return e;
     void* args[] = {&p};
-    return launch_grid(k, dim3(unsigned(f.blocks)), dim3(f.threads, f.per_block), smem, args, s);
+    return launch_grid(k, dim3(unsigned(f.blocks)), dim3(f.threads, f.per_block),
+                       std::max(rows, sums), args, s);
 }
 
 template <typename T, int V>
 cudaError_t launch_source(NormGradParams& p, cudaStream_t s) {
     // bulk copies take whole 16-byte pieces
     if (V > 1 && p.width > 512 && p.width <= kFusedWidth) {
-        if (!p.ckpt.codes) return launch_staged<T, false>(p, s);
-        if (p.width % 16 == 0 && rows_aligned(p.ckpt.codes, p.ckpt.code_stride, 1, 16))
-            return launch_staged<T, true>(p, s);
+        const bool saved = p.ckpt.codes != nullptr;
+        const int depth = staged_depth(p.width, p.width * int64_t(sizeof(T) + (saved ? 1 : sizeof(T))));
+        if (depth >= 4 && !saved) return launch_staged<T, false>(p, depth, s);
+        if (depth >= 4 && p.width % 16 == 0 && rows_aligned(p.ckpt.codes, p.ckpt.code_stride, 1, 16))
+            return launch_staged<T, true>(p, depth, s);
     }
     return p.ckpt.codes ? launch_backward<T, V, true>(p, s) : launch_backward<T, V, false>(p, s);
 }

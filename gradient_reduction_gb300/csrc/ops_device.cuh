@@ -190,13 +190,20 @@ __device__ __forceinline__ float group_sum(float v, int n) {
     return v;
 }
 
+__device__ __forceinline__ float group_sum8(float v) {
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
 // The smallest power of two that is at least n (n = 1 .. 32).
 __device__ __forceinline__ int power_of_two(int n) { return n <= 1 ? 1 : 2 << (31 - __clz(n - 1)); }
 
 // Barrier of the blockDim.x (a multiple of 32) threads that share threadIdx.y;
 // at most 15 of them.
 __device__ __forceinline__ void row_barrier() {
-    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+    if (blockDim.y == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
 }
 
 // Sum of `v` over the blockDim.x threads that share threadIdx.y (a power of
@@ -411,17 +418,23 @@ __device__ __forceinline__ void load_codes(const int8_t* p, CodeRaw<V>& r) {
     }
 }
 
-// code * step: flipping the code's sign bit gives code + 128, which as the
-// low byte of 2^23's bits is the float 2^23 + 128 + code.
+// The codes as fp32 pairs: flipping a code's sign bit gives code + 128, which
+// as the low byte of 2^23's bits is the float 2^23 + 128 + code.
 template <int V>
-__device__ __forceinline__ void decode2(const CodeRaw<V>& r, float step, F2 (&f)[V / 2]) {
+__device__ __forceinline__ void codes2(const CodeRaw<V>& r, F2 (&f)[V / 2]) {
     float q[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
         q[i] = __uint_as_float(__byte_perm(r.w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7650 + (i & 3)));
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i)
-        f[i] = mul2(add2(f2(q[2 * i], q[2 * i + 1]), f2(-8388736.0f)), f2(step));
+    for (int i = 0; i < V / 2; ++i) f[i] = add2(f2(q[2 * i], q[2 * i + 1]), f2(-8388736.0f));
+}
+// code * step.
+template <int V>
+__device__ __forceinline__ void decode2(const CodeRaw<V>& r, float step, F2 (&f)[V / 2]) {
+    codes2<V>(r, f);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) f[i] = mul2(f[i], f2(step));
 }
 template <int V>
 __device__ __forceinline__ void decode(const CodeRaw<V>& r, float step, float (&f)[V]) {
