@@ -96,31 +96,46 @@ struct Source {
     }
 };
 
-// A block's column sums, first over its rows-at-a-time through `columns`
-// ([blockDim.y - 1][2][threads * V * NV] floats of shared memory), to its
-// place among the partial sums.
+// A block's column sums, first over its rows-at-a-time, to its place among the
+// partial sums: rows that share a warp by exchanges, the others through
+// `columns` ([groups - 1][2][threads * V * NV] floats of shared memory, see
+// column_groups).
 template <int V, int NV>
 __device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[V * NV / 2],
                                               F2 (&db)[V * NV / 2], float* columns) {
     constexpr int E = V * NV;
     const int tx = int(threadIdx.x), threads = int(blockDim.x);
     if (!p.partial) return;
-    // the block's rows-at-a-time, added in order by the first
-    if (blockDim.y > 1) {
-        __syncthreads();
-        float* mine = columns + (int(threadIdx.y) - 1) * 2 * threads * E;
-        float2* const mine2 = reinterpret_cast<float2*>(mine);
-        if (threadIdx.y > 0) {
+    int group = int(threadIdx.y), groups = int(blockDim.y);
+    bool lead = true;
+    if (threads < 32) {
+        for (int d = threads; d < 32; d <<= 1) {
 #pragma unroll
             for (int k = 0; k < E / 2; ++k) {
-                halves(dw[k], mine2[k * threads + tx].x, mine2[k * threads + tx].y);
-                float2& t = mine2[(E / 2 + k) * threads + tx];
-                halves(db[k], t.x, t.y);
+                dw[k] = add2(dw[k], F2{__shfl_xor_sync(0xFFFFFFFFu, dw[k].v, d)});
+                db[k] = add2(db[k], F2{__shfl_xor_sync(0xFFFFFFFFu, db[k].v, d)});
+            }
+        }
+        const int thread = int(threadIdx.y) * threads + tx;
+        group = thread >> 5;
+        groups = threads * int(blockDim.y) >> 5;
+        lead = (thread & 31) < threads;
+    }
+    if (groups > 1) {
+        __syncthreads();
+        float2* const mine = reinterpret_cast<float2*>(columns + (group - 1) * 2 * threads * E);
+        if (group > 0 && lead) {
+#pragma unroll
+            for (int k = 0; k < E / 2; ++k) {
+                float2& t = mine[k * threads + tx];
+                halves(dw[k], t.x, t.y);
+                float2& u = mine[(E / 2 + k) * threads + tx];
+                halves(db[k], u.x, u.y);
             }
         }
         __syncthreads();
-        if (threadIdx.y > 0) return;
-        for (int y = 0; y + 1 < int(blockDim.y); ++y) {
+        if (group > 0 || !lead) return;
+        for (int y = 0; y + 1 < groups; ++y) {
             const float2* other = reinterpret_cast<const float2*>(columns + y * 2 * threads * E);
 #pragma unroll
             for (int k = 0; k < E / 2; ++k) {
@@ -156,8 +171,8 @@ __device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[
     }
 }
 
-// One pass: blockDim.x threads (a multiple of 32, at most 512) share a row,
-// NV vectors of V channels each, vector i at (i * blockDim.x + threadIdx.x) *
+// One pass: blockDim.x threads (see row_sum; at most 512) share a row, NV
+// vectors of V channels each, vector i at (i * blockDim.x + threadIdx.x) *
 // V; blockDim.y rows at a time per block, the blocks' rows interleaved.
 template <typename T, int V, int NV, bool kSaved>
 __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ NormGradParams p) {
@@ -641,12 +656,15 @@ struct FusedShape {
     int64_t blocks;
 };
 FusedShape fused_shape(int64_t rows, int64_t width, int v, int nv) {
-    FusedShape f;
-    f.threads = int(round_up(ceil_div(width, int64_t(v) * nv), 32));
-    f.per_block = std::max(1, 256 / f.threads);
-    const int64_t resident = int64_t(kSms) * (512 / (f.threads * f.per_block));
-    f.blocks = std::max<int64_t>(1, std::min(resident, ceil_div(rows, f.per_block)));
-    return f;
+    const RowShape r = row_shape(width, v * nv, 1, 256);
+    const int64_t resident = int64_t(kSms) * (512 / (r.threads * r.per_block));
+    return FusedShape{r.threads, r.per_block,
+                      std::max<int64_t>(1, std::min(resident, ceil_div(rows, r.per_block)))};
+}
+
+// Groups of a block whose column sums meet in shared memory (store_partial).
+int column_groups(const FusedShape& f) {
+    return f.threads < 32 ? f.threads * f.per_block / 32 : f.per_block;
 }
 
 template <typename T, int V, int NV, bool kSaved>
@@ -654,8 +672,8 @@ cudaError_t launch_fused(NormGradParams& p, cudaStream_t s) {
     const FusedShape f = fused_shape(p.rows, p.width, V, NV);
     p.slices = int(f.blocks);
     void* args[] = {&p};
-    const size_t smem = size_t(f.per_block - 1) * 2 * f.threads * V * NV * 4;
     // at most 7 * 2 * 32 * 16 floats: within the 48 KB every kernel may have
+    const size_t smem = size_t(column_groups(f) - 1) * 2 * f.threads * V * NV * 4;
     return launch_grid((const void*)norm_grad_fused<T, V, NV, kSaved>, dim3(unsigned(f.blocks)),
                        dim3(f.threads, f.per_block), smem, args, s);
 }
