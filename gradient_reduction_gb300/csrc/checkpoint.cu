@@ -19,7 +19,7 @@ namespace {
 
 // blockDim.x threads along a row (a multiple of the lanes that hold a block
 // of channels, so that its peak is found within a warp), NV vectors of V
-// channels each per thread, blockDim.y rows per block; blockIdx.y counts
+// channels each per thread (own_channel), blockDim.y rows per block; blockIdx.y counts
 // along the row.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads) checkpoint_save(const __grid_constant__ CkptParams p) {
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) checkpoint_save(const __grid_constan
     Raw<T, V> raw[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+        const int c = own_channel<V, NV>(i);
         zero_raw(raw[i]);
         if (c < width) load_raw(x + c, raw[i]);
     }
@@ -57,14 +57,14 @@ __global__ void __launch_bounds__(kThreads) checkpoint_load(const __grid_constan
     float step[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+        const int c = own_channel<V, NV>(i);
         if (c >= width) continue;
         load_codes<V>(from + c, codes[i]);
         step[i] = step_value(steps[c / kBlockChannels]);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * int(blockDim.x) + int(threadIdx.x)) * V;
+        const int c = own_channel<V, NV>(i);
         if (c >= width) continue;
         float f[V];
         decode<V>(codes[i], step[i], f);

@@ -42,8 +42,8 @@ __device__ __forceinline__ void load_affine(const NormParams& p, int c, float (&
 
 // Vector accesses.  blockDim.x threads share a row (see row_sum), blockDim.y
 // rows at a time per block, the blocks' rows interleaved; each thread holds NV
-// vectors of V elements, vector i at (i * blockDim.x + threadIdx.x) * V, and
-// loads those of its next row while it works on one.
+// vectors of V elements (own_channel) and loads those of its next row while it
+// works on one.
 template <typename T, int V, int NV, bool kCkpt>
 __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormParams p) {
     __shared__ float s[2][2][8][32];
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(1024) norm_rows_any(const __grid_constant__ No
     __shared__ float s[2][8][32];
     grid_wait();
     grid_release();
-    const int tx = int(threadIdx.x), threads = int(blockDim.x);
+    const int tx = int(threadIdx.x);
     const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     const bool live = row < p.rows;   // the barriers below are for the whole block
     const int64_t r = live ? row : 0;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(1024) norm_rows_any(const __grid_constant__ No
     float d[NV], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = i * threads + tx;
+        const int c = own_channel<1, NV>(i);
         zero_raw(raw[i]);
         if (c < width) load_raw(x + c, raw[i]);
     }
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(1024) norm_rows_any(const __grid_constant__ No
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        d[i] = i * threads + tx < width ? __fsub_rn(d[i], mean) : 0.0f;
+        d[i] = own_channel<1, NV>(i) < width ? __fsub_rn(d[i], mean) : 0.0f;
         sq = __fmaf_rn(d[i], d[i], sq);
     }
     const float var = __fmul_rn(row_sum(sq, s[1]), p.inv_width);
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(1024) norm_rows_any(const __grid_constant__ No
     T* y = static_cast<T*>(p.y) + r * p.y_stride;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = i * threads + tx;
+        const int c = own_channel<1, NV>(i);
         zero_raw(raw[i]);
         if (c < width) {
             float f[1], w[1], b[1];

@@ -154,7 +154,7 @@ __device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * threads + tx) * V;
+        const int c = own_channel<V, NV>(i);
         if (c < p.width) {
             if constexpr (V >= 4) {
 #pragma unroll
@@ -172,8 +172,7 @@ __device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[
 }
 
 // One pass: blockDim.x threads (see row_sum; at most 512) share a row, NV
-// vectors of V channels each, vector i at (i * blockDim.x + threadIdx.x) *
-// V; blockDim.y rows at a time per block, the blocks' rows interleaved.
+// vectors of V channels each (own_channel); blockDim.y rows at a time per block, the blocks' rows interleaved.
 template <typename T, int V, int NV, bool kSaved>
 __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ NormGradParams p) {
     constexpr int E = V * NV;
@@ -191,7 +190,7 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
         if (p.weight) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * threads + tx) * V;
+                const int c = own_channel<V, NV>(i);
                 float v[V];
                 if (c < p.width) {
                     load_params<V>(p.weight, p.param_bf16, p.param_vec, c, v);
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
         rstd = live ? p.rstd[r] : 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * threads + tx) * V;
+            const int c = own_channel<V, NV>(i);
             zero_raw(dy[i]);
             x[i].zero();
             if (live && c < p.width) {
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
             T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * threads + tx) * V;
+                const int c = own_channel<V, NV>(i);
                 if (c < p.width) {
                     float v[V];
 #pragma unroll
@@ -656,7 +655,7 @@ struct FusedShape {
     int64_t blocks;
 };
 FusedShape fused_shape(int64_t rows, int64_t width, int v, int nv) {
-    const RowShape r = row_shape(width, v * nv, 1, 256);
+    const RowShape r = row_shape(width, v * nv, v == 1 ? 32 : 1, 256);
     const int64_t resident = int64_t(kSms) * (512 / (r.threads * r.per_block));
     return FusedShape{r.threads, r.per_block,
                       std::max<int64_t>(1, std::min(resident, ceil_div(rows, r.per_block)))};
@@ -686,7 +685,9 @@ cudaError_t launch_backward(NormGradParams& p, cudaStream_t s) {
             return p.width <= 4096 ? launch_fused<T, 8, 1, kSaved>(p, s)
                                    : launch_fused<T, 8, 2, kSaved>(p, s);
         else if constexpr (V == 8) return launch_fused<T, 8, 2, kSaved>(p, s);
-        else return launch_fused<T, 1, 16, kSaved>(p, s);
+        else
+            return p.width <= 128 ? launch_fused<T, 1, 4, kSaved>(p, s)
+                                  : launch_fused<T, 1, 16, kSaved>(p, s);
     }
     p.slices = slice_count(p.rows, p.width);
     p.slice_rows = ceil_div(p.rows, p.slices);
@@ -756,7 +757,9 @@ dpr_status dpr_layernorm_backward_workspace(int64_t rows, int64_t width, int64_t
     // the most that any access width asks for: 32 threads upward share a row
     int64_t slices = slice_count(rows, width), sums = round_up(rows * 8, 16);
     if (width <= kFusedWidth) {
-        slices = std::max(fused_shape(rows, width, 16, 1).blocks, fused_shape(rows, width, 8, 1).blocks);
+        slices = std::max({fused_shape(rows, width, 16, 1).blocks,
+                           fused_shape(rows, width, 8, 1).blocks,
+                           fused_shape(rows, width, 1, 16).blocks});
         sums = 0;
     }
     *bytes = sums + slices * 2 * round_up(width, 4) * 4;

@@ -176,6 +176,17 @@ __device__ __forceinline__ void load_params(const void* p, bool is_bf16, bool ve
     }
 }
 
+// First channel of the i-th of a thread's NV vectors: vectors of a row are
+// dealt out thread by thread; single elements warp by warp, 32 NV channels
+// each (blockDim.x a multiple of 32), which puts a thread's elements at fixed
+// distances.  Either way the threads of a block of channels are neighbours.
+template <int V, int NV>
+__device__ __forceinline__ int own_channel(int i) {
+    const int tx = int(threadIdx.x);
+    if constexpr (V == 1) return (tx >> 5) * (32 * NV) + i * 32 + (tx & 31);
+    else return (i * int(blockDim.x) + tx) * V;
+}
+
 // --- sums over the threads of a row -------------------------------------------
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -368,12 +379,10 @@ __device__ __forceinline__ void save_vector(const Raw<T, V>& raw, int c, bool on
     save_vector(raw, f, c, on, codes, steps);
 }
 
-// Saves a thread's NV vectors of a row, vector i at (i * blockDim.x +
-// threadIdx.x) * V; nothing from `width` on.  Every thread calls it.
+// Saves a thread's NV vectors of a row; nothing from `width` on.  Every thread calls it.
 template <typename T, int V, int NV>
 __device__ __forceinline__ void save_row(const Raw<T, V> (&raw)[NV], int width, int8_t* codes,
                                          uint8_t* steps) {
-    const int tx = int(threadIdx.x), threads = int(blockDim.x);
     if constexpr (V == 1) {
         // a warp's 32 lanes are a block of channels: all peaks first, for their latencies
         uint32_t byte[NV];
@@ -382,15 +391,15 @@ __device__ __forceinline__ void save_row(const Raw<T, V> (&raw)[NV], int width, 
             byte[i] = step_byte(__reduce_max_sync(0xFFFFFFFFu, peak_bits(raw[i])));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = i * threads + tx;
+            const int c = own_channel<V, NV>(i);
             const uint32_t q = encode_one(raw[i], byte[i]);
             if (c < width) codes[c] = int8_t(q);
-            if (c < width && (tx & 31) == 0) steps[c / kBlockChannels] = uint8_t(byte[i]);
+            if (c < width && (threadIdx.x & 31) == 0) steps[c / kBlockChannels] = uint8_t(byte[i]);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * threads + tx) * V;
+            const int c = own_channel<V, NV>(i);
             save_vector(raw[i], c, c < width, codes, steps);
         }
     }
