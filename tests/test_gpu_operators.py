@@ -626,6 +626,110 @@ def test_chains_on_side_streams_and_graphs_repeat_bit_for_bit(rows, width, progr
         dpr.dpr_set_programmatic_launch(old)
 
 
+def test_scratch_memory_is_shared_safely():
+    """Calls of different sizes on one stream, on two streams at once and inside a capture, each
+    with the library's own scratch memory, give what separate workspaces give."""
+    H.device()
+    sizes = [(40, 1056), (3, 8192), (700, 512), (40, 1056), (64, 4096)]
+
+    def make(rows, width, seed):
+        x, dy = (activation(rows, width, seed + k, F32).cuda() for k in range(2))
+        mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+        out = [torch.empty_like(x), torch.empty(width, device="cuda"), torch.empty(width, device="cuda")]
+        return (dy, x, None, mean, rstd, *out), out
+
+    calls = [make(r, w, 10 * i) for i, (r, w) in enumerate(sizes)]
+    want = []
+    for args, out in calls:
+        dpr.dpr_layernorm_backward(*args, workspace=torch.empty(16 << 20, dtype=torch.uint8, device="cuda"))
+        want.append([t.clone() for t in out])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for args, out in calls[:3]:
+            dpr.dpr_layernorm_backward(*args)
+        with torch.cuda.stream(side):
+            for args, out in calls[3:]:
+                dpr.dpr_layernorm_backward(*args)
+    torch.cuda.synchronize()
+    for (args, out), w in zip(calls, want):
+        assert _equal(out, w)
+        for t in out:
+            t.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for args, out in calls:
+            dpr.dpr_layernorm_backward(*args)
+    dpr.dpr_layernorm_backward(*make(5000, 8192, 99)[0])       # grows the kept memory
+    graph.replay()
+    torch.cuda.synchronize()
+    for (args, out), w in zip(calls, want):
+        assert _equal(out, w)
+
+
+def test_binding_refusals():
+    H.device()
+    x = torch.zeros(8, 64, device="cuda")
+    half = x.to(torch.float16)
+    saved = dpr.dpr_checkpoint_empty(8, 64)
+    stat, vec = torch.zeros(8, device="cuda"), torch.zeros(64, device="cuda")
+    bad = pytest.raises(ValueError)
+    with bad:
+        dpr.dpr_layernorm_forward(half, None, None, EPS, half)                    # dtype
+    with bad:
+        dpr.dpr_layernorm_forward(x, None, None, EPS, x[:4].clone())              # shape
+    with bad:
+        dpr.dpr_layernorm_forward(x, None, None, EPS, x.bfloat16())               # y's dtype
+    with bad:
+        dpr.dpr_layernorm_forward(x, vec[:32], None, EPS, x.clone())              # weight's length
+    with bad:
+        dpr.dpr_layernorm_forward(x, vec, vec.bfloat16(), EPS, x.clone())         # mixed dtypes
+    with bad:
+        dpr.dpr_layernorm_forward(x, None, None, EPS, x.clone(), stat.bfloat16())
+    with bad:
+        dpr.dpr_layernorm_forward(x, None, None, EPS, x.clone(), x_checkpoint=x)  # no Checkpoint
+    with bad:
+        dpr.dpr_layernorm_forward(x, None, None, EPS, x.clone(),
+                                  y_checkpoint=dpr.dpr_checkpoint_empty(8, 32))
+    with bad:
+        dpr.dpr_layernorm_forward(x.t(), None, None, EPS, x.t())                  # inner stride
+    with bad:
+        dpr.dpr_layernorm_forward(x.cpu(), None, None, EPS, x)
+    with pytest.raises(dpr.DprError):
+        dpr.dpr_layernorm_forward(x, None, None, -1.0, x.clone())
+    with pytest.raises(dpr.DprError):
+        dpr.dpr_layernorm_forward(x[:4], None, None, EPS, x[2:6])                 # overlap
+    args = (x, x.clone(), None, stat, stat.clone())
+    with bad:
+        dpr.dpr_layernorm_backward(*args, x[:, :32].clone())
+    with bad:
+        dpr.dpr_layernorm_backward(x, x.bfloat16(), None, stat, stat, x.clone())
+    with bad:
+        dpr.dpr_layernorm_backward(x, x, None, None, stat, x.clone())
+    with bad:
+        dpr.dpr_layernorm_backward(*args, x.clone(), vec, vec.bfloat16())
+    with bad:
+        dpr.dpr_layernorm_backward(*args, x.clone(), vec, vec.clone(),
+                                   workspace=torch.empty(4, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(dpr.DprError):
+        dpr.dpr_layernorm_backward(*args, x.clone(), vec, vec)                    # one for both
+    with bad:
+        dpr.dpr_checkpoint_save(x, dpr.Checkpoint(saved.codes, saved.steps[:, :1]))
+    with bad:
+        dpr.dpr_checkpoint_save(x, dpr.Checkpoint(saved.codes.view(torch.uint8), saved.steps))
+    with bad:
+        dpr.dpr_checkpoint_load(saved, torch.zeros(8, 32, device="cuda"))
+    dy = torch.zeros(8, 40, dtype=BF, device="cuda")
+    with bad:
+        dpr.dpr_linear_weight_grad(dy.float(), saved, torch.zeros(40, 64, device="cuda"))
+    with bad:
+        dpr.dpr_linear_weight_grad(dy, saved, torch.zeros(64, 40, device="cuda"))
+    with bad:
+        dpr.dpr_linear_weight_grad(dy[:4], saved, torch.zeros(40, 64, device="cuda"))
+    with bad:
+        dpr.dpr_linear_weight_grad(dy, saved, torch.zeros(40 * 64, device="cuda"))
+
+
 def test_leading_dimensions_merge():
     H.device()
     x = activation(24, 160, 1, BF).cuda()
@@ -674,3 +778,47 @@ def test_offsets_past_32_bits():
 def test_no_wait_ran_out():
     H.device()
     assert dpr.dpr_device_wait_failures() == 0
+
+
+@pytest.mark.parametrize("ranks,tokens,hidden,out", [(2, 300, 256, 200), (4, 130, 200, 72)])
+def test_step_of_a_block_into_the_bucket(ranks, tokens, hidden, out):
+    """The example's step: gradients of the block written into flat buckets from 8-bit
+    activations and reduce-scattered, against an fp32 autograd pass.  An activation is off by
+    at most half a step, step <= max|x| / 63.5: relative to the norm of a block of normal
+    values (max about 3 rms) an rms error of at most 3 / 63.5 / sqrt(12) = 1.4e-2; the
+    gradients read them once, and bf16 rounding adds 2^-8."""
+    H.device()
+    from examples import norm_linear_step as ex
+    g = torch.Generator(device="cuda").manual_seed(5)
+    block = ex.Block(hidden, out, ranks, g)
+    xs, dzs = ex.data(block, tokens, g)
+    parts, dxs, kept = ex.step(block, xs, dzs)
+    grads, want_dx = ex.autograd(block, xs, dzs)
+    assert kept < 0.56 * 4 * ranks * tokens * hidden
+    for got, want in zip(block.gradients(parts.view(-1)), grads):
+        assert ex.relative(got, want) < 2.5e-2
+    for got, want in zip(dxs, want_dx):
+        assert ex.relative(got, want) < 2.5e-2
+    # the bucket's gaps stay zero
+    used = torch.zeros(block.numel, dtype=torch.bool)
+    for t in block.gradients(used):
+        t.fill_(True)
+    assert bool((parts.view(-1).cpu()[~used] == 0).all())
+
+
+def test_step_matches_its_own_calls_bit_for_bit():
+    """The partitions are the exact ring mean of the gradients that the calls give on their own."""
+    H.device()
+    from examples import norm_linear_step as ex
+    from oracle import ring
+    g = torch.Generator(device="cuda").manual_seed(6)
+    block = ex.Block(160, 96, 2, g)
+    xs, dzs = ex.data(block, 77, g)
+    parts, _, _ = ex.step(block, xs, dzs)
+    buckets = torch.zeros(2, block.numel, dtype=BF, device="cuda")
+    for r in range(2):
+        _, kept = ex.forward(block, xs[r])
+        ex.backward(block, dzs[r], kept, buckets[r])
+    want, _ = ring.reduce_scatter([H.bits(b) for b in buckets], 2, 1, ring.RING_FP32, 0.5)
+    for j in range(2):
+        H.assert_f32_equal(parts[j].cpu().numpy(), want[j])
