@@ -24,7 +24,8 @@ struct NormParams {
     int64_t rows;
     int width;
     float eps;
-    float inv_width;
+    float count;            // width
+    float inv_width;        // its rounded reciprocal
     int param_bf16;
     int param_vec;          // weight and bias allow 16-byte accesses
 };
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormPar
             if (row + stride < p.rows && (i * threads + tx) * V < p.width)
                 load_raw(x + i * threads * V, next[i]);
         }
-        const float mean = __fmul_rn(row_sum(total(part), s[turn][0]), p.inv_width);
+        const float mean = divide(row_sum(total(part), s[turn][0]), p.count, p.inv_width);
         part = f2(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormPar
                     part = fma2(d[i][k], d[i][k], part);
                 }
             }
-        const float var = __fmul_rn(row_sum(total(part), s[turn][1]), p.inv_width);
+        const float var = divide(row_sum(total(part), s[turn][1]), p.count, p.inv_width);
         const float rstd = inverse_sqrt(__fadd_rn(var, p.eps));
         if (tx == 0 && live) {
             if (p.mean) p.mean[row] = mean;
@@ -158,14 +159,14 @@ __global__ void __launch_bounds__(1024) norm_rows_any(const __grid_constant__ No
         d[i] = f[0];
         sum = __fadd_rn(sum, d[i]);
     }
-    const float mean = __fmul_rn(row_sum(sum, s[0]), p.inv_width);
+    const float mean = divide(row_sum(sum, s[0]), p.count, p.inv_width);
     float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         d[i] = own_channel<1, NV>(i) < width ? __fsub_rn(d[i], mean) : 0.0f;
         sq = __fmaf_rn(d[i], d[i], sq);
     }
-    const float var = __fmul_rn(row_sum(sq, s[1]), p.inv_width);
+    const float var = divide(row_sum(sq, s[1]), p.count, p.inv_width);
     const float rstd = inverse_sqrt(__fadd_rn(var, p.eps));
     if (tx == 0 && live) {
         if (p.mean) p.mean[row] = mean;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(1024) norm_long_rows(const __grid_constant__ N
 #pragma unroll
         for (int k = 0; k < V; ++k) sum = __fadd_rn(sum, f[k]);
     }
-    const float mean = __fmul_rn(row_sum(sum, s[0]), p.inv_width);
+    const float mean = divide(row_sum(sum, s[0]), p.count, p.inv_width);
     float sq = 0.0f;
     for (int c = first; c < p.width; c += step) {
         load_raw(x + c, raw);
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(1024) norm_long_rows(const __grid_constant__ N
             sq = __fmaf_rn(d, d, sq);
         }
     }
-    const float var = __fmul_rn(row_sum(sq, s[1]), p.inv_width);
+    const float var = divide(row_sum(sq, s[1]), p.count, p.inv_width);
     const float rstd = inverse_sqrt(__fadd_rn(var, p.eps));
     if (threadIdx.x == 0) {
         if (p.mean) p.mean[row] = mean;
@@ -368,7 +369,7 @@ extern "C" dpr_status dpr_layernorm_forward(const void* x, int64_t x_stride, int
         a16 = a16 && rows_aligned(c->codes, c->code_stride, 1, 8);
     }
     p.rows = rows; p.width = int(width);
-    p.eps = eps; p.inv_width = 1.0f / float(width);
+    p.eps = eps; p.count = float(width); p.inv_width = 1.0f / float(width);
     p.param_bf16 = param_dtype == DPR_BF16;
     p.param_vec = aligned(weight, 16) && aligned(bias, 16);
     cudaStream_t s = static_cast<cudaStream_t>(stream);

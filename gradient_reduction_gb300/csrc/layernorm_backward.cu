@@ -34,7 +34,8 @@ struct NormGradParams {
     int slices;
     int64_t slice_rows;       // rows per slice (two passes)
     int depth;                // rows of a group in flight (one pass, staged)
-    float inv_width;
+    float count;              // width
+    float inv_width;          // its rounded reciprocal
     int param_bf16;
     int param_vec;
 };
@@ -263,8 +264,8 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
         float a = total(sum_g), b = total(sum_gh);
         row_sums(a, b, s[turn]);
         if (row < p.rows) {
-            const F2 minus_a = f2(-__fmul_rn(a, p.inv_width)), r2 = f2(r);
-            const F2 minus_b = f2(-__fmul_rn(b, p.inv_width));
+            const F2 minus_a = f2(-divide(a, p.count, p.inv_width)), r2 = f2(r);
+            const F2 minus_b = f2(-divide(b, p.count, p.inv_width));
             float d[E];
 #pragma unroll
             for (int k = 0; k < E / 2; ++k)
@@ -470,8 +471,8 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (row + j * stride >= p.rows) break;
-            const F2 minus_a = f2(-__fmul_rn(sums[2 * j], p.inv_width));
-            const F2 minus_b = f2(-__fmul_rn(sums[2 * j + 1], p.inv_width));
+            const F2 minus_a = f2(-divide(sums[2 * j], p.count, p.inv_width));
+            const F2 minus_b = f2(-divide(sums[2 * j + 1], p.count, p.inv_width));
             const F2 r2 = f2(now[j].rstd);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(256) norm_grad_rows(const __grid_constant__ No
     a = row_sum(a, s[0]);
     b = row_sum(b, s[1]);
     if (live && threadIdx.x == 0)
-        p.row_avg[row] = make_float2(__fmul_rn(a, p.inv_width), __fmul_rn(b, p.inv_width));
+        p.row_avg[row] = make_float2(divide(a, p.count, p.inv_width), divide(b, p.count, p.inv_width));
 }
 
 // dx of a tile of 32 V columns by a slice of the rows, and the tile's column
@@ -731,7 +732,8 @@ cudaError_t launch_staged(NormGradParams& p, int depth, cudaStream_t s) {
 
 template <typename T, int V>
 cudaError_t launch_source(NormGradParams& p, cudaStream_t s) {
-    // bulk copies take whole 16-byte pieces
+    // bulk copies take whole 16-byte pieces; more than 512 channels are at least
+    // 64 threads a row, so at most the 4 groups a block that the kernel has room for
     if (V > 1 && p.width > 512 && p.width <= kFusedWidth) {
         const bool saved = p.ckpt.codes != nullptr;
         const int depth = staged_depth(p.width, p.width * int64_t(sizeof(T) + (saved ? 1 : sizeof(T))));
@@ -831,6 +833,7 @@ dpr_status dpr_layernorm_backward(const void* dy, int64_t dy_stride, const void*
             p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums);
         p.partial_width = int(round_up(width, 4));
         p.rows = rows; p.width = int(width);
+        p.count = float(width);
         p.inv_width = 1.0f / float(width);
         p.param_bf16 = param_dtype == DPR_BF16;
         p.param_vec = aligned(weight, 16);

@@ -252,12 +252,25 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float2 (*s)[32]) {
     b = group_sum(v.y, n);
 }
 
-// 1 / sqrt(v) for v >= 0, within one unit in the last place or so: the
-// hardware's approximation and one Newton step.  (0 gives infinity.)
+// 1 / sqrt(v) for v >= 0, all but correctly rounded: the hardware's
+// approximation r, corrected by r (1 - v r^2) / 2 with the residual taken
+// exactly to first order.  A relative error of rstd scales its whole row, and
+// in fp32 turns codes of the row's checkpoint over, so the last bit counts.
+// (0 gives infinity.)
 __device__ __forceinline__ float inverse_sqrt(float v) {
     const float r = rsqrtf(v);
-    const float better = __fmul_rn(r, __fmaf_rn(__fmul_rn(-0.5f, v), __fmul_rn(r, r), 1.5f));
-    return v > 1e-30f && v < 1e30f ? better : r;
+    const float h = __fmul_rn(v, r), low = __fmaf_rn(v, r, -h);
+    const float e = __fmaf_rn(-low, r, __fmaf_rn(-h, r, 1.0f));
+    const float better = __fmaf_rn(__fmul_rn(0.5f, r), e, r);
+    return v > 1e-30f && v < 1e30f ? better : __fdiv_rn(1.0f, __fsqrt_rn(v));
+}
+
+// s / n, all but correctly rounded: the product with the rounded reciprocal,
+// corrected by its remainder.
+__device__ __forceinline__ float divide(float s, float n, float inverse) {
+    const float q = __fmul_rn(s, inverse);
+    const float better = __fmaf_rn(__fmaf_rn(-q, n, s), inverse, q);
+    return fabsf(s) < 1e30f ? better : q;   // the remainder of a huge or infinite s is none
 }
 
 // --- the 8-bit format -----------------------------------------------------------

@@ -415,6 +415,65 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
     if (warp == 1) tc::tmem_free(tmem, 512);
 }
 
+// Up to four tokens: the product is an outer product or little more, and
+// writing dW is all that takes time, which the tensor-core kernel's eight
+// storing warps do more slowly (4 tokens, 4096 x 4096, fp32: 11.8 us here,
+// 16.7 there; 2 tokens, 10038 x 2934: 28 and 51).  A block holds the tokens of
+// 1024 in-features, 4 a thread, in registers, and walks over out-features 4 at
+// a time, whose dY it keeps in shared memory.  Any strides and addresses.
+// (With 16 tokens in registers the loads of the codes one by one take longer
+// than the tensor-core kernel does: 38 us against 17.)
+constexpr int kFew = 4;
+constexpr int kFewThreads = 256, kFewOut = 64;
+__global__ void __launch_bounds__(kFewThreads)
+weight_grad_few(const __grid_constant__ WeightGradParams p, const uint16_t* dy, int64_t dy_stride,
+                dpr_checkpoint x, int tokens) {
+    __shared__ __align__(16) float d[kFew][kFewOut];
+    grid_wait();
+    grid_release();
+    const int i0 = int(blockIdx.x) * 4 * kFewThreads + int(threadIdx.x);
+    const int o0 = int(blockIdx.y) * kFewOut;
+    for (int q = int(threadIdx.x); q < kFew * kFewOut; q += kFewThreads) {
+        const int t = q / kFewOut, o = o0 + q % kFewOut;
+        d[t][q % kFewOut] = t < tokens && o < p.out_features ? bf_1(dy[t * dy_stride + o]) : 0.0f;
+    }
+    float v[kFew][4];
+#pragma unroll
+    for (int t = 0; t < kFew; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * kFewThreads;
+            v[t][j] = 0.0f;
+            if (t < tokens && i < p.in_features) {
+                CodeRaw<1> code;
+                float f[1];
+                load_codes<1>(x.codes + t * x.code_stride + i, code);
+                decode<1>(code, step_value(x.steps[t * x.step_stride + i / kBlockChannels]), f);
+                v[t][j] = f[0];
+            }
+        }
+    __syncthreads();
+    const int rows = min(kFewOut, p.out_features - o0);
+    for (int r = 0; r < rows; r += 4) {
+        float acc[4][4] = {};
+#pragma unroll
+        for (int t = 0; t < kFew; ++t) {
+            const float4 a = *reinterpret_cast<const float4*>(&d[t][r]);
+            const float w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = __fmaf_rn(w[m], v[t][j], acc[m][j]);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r + m < rows && i0 + j * kFewThreads < p.in_features)
+                    put_grad(p, int64_t(o0 + r + m) * p.dw_stride + i0 + j * kFewThreads, acc[m][j]);
+    }
+}
+
 // Tiles summed in parts: the parts in token order, then as put_grad.  A block
 // joins two out-features of a dealt-out tile, 64 threads and 4 in-features a
 // thread for each, so that a single tile still spreads over 128 SMs; the
@@ -461,15 +520,27 @@ weight_grad_join(const __grid_constant__ WeightGradParams p, int pairs) {
             put_grad(p, int64_t(o + row) * p.dw_stride + i + column + 64 * j, v[j]);
 }
 
-// Rows copied to 16-byte-aligned ones, for inputs that TMA cannot read.
+// Rows copied to 16-byte-aligned ones, for inputs that TMA cannot read; four
+// loads of a thread in flight before its stores.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) repack_rows(const T* from, int64_t from_stride, T* to,
-                                                        int64_t to_stride, int64_t rows, int width) {
+__global__ void __launch_bounds__(kThreads)
+repack_rows(const T* __restrict__ from, int64_t from_stride, T* __restrict__ to, int64_t to_stride,
+            int64_t rows, int width) {
     grid_wait();
     grid_release();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int c = int(threadIdx.x); c < width; c += kThreads)
-            to[r * to_stride + c] = from[r * from_stride + c];
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T* f = from + r * from_stride;
+        T* t = to + r * to_stride;
+        for (int c0 = int(threadIdx.x); c0 < width; c0 += 4 * kThreads) {
+            T v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j * kThreads < width) v[j] = f[c0 + j * kThreads];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j * kThreads < width) t[c0 + j * kThreads] = v[j];
+        }
+    }
 }
 
 // dW = 0, for a call without tokens.
@@ -540,13 +611,14 @@ struct Plan {
 constexpr int kPairs = 76;           // of a GB300's 152 SMs
 
 // Can TMA read these rows where they are?
-bool tma_rows(const void* p, int64_t stride, int64_t size, int64_t rows, int64_t width) {
-    return aligned(p, 16) && (rows <= 1 || (stride >= width && stride * size % 16 == 0));
+bool tma_rows(const void* p, int64_t stride, int64_t size, int64_t width) {
+    return aligned(p, 16) && stride >= width && stride * size % 16 == 0;
 }
 
 Plan make_plan(const void* dy, int64_t dy_stride, const dpr_checkpoint* x, int64_t rows,
                int64_t out_features, int64_t in_features) {
     Plan q = {};
+    if (rows <= kFew) return q;
     q.out_tiles = int(ceil_div(out_features, kTile));
     q.in_tiles = int(ceil_div(in_features, kTile));
     q.blocks = int(ceil_div(rows, kTokens));
@@ -558,10 +630,10 @@ Plan make_plan(const void* dy, int64_t dy_stride, const dpr_checkpoint* x, int64
     q.rest_chunk = std::min<int64_t>(q.blocks, std::max<int64_t>(ceil_div(steps, kPairs), 4));
     q.join = q.rest_tiles > 0 && q.rest_chunk < q.blocks;
     q.partial_bytes = q.join ? int64_t(2 * kPairs) * kTile * kTile * 4 : 0;
-    q.copy_dy = !tma_rows(dy, dy_stride, 2, rows, out_features);
+    q.copy_dy = !tma_rows(dy, dy_stride, 2, out_features);
     q.dy_bytes = q.copy_dy ? rows * round_up(out_features, 8) * 2 : 0;
-    q.copy_x = !tma_rows(x->codes, x->code_stride, 1, rows, in_features) ||
-               !tma_rows(x->steps, x->step_stride, 1, rows,
+    q.copy_x = !tma_rows(x->codes, x->code_stride, 1, in_features) ||
+               !tma_rows(x->steps, x->step_stride, 1,
                          ceil_div(in_features, kBlockChannels));
     if (q.copy_x) {
         q.code_bytes = rows * round_up(in_features, 16);
@@ -587,7 +659,7 @@ cudaError_t repack(const void* from, int64_t from_stride, void* to, int64_t to_s
     const T* f = static_cast<const T*>(from);
     T* t = static_cast<T*>(to);
     void* args[] = {&f, &from_stride, &t, &to_stride, &rows, &width};
-    return launch_grid((const void*)repack_rows<T>, dim3(unsigned(std::min<int64_t>(rows, 152 * 8))),
+    return launch_grid((const void*)repack_rows<T>, dim3(unsigned(std::min<int64_t>(rows, 152 * 16))),
                        dim3(kThreads), 0, args, s);
 }
 
@@ -650,6 +722,17 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
                                               dim3(kThreads), 0, args, s));
     }
 
+    if (rows <= kFew) {
+        const uint16_t* d = static_cast<const uint16_t*>(dy);
+        dpr_checkpoint x = *x_ckpt;
+        int tokens = int(rows);
+        void* args[] = {&p, &d, &dy_stride, &x, &tokens};
+        return record_cuda_status(launch_grid(
+            (const void*)weight_grad_few,
+            dim3(unsigned(ceil_div(in_features, 4 * kFewThreads)),
+                 unsigned(ceil_div(out_features, kFewOut))),
+            dim3(kFewThreads), 0, args, s));
+    }
     const Plan q = make_plan(dy, dy_stride, x_ckpt, rows, out_features, in_features);
     p.out_tiles = q.out_tiles; p.in_tiles = q.in_tiles; p.blocks = q.blocks;
     p.waves = q.waves; p.rest_tiles = q.rest_tiles; p.rest_chunk = q.rest_chunk;
@@ -676,12 +759,6 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
     }
     EncodeTiled fn = nullptr;
     if (e == cudaSuccess) e = encoder(&fn);
-    // one row's stride is never used, but has to be a multiple of 16 bytes all the same
-    if (rows == 1) {
-        dy_stride = round_up(out_features, 8);
-        x.code_stride = round_up(in_features, 16);
-        x.step_stride = round_up(ceil_div(in_features, kBlockChannels), 16);
-    }
     if (e == cudaSuccess)
         e = encode(fn, &p.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, dy_stride, rows,
                    out_features, 64, CU_TENSOR_MAP_SWIZZLE_128B);

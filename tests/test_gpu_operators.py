@@ -478,7 +478,8 @@ def _weight_grad(rows, o, i, dtype, layout="plain", accumulate=False, exact=Fals
         p.check_guards("weight gradient")
 
 
-SIZES = [(1, 1, 1), (1, 8, 16), (2, 64, 33), (15, 8, 128), (16, 128, 128), (17, 256, 160),
+SIZES = [(1, 1, 1), (1, 8, 16), (2, 64, 33), (3, 70, 1100), (4, 257, 2050), (5, 257, 2050),
+         (15, 8, 128), (16, 128, 128), (17, 256, 160),
          (63, 100, 100), (64, 256, 128), (65, 264, 144), (128, 512, 512), (200, 1000, 48),
          (500, 72, 1008), (1025, 136, 272), (333, 257, 511)]
 
@@ -493,7 +494,7 @@ def test_weight_grad_sizes(rows, o, i, dtype):
 
 @pytest.mark.parametrize("layout", list(LAYOUTS))
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("rows,o,i", [(70, 136, 144), (33, 65, 97)])
+@pytest.mark.parametrize("rows,o,i", [(70, 136, 144), (33, 65, 97), (3, 65, 97)])
 def test_weight_grad_layouts(rows, o, i, dtype, layout):
     H.device()
     _weight_grad(rows, o, i, dtype, layout)
