@@ -35,10 +35,18 @@ namespace {
 template <int V>
 __device__ __forceinline__ void load_affine(const NormParams& p, int c, float (&w)[V],
                                             float (&b)[V]) {
+    if (p.weight) {
+        load_params<V>(p.weight, p.param_bf16, p.param_vec, c, w);
+    } else {
 #pragma unroll
-    for (int k = 0; k < V; ++k) { w[k] = 1.0f; b[k] = 0.0f; }
-    if (p.weight) load_params<V>(p.weight, p.param_bf16, p.param_vec, c, w);
-    if (p.bias) load_params<V>(p.bias, p.param_bf16, p.param_vec, c, b);
+        for (int k = 0; k < V; ++k) w[k] = 1.0f;
+    }
+    if (p.bias) {
+        load_params<V>(p.bias, p.param_bf16, p.param_vec, c, b);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) b[k] = 0.0f;
+    }
 }
 
 // Vector accesses.  blockDim.x threads share a row (see row_sum), blockDim.y
@@ -59,8 +67,8 @@ __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormPar
     Raw<T, V> next[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        zero_raw(next[i]);
         if (row < p.rows && (i * threads + tx) * V < p.width) load_raw(x + i * threads * V, next[i]);
+        else zero_raw(next[i]);
     }
     int turn = 0;
     // rows that share a warp take the same number of turns: their lanes work together
@@ -85,9 +93,9 @@ __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormPar
         x += x_step;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            zero_raw(next[i]);
             if (row + stride < p.rows && (i * threads + tx) * V < p.width)
                 load_raw(x + i * threads * V, next[i]);
+            else zero_raw(next[i]);
         }
         const float mean = divide(row_sum(total(part), s[turn][0]), p.count, p.inv_width);
         part = f2(0.0f);
@@ -111,7 +119,6 @@ __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormPar
             const int c = (i * threads + tx) * V;
             const bool on = live && c < p.width;
             Raw<T, V> raw;
-            zero_raw(raw);
             if (on) {
                 float w[V], b[V];
                 load_affine<V>(p, c, w, b);
@@ -121,6 +128,8 @@ __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormPar
                                    f2(b[2 * k], b[2 * k + 1]));
                 pack2(d[i], raw);
                 store_raw(y + i * threads * V, raw);
+            } else {
+                zero_raw(raw);
             }
             if (kCkpt && p.y_ckpt.codes) {
                 const int64_t r = live ? row : 0;

@@ -219,11 +219,12 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = own_channel<V, NV>(i);
-            zero_raw(dy[i]);
-            x[i].zero();
             if (live && c < p.width) {
                 load_raw(static_cast<const T*>(p.dy) + r * p.dy_stride + c, dy[i]);
                 x[i].load(p, r, c);
+            } else {
+                zero_raw(dy[i]);
+                x[i].zero();
             }
         }
     };
