@@ -27,7 +27,7 @@ struct NormParams {
     float count;            // width
     float inv_width;        // its rounded reciprocal
     int param_bf16;
-    int param_vec;          // weight and bias allow 16-byte accesses
+    int param_vec;          // bytes an access of weight and bias may take
 };
 
 namespace {
@@ -54,11 +54,12 @@ __device__ __forceinline__ void load_affine(const NormParams& p, int c, float (&
 // vectors of V elements and loads those of its next row while it works on one.
 // Reads x, writes y: 4 bytes an element in bf16.  16384 x 4096 bf16: 50.5 us,
 // 5.3 TB/s (0.78 of the measured copy rate), with both checkpoints written 80 us,
-// 5.1 TB/s; 16384 x 8192 fp32: 172 us, 6.2 TB/s.  What bounds bf16 is the
+// 5.1 TB/s; 16384 x 8192 fp32: 165 us, 6.5 TB/s.  What bounds bf16 is the
 // row's chain of two sums across the threads and its instructions (16 warps an
 // SM at 110 registers, 56% of the issue slots used), not memory: fewer channels
-// a thread (16: 57 us) or more (64: spills) are slower, and so are copies into
-// shared memory ahead of time (62 us), which cost more than the registers.
+// a thread (16: 57 us) or more (64: spills) are slower, and so are registers
+// capped for more warps (104: 54 us) and copies into shared memory ahead of time
+// (62 us), which cost more than the registers.
 template <typename T, int V, int NV, bool kCkpt>
 __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormParams p) {
     __shared__ float s[2][2][8][32];
@@ -389,7 +390,7 @@ extern "C" dpr_status dpr_layernorm_forward(const void* x, int64_t x_stride, int
     p.rows = rows; p.width = int(width);
     p.eps = eps; p.count = float(width); p.inv_width = 1.0f / float(width);
     p.param_bf16 = param_dtype == DPR_BF16;
-    p.param_vec = aligned(weight, 16) && aligned(bias, 16);
+    p.param_vec = param_access(weight, bias);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     const bool bf = dtype == DPR_BF16;

@@ -738,8 +738,8 @@ cudaError_t launch_staged(NormGradParams& p, int depth, cudaStream_t s) {
     const size_t sums = size_t(f.per_block - 1) * 2 * f.threads * 16 * 4;
     const size_t rows = size_t(f.per_block) * depth * p.width * (sizeof(T) + (kSaved ? 1 : sizeof(T)));
     const void* k = (const void*)norm_grad_staged<T, kSaved>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(kShared));
+    static std::atomic<uint64_t> allowed{0};   // of this kernel: one per instantiation
+    const cudaError_t e = allow_shared_memory(k, int(kShared), &allowed);
     if (e != cudaSuccess) return e;
     void* args[] = {&p};
     return launch_grid(k, dim3(unsigned(f.blocks)), dim3(f.threads, f.per_block),
@@ -852,7 +852,7 @@ dpr_status dpr_layernorm_backward(const void* dy, int64_t dy_stride, const void*
         p.count = float(width);
         p.inv_width = 1.0f / float(width);
         p.param_bf16 = param_dtype == DPR_BF16;
-        p.param_vec = aligned(weight, 16);
+        p.param_vec = param_access(weight, nullptr);
         bool a32 = rows_aligned(dy, dy_stride, es, 32) && rows_aligned(dx, dx_stride, es, 32);
         bool a16 = rows_aligned(dy, dy_stride, es, 16) && rows_aligned(dx, dx_stride, es, 16);
         if (x_ckpt) {

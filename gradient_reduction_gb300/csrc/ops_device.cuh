@@ -141,14 +141,30 @@ __device__ __forceinline__ void pack2(const F2 (&f)[V / 2], Raw<T, V>& r) {
     pack(v, r);
 }
 
-// V parameter values (weight, bias), bf16 or fp32 by `is_bf16`; `vec`:
-// 16-byte accesses are allowed.
+// V parameter values (weight, bias), bf16 or fp32 by `is_bf16`; `vec`: how many
+// bytes an access may take (32, 16 or one element).  32-byte accesses matter
+// although the values come from L1: two 16-byte ones touch every sector twice.
+// Volatile, so that none moves above the wait for the grid before.
+__device__ __forceinline__ void ld_v8_cached(const void* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+          "=r"(w[7])
+        : "l"(p));
+}
 template <int V>
-__device__ __forceinline__ void load_params(const void* p, bool is_bf16, bool vec, int64_t at,
+__device__ __forceinline__ void load_params(const void* p, bool is_bf16, int vec, int64_t at,
                                             float (&f)[V]) {
     if (is_bf16) {
         const uint16_t* q = static_cast<const uint16_t*>(p) + at;
-        if (V >= 8 && vec) {
+        if (V == 16 && vec == 32) {
+            uint32_t w[8];
+            ld_v8_cached(q, w);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) {
+                f[2 * i] = bf_lo(w[i & 7]);
+                f[2 * i + 1] = bf_hi(w[i & 7]);
+            }
+        } else if (V >= 8 && vec >= 16) {
 #pragma unroll
             for (int i = 0; i < V / 8; ++i) {
                 const uint4 v = *reinterpret_cast<const uint4*>(q + 8 * i);
@@ -163,7 +179,15 @@ __device__ __forceinline__ void load_params(const void* p, bool is_bf16, bool ve
         }
     } else {
         const float* q = static_cast<const float*>(p) + at;
-        if (V >= 8 && vec) {
+        if (V >= 8 && vec == 32) {
+#pragma unroll
+            for (int i = 0; i < V / 8; ++i) {
+                uint32_t w[8];
+                ld_v8_cached(q + 8 * i, w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[8 * i + k] = __uint_as_float(w[k]);
+            }
+        } else if (V >= 4 && vec >= 16) {
 #pragma unroll
             for (int i = 0; i < V / 4; ++i) {
                 const float4 v = *reinterpret_cast<const float4*>(q + 4 * i);

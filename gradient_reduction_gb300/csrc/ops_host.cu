@@ -29,19 +29,33 @@ cudaError_t resident_blocks(const void* kernel, int threads, int64_t* blocks) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_tuple(kernel, threads, dev);
-    auto it = cache.find(key);
-    if (it == cache.end()) {
-        int sms = 0, per_sm = 0;
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess)
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
-        if (e != cudaSuccess) return e;
-        it = cache.emplace(key, int64_t(sms) * (per_sm < 1 ? 1 : per_sm)).first;
+    try {
+        std::lock_guard<std::mutex> lock(mu);
+        const auto key = std::make_tuple(kernel, threads, dev);
+        auto it = cache.find(key);
+        if (it == cache.end()) {
+            int sms = 0, per_sm = 0;
+            e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+            if (e != cudaSuccess) return e;
+            it = cache.emplace(key, int64_t(sms) * (per_sm < 1 ? 1 : per_sm)).first;
+        }
+        *blocks = it->second;
+    } catch (...) {   // out of host memory: no exception leaves a C entry
+        return cudaErrorMemoryAllocation;
     }
-    *blocks = it->second;
     return cudaSuccess;
+}
+
+cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>* done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (e != cudaSuccess || (dev < 64 && (done->load(std::memory_order_acquire) & bit))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done->fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 dpr_status check_matrix_size(int64_t rows, int64_t width) {

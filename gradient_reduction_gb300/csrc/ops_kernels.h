@@ -2,6 +2,7 @@
 // with any block size, argument checks, and the selection of access widths.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -74,6 +75,10 @@ struct SpanList {
 // the current device at once; remembered per kernel and size.
 cudaError_t resident_blocks(const void* kernel, int threads, int64_t* blocks);
 
+// Allows `kernel` that much dynamic shared memory, once per device (`done`: a
+// bit for each, the kernel's own).
+cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>* done);
+
 // Threads that share a row of `width` channels at `elems` per thread, and rows
 // per block of at least `block` threads: a power of two below 32 (at least
 // `least`, the lanes that hold a block of channels), else a multiple of 32.
@@ -87,6 +92,12 @@ inline RowShape row_shape(int64_t width, int elems, int least, int block) {
     else
         while (threads < need || threads < least) threads *= 2;
     return RowShape{threads, threads >= block ? 1 : block / threads};
+}
+
+// Bytes an access of parameters may take (NULL allows any).
+inline int param_access(const void* weight, const void* bias) {
+    if (aligned(weight, 32) && aligned(bias, 32)) return 32;
+    return aligned(weight, 16) && aligned(bias, 16) ? 16 : 1;
 }
 
 // Elements per access for an activation of `dtype` whose rows are `width`

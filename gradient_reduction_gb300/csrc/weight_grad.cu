@@ -585,19 +585,6 @@ cudaError_t encoder(EncodeTiled* fn) {
     return cudaSuccess;
 }
 
-// weight_grad_pairs' shared memory, allowed once per device.
-cudaError_t allow_shared_memory() {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) & bit))) return e;
-    e = cudaFuncSetAttribute((const void*)weight_grad_pairs,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
-    return e;
-}
-
 // A [rows, width] tensor read in boxes of `box` elements by kTokens rows.
 cudaError_t encode(EncodeTiled fn, CUtensorMap* map, CUtensorMapDataType type, int64_t size,
                    const void* p, int64_t stride, int64_t rows, int64_t width, int box,
@@ -781,7 +768,9 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
     if (e == cudaSuccess)
         e = encode(fn, &p.steps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.steps, x.step_stride, rows,
                    ceil_div(in_features, kBlockChannels), 16, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (e == cudaSuccess) e = allow_shared_memory();
+    static std::atomic<uint64_t> allowed{0};
+    if (e == cudaSuccess)
+        e = allow_shared_memory((const void*)weight_grad_pairs, kSmemBytes, &allowed);
     if (e != cudaSuccess) return record_cuda_status(e);
     void* args[] = {&p};
     // pairs without work are not launched, unless whole waves need all of them
