@@ -216,6 +216,50 @@ def test_norm_forward_layouts(width, layout, dtype, pdtype):
     _forward(3, width, dtype, pdtype, layout, ckpt=True)
 
 
+# where a rule changes the kernel: vectors of 8, 48 channels a thread, three reads of a row, the
+# staged, register and two-pass backward kernels
+EDGES = [510, 512, 520, 528, 4104, 5136, 8192, 8200, 10240, 12288, 16376, 24576, 24592]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("width", EDGES)
+def test_norm_at_the_edges_of_the_rules(width, dtype):
+    H.device()
+    _forward(6, width, dtype, dtype, ckpt=True)
+    _backward(6, width, dtype, dtype)
+    _backward(6, width, dtype, dtype, source="saved")
+
+
+@pytest.mark.parametrize("rows,width", [(1300, 528), (2500, 1024), (700, 4096), (900, 8192),
+                                        (4000, 64), (1250, 16), (9000, 8)])
+def test_norm_many_rows_per_block(rows, width):
+    """Several rows to every block of the GPU: loops, rings and prefetches go round."""
+    H.device()
+    for dtype in (BF, F32):
+        _forward(rows, width, dtype, F32, ckpt=True)
+        _backward(rows, width, dtype, F32)
+        _backward(rows, width, dtype, F32, source="saved", into="dy")
+
+
+@pytest.mark.parametrize("shift", [0, 8, 1])
+@pytest.mark.parametrize("pdtype", [BF, F32])
+def test_norm_parameters_at_any_address(shift, pdtype):
+    """Weight and bias 32-byte, 16-byte (bf16) and element aligned give the same bits."""
+    H.device()
+    x, dy = (activation(40, 1056, k, BF).cuda() for k in range(2))
+    w0, b0 = (activation(1, 1056, 5 + k, pdtype)[0] for k in range(2))
+    mean, rstd = torch.empty(40, device="cuda"), torch.empty(40, device="cuda")
+    got = []
+    for s in (0, shift):
+        w, b = (Placed(1, 1056, pdtype, 0, s, t[None]).view[0] for t in (w0, b0))
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        dw, db = torch.empty(1056, device="cuda"), torch.empty(1056, device="cuda")
+        dpr.dpr_layernorm_forward(x, w, b, EPS, y, mean, rstd)
+        dpr.dpr_layernorm_backward(dy, x, w, mean, rstd, dx, dw, db)
+        got.append((y, dx, dw, db))
+    assert _equal(*got)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 7, 8, 9, 33, 300])
 def test_norm_forward_rows(rows):
     H.device()
@@ -508,6 +552,16 @@ def test_weight_grad_long(rows, o, i, dtype):
     H.device()
     _weight_grad(rows, o, i, dtype, exact=True)
     _weight_grad(rows, o, i, dtype, exact=True, accumulate=True)
+    _weight_grad(rows, o, i, dtype)
+
+
+@pytest.mark.parametrize("rows,o,i,dtype", [(200, 2304, 2304, F32), (1100, 2310, 2305, BF),
+                                            (65, 5000, 1100, BF), (3, 3001, 1030, F32)])
+def test_weight_grad_more_tiles_than_pairs(rows, o, i, dtype):
+    """Whole waves of tiles and a dealt-out rest in one call."""
+    H.device()
+    _weight_grad(rows, o, i, dtype, exact=True)
+    _weight_grad(rows, o, i, dtype, exact=True, accumulate=True, layout="odd")
     _weight_grad(rows, o, i, dtype)
 
 
