@@ -6,8 +6,10 @@
 // sums are joined by a second, small kernel in a fixed order.  Rows of at most
 // 512 channels, or whose parts are not 16-byte aligned, are loaded into
 // registers a row ahead (norm_grad_fused), the others staged in shared memory
-// (norm_grad_staged; fp32 rows too large for that, in registers).  Longer rows
-// take two passes, row sums first, then columns.
+// (norm_grad_staged; fp32 rows too large for that, in registers).  Rows of up
+// to 16384 channels whose parts are aligned take the staged kernel too, a row
+// to two CTAs of a cluster.  All others take two passes, row sums first, then
+// columns.
 #include <algorithm>
 
 #include "ops_device.cuh"
@@ -102,10 +104,11 @@ struct Source {
 // A block's column sums, first over its rows-at-a-time, to its place among the
 // partial sums: rows that share a warp by exchanges, the others through
 // `columns` ([groups - 1][2][threads * V * NV] floats of shared memory, see
-// column_groups).
+// column_groups).  The block owns `width` columns from `base` on.
 template <int V, int NV>
 __device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[V * NV / 2],
-                                              F2 (&db)[V * NV / 2], float* columns) {
+                                              F2 (&db)[V * NV / 2], float* columns, int64_t slice,
+                                              int base, int width) {
     constexpr int E = V * NV;
     const int tx = int(threadIdx.x), threads = int(blockDim.x);
     if (!p.partial) return;
@@ -148,7 +151,7 @@ __device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[
             }
         }
     }
-    float* to = p.partial + int64_t(blockIdx.x) * 2 * p.partial_width;
+    float* to = p.partial + slice * 2 * p.partial_width + base;
     float out_w[E], out_b[E];
 #pragma unroll
     for (int k = 0; k < E / 2; ++k) {
@@ -158,7 +161,7 @@ __device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = own_channel<V, NV>(i);
-        if (c < p.width) {
+        if (c < width) {
             if constexpr (V >= 4) {
 #pragma unroll
                 for (int k = i * V; k < i * V + V; k += 4) {
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ N
             }
         }
     }
-    store_partial<V, NV>(p, dw, db, columns);
+    store_partial<V, NV>(p, dw, db, columns, blockIdx.x, 0, p.width);
 }
 
 // Four sums over the blockDim.x threads (64 to 512) that share threadIdx.y;
@@ -331,39 +334,55 @@ __device__ __forceinline__ void row_sums4(float (&v)[4], float (*s)[16][4]) {
 // issue slots, at 16 warps an SM that its 128 registers allow).  One row a turn
 // in registers: 76 and 83 us; 8 channels a thread: 125 and 134 us; deeper
 // staging or loads asked for earlier: no difference.
-template <typename T, bool kSaved>
+// kPair: a row to two CTAs of a cluster, which send each other their half's
+// four sums.  8192 x 11008 bf16: 117 us (two passes: 166), from a checkpoint 138
+// (154); 8192 x 12288: 117 and 144 us, 8192 x 12288 fp32: 206 us, 5.9 TB/s.  A
+// turn waits once for the other CTA, with one CTA an SM to fill the gap.
+template <typename T, bool kSaved, bool kPair>
 __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ NormGradParams p) {
     constexpr int V = 16 / int(sizeof(T)), NV = 16 / V, E = 16;
     __shared__ float s[2][4][16][4];
     __shared__ __align__(8) uint64_t bars[4][kMaxDepth];
+    __shared__ __align__(16) float other[2][4];      // the other CTA's four sums
+    __shared__ __align__(8) uint64_t sent[2];
     extern __shared__ __align__(16) uint8_t ring[];
     const int tx = int(threadIdx.x), threads = int(blockDim.x);
     const uint32_t full = tc::smem_addr(bars[threadIdx.y]);
     if (tx == 0) {
         for (int k = 0; k < p.depth; ++k) tc::mbar_init(full + 8 * k, 1);
+        if constexpr (kPair)
+            for (int k = 0; k < 2; ++k) tc::mbar_init(tc::smem_addr(&sent[k]), 1);
         tc::mbar_init_fence();
     }
     __syncthreads();
+    if constexpr (kPair) tc::cluster_sync();
     grid_wait();
     grid_release();
-    const uint32_t dy_bytes = uint32_t(p.width) * sizeof(T);
-    const uint32_t x_bytes = kSaved ? uint32_t(p.width) : dy_bytes;
+    // this CTA's columns and the place of its rows among those of all
+    const uint32_t rank = kPair ? tc::cluster_rank() : 0;
+    const int base = int(rank) * threads * E;
+    const int width = kPair && rank == 0 ? threads * E : p.width - base;
+    const int64_t slice = kPair ? blockIdx.x >> 1 : blockIdx.x;
+    const int64_t slices = kPair ? gridDim.x >> 1 : gridDim.x;
+    const uint32_t dy_bytes = uint32_t(width) * sizeof(T);
+    const uint32_t x_bytes = kSaved ? uint32_t(width) : dy_bytes;
     const uint32_t stage = dy_bytes + x_bytes;
     const uint32_t mine = tc::smem_addr(ring) + threadIdx.y * p.depth * stage;
-    const int64_t stride = int64_t(gridDim.x) * blockDim.y;
-    const int64_t row0 = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t stride = slices * blockDim.y;
+    const int64_t row0 = slice * blockDim.y + threadIdx.y;
     const auto fetch = [&](int64_t r, uint32_t k) {
-        const void* x = kSaved ? static_cast<const void*>(p.ckpt.codes + r * p.ckpt.code_stride)
-                               : static_cast<const T*>(p.x) + r * p.x_stride;
+        const void* x = kSaved ? static_cast<const void*>(p.ckpt.codes + r * p.ckpt.code_stride + base)
+                               : static_cast<const T*>(p.x) + r * p.x_stride + base;
         tc::mbar_expect(full + 8 * k, stage);
-        tc::bulk_load(mine + k * stage, static_cast<const T*>(p.dy) + r * p.dy_stride, dy_bytes,
+        tc::bulk_load(mine + k * stage, static_cast<const T*>(p.dy) + r * p.dy_stride + base, dy_bytes,
                       full + 8 * k);
         tc::bulk_load(mine + k * stage + dy_bytes, x, x_bytes, full + 8 * k);
         // a row's step bytes are a DRAM access of their own: asked for as early
         if constexpr (kSaved)
-            for (int at = 0; at * kBlockChannels < p.width; at += 128)
+            for (int at = 0; at * kBlockChannels < width; at += 128)
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(p.ckpt.steps +
-                                                              r * p.ckpt.step_stride + at));
+                                                              r * p.ckpt.step_stride +
+                                                              base / kBlockChannels + at));
     };
     int64_t asked = row0;               // the next row to be fetched, by the first thread
     if (tx == 0)
@@ -378,7 +397,8 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
             float v[V];
 #pragma unroll
             for (int k = 0; k < V; ++k) v[k] = 1.0f;
-            if (p.weight && c < p.width) load_params<V>(p.weight, p.param_bf16, p.param_vec, c, v);
+            if (p.weight && c < width)
+                load_params<V>(p.weight, p.param_bf16, p.param_vec, base + c, v);
 #pragma unroll
             for (int k = 0; k < V; ++k) f[i * V + k] = v[k];
         }
@@ -394,7 +414,7 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
         float mean, rstd, step[NV];
     };
     Small now[2], next[2];
-    const uint8_t* steps = kSaved ? p.ckpt.steps + row0 * p.ckpt.step_stride + tx * V / kBlockChannels
+    const uint8_t* steps = kSaved ? p.ckpt.steps + row0 * p.ckpt.step_stride + (base + tx * V) / kBlockChannels
                                   : nullptr;
     const int64_t step_turn = 2 * stride * p.ckpt.step_stride;
     const auto load_small = [&](int64_t r, int j, Small& m) {   // steps: of row r - j * stride
@@ -404,7 +424,7 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
         if constexpr (kSaved) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if ((i * threads + tx) * V < p.width)
+                if ((i * threads + tx) * V < width)
                     m.step[i] = step_value(
                         steps[j * stride * p.ckpt.step_stride + i * threads * V / kBlockChannels]);
         }
@@ -432,10 +452,11 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
     };
 #pragma unroll
     for (int j = 0; j < 2; ++j) load_small(row0 + j * stride, j, now[j]);
-    T* dx = static_cast<T*>(p.dx) + row0 * p.dx_stride + tx * V;
+    T* dx = static_cast<T*>(p.dx) + row0 * p.dx_stride + base + tx * V;
     const int64_t dx_row = stride * p.dx_stride;
     uint32_t k = 0, parity = 0, turns = 0, last = 0;    // `last`: the first stage of the turn before
     int turn = 0;
+    uint32_t sent_parity = 0;
     bool ok = true;
     for (int64_t row = row0; row < p.rows; row += 2 * stride, dx += 2 * dx_row, turn ^= 1) {
         uint32_t at[2];
@@ -451,7 +472,7 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
                 ++turns;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    if ((i * threads + tx) * V >= p.width) continue;
+                    if ((i * threads + tx) * V >= width) continue;
                     F2 d[V / 2], h[V / 2];
                     read(at[j], i, now[j], d, h);
 #pragma unroll
@@ -469,6 +490,20 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
 #pragma unroll
         for (int j = 0; j < 2; ++j) load_small(row + (2 + j) * stride, j, next[j]);
         row_sums4(sums, s[turn]);
+        if constexpr (kPair) {
+            // The other half's sums arrive on this CTA's barrier.  A buffer is
+            // free again two turns on: the other CTA sends those sums after it
+            // has this CTA's of the turn between, which follow all reads here.
+            const uint32_t to = tc::smem_addr(other[turn]), bar = tc::smem_addr(&sent[turn]);
+            if (tx == 0) {
+                tc::mbar_expect(bar, 16);
+                tc::send4(tc::map_to(to, rank ^ 1), sums, tc::map_to(bar, rank ^ 1));
+            }
+            if (ok) ok = tc::mbar_wait(bar, sent_parity);
+            sent_parity ^= uint32_t(turn);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sums[j] = __fadd_rn(sums[j], other[turn][j]);
+        }
         // the whole group is past the turn before: its two stages are free
         if (tx == 0 && row != row0) {
 #pragma unroll
@@ -488,7 +523,7 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
             const F2 r2 = f2(now[j].rstd);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if ((i * threads + tx) * V >= p.width) continue;
+                if ((i * threads + tx) * V >= width) continue;
                 F2 d[V / 2], h[V / 2];
                 read(at[j], i, now[j], d, h);
 #pragma unroll
@@ -514,15 +549,19 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
             const uint32_t uses = turns / p.depth + (uint32_t(j) < turns % p.depth);
             if (uses > 0) tc::mbar_wait(full + 8 * j, (uses - 1) & 1);
         }
+        if constexpr (kPair)    // the last sums sent here, by the buffer of the last turn
+            tc::mbar_wait(tc::smem_addr(&sent[turn ^ 1]), sent_parity ^ uint32_t(turn ^ 1));
     }
     __syncthreads();    // the ring is free: the blocks' sums go through it
-    store_partial<V, NV>(p, dw, db, reinterpret_cast<float*>(ring));
+    if constexpr (kPair) tc::cluster_sync();    // neither CTA leaves while the other may send to it
+    store_partial<V, NV>(p, dw, db, reinterpret_cast<float*>(ring), slice, base, width);
 }
 
-// Two passes (more than 8192 channels): avg(g) and avg(g * xhat) of every row,
-// blockDim.x threads per row.  dy and x are read twice, so 10 bytes an element
-// in bf16 instead of 6: 8192 x 11008 bf16 167 us, 155 us from a checkpoint,
-// about the 132 us that those bytes need.
+// Two passes (more than 16384 channels, or 8192 where rows are not aligned or a
+// CTA's share of four rows is more than its shared memory): avg(g) and avg(g *
+// xhat) of every row, blockDim.x threads per row.  dy and x are read twice, so
+// 10 bytes an element in bf16 instead of 6: 8192 x 11008 bf16 would take 167 us,
+// 155 from a checkpoint, about the 132 us that those bytes need.
 template <typename T, int V, bool kSaved>
 __global__ void __launch_bounds__(256) norm_grad_rows(const __grid_constant__ NormGradParams p) {
     __shared__ float s[2][32][32];
@@ -730,6 +769,28 @@ int staged_depth(int64_t width, int64_t row_bytes) {
     return int(std::min<int64_t>(kMaxDepth, kShared / (groups * row_bytes)));
 }
 
+// Rows of 8193 to 16384 channels: two CTAs of a cluster share a row, the first
+// takes threads * 16 channels of it.
+constexpr int kPairWidth = 16384;
+FusedShape pair_shape(int64_t rows, int64_t width) {
+    return FusedShape{int(round_up(ceil_div(width, 32), 32)), 1, std::min<int64_t>(kSms / 2, rows)};
+}
+
+template <typename T, bool kSaved>
+cudaError_t launch_pairs(NormGradParams& p, cudaStream_t s) {
+    const FusedShape f = pair_shape(p.rows, p.width);
+    const size_t row_bytes = size_t(f.threads) * 16 * (sizeof(T) + (kSaved ? 1 : sizeof(T)));
+    p.slices = int(f.blocks);
+    p.depth = int(std::min<int64_t>(kMaxDepth, kShared / int64_t(row_bytes)));
+    const void* k = (const void*)norm_grad_staged<T, kSaved, true>;
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_shared_memory(k, int(kShared), &allowed);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&p};
+    return launch_grid(k, dim3(unsigned(2 * f.blocks)), dim3(f.threads), p.depth * row_bytes, args,
+                       s, 2);
+}
+
 template <typename T, bool kSaved>
 cudaError_t launch_staged(NormGradParams& p, int depth, cudaStream_t s) {
     const FusedShape f = fused_shape(p.rows, p.width, 16, 1);
@@ -737,7 +798,7 @@ cudaError_t launch_staged(NormGradParams& p, int depth, cudaStream_t s) {
     p.depth = depth;
     const size_t sums = size_t(f.per_block - 1) * 2 * f.threads * 16 * 4;
     const size_t rows = size_t(f.per_block) * depth * p.width * (sizeof(T) + (kSaved ? 1 : sizeof(T)));
-    const void* k = (const void*)norm_grad_staged<T, kSaved>;
+    const void* k = (const void*)norm_grad_staged<T, kSaved, false>;
     static std::atomic<uint64_t> allowed{0};   // of this kernel: one per instantiation
     const cudaError_t e = allow_shared_memory(k, int(kShared), &allowed);
     if (e != cudaSuccess) return e;
@@ -756,6 +817,15 @@ cudaError_t launch_source(NormGradParams& p, cudaStream_t s) {
         if (depth >= 4 && !saved) return launch_staged<T, false>(p, depth, s);
         if (depth >= 4 && p.width % 16 == 0 && rows_aligned(p.ckpt.codes, p.ckpt.code_stride, 1, 16))
             return launch_staged<T, true>(p, depth, s);
+    }
+    if (V > 1 && p.width > kFusedWidth && p.width <= kPairWidth) {
+        const bool saved = p.ckpt.codes != nullptr;
+        const int64_t row_bytes = int64_t(pair_shape(p.rows, p.width).threads) * 16 *
+                                  int64_t(sizeof(T) + (saved ? 1 : sizeof(T)));
+        const bool fits = 4 * row_bytes <= kShared;
+        if (fits && !saved) return launch_pairs<T, false>(p, s);
+        if (fits && p.width % 16 == 0 && rows_aligned(p.ckpt.codes, p.ckpt.code_stride, 1, 16))
+            return launch_pairs<T, true>(p, s);
     }
     return p.ckpt.codes ? launch_backward<T, V, true>(p, s) : launch_backward<T, V, false>(p, s);
 }
@@ -779,6 +849,8 @@ dpr_status dpr_layernorm_backward_workspace(int64_t rows, int64_t width, int64_t
                            fused_shape(rows, width, 8, 1).blocks,
                            fused_shape(rows, width, 1, 16).blocks});
         sums = 0;
+    } else if (width <= kPairWidth) {
+        slices = std::max(slices, pair_shape(rows, width).blocks);
     }
     *bytes = sums + slices * 2 * round_up(width, 4) * 4;
     return DPR_OK;

@@ -8,18 +8,25 @@
 namespace dpr {
 
 cudaError_t launch_grid(const void* kernel, dim3 grid, dim3 block, size_t smem, void** args,
-                        cudaStream_t s) {
+                        cudaStream_t s, int cluster) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    if (cluster > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(cluster);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
     const bool legacy = s == nullptr || s == cudaStreamLegacy || s == cudaStreamPerThread;
     cfg.attrs = attr;
-    cfg.numAttrs = (!legacy && programmatic_launch_enabled()) ? 1 : 0;
+    if (!legacy && programmatic_launch_enabled()) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
     return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 

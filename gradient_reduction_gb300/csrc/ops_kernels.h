@@ -13,8 +13,9 @@
 namespace dpr {
 
 // As launch_kernel, with a block shape and dynamic shared memory.
+// `cluster`: consecutive blocks that form a cluster (a divisor of grid.x).
 cudaError_t launch_grid(const void* kernel, dim3 grid, dim3 block, size_t smem, void** args,
-                        cudaStream_t s);
+                        cudaStream_t s, int cluster = 1);
 
 bool programmatic_launch_enabled();   // defined beside launch_kernel
 
