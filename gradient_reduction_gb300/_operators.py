@@ -15,7 +15,7 @@ import threading
 
 import torch
 
-from ._binding import _check, _stream, lib
+from ._binding import _check, _raw_stream, _stream, lib
 
 CHECKPOINT_BLOCK = 32            # channels that share a step
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -70,6 +70,13 @@ def _device(t: torch.Tensor, what: str) -> int:
     if dev < 0 or dev != _get_device():
         _wrong_device(t, what)
     return dev
+
+
+def _handle(stream, dev: int) -> int:
+    """The handle of `stream`; without one, of the current device's current stream."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def _matrix(t: torch.Tensor, what: str, dev: int):
@@ -174,7 +181,7 @@ _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
                      torch.cuda.is_current_stream_capturing)
 
 
-def _workspace(t, nbytes: int, stream, dev: int):
+def _workspace(t, nbytes: int, stream, handle: int, dev: int):
     """The caller's scratch memory, or some of PyTorch's: kept between calls on
     the current stream, except inside a graph capture, whose memory has to be
     the graph's own.  For another stream it is allocated there, so that it is
@@ -190,7 +197,7 @@ def _workspace(t, nbytes: int, stream, dev: int):
     if stream is None:
         if nbytes > _KEEP_BYTES or _capturing():
             return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-        key = (dev, _stream(None))
+        key = (dev, handle)
         t = _scratch.kept.get(key)
         if t is None or t.numel() < nbytes:
             t = _scratch.kept[key] = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
@@ -223,7 +230,7 @@ def dpr_layernorm_forward(x: torch.Tensor, weight, bias, eps: float, y: torch.Te
         px, sx, rows, width, _code(x, "x"), _vector(weight, width, "weight", dev),
         _vector(bias, width, "bias", dev), _pair_code(weight, bias, "weight and bias"), eps, py, sy,
         _statistic(mean, rows, "mean", dev), _statistic(rstd, rows, "rstd", dev), cx, cy,
-        _stream(stream))
+        _handle(stream, dev))
     if st:
         _check("dpr_layernorm_forward", st)
 
@@ -254,13 +261,14 @@ def dpr_layernorm_backward(dy: torch.Tensor, x, weight, mean: torch.Tensor, rstd
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward pass are needed")
     nbytes = _workspace_bytes("dpr_layernorm_backward_workspace", rows, width)
-    ws = _workspace(workspace, nbytes, stream, dev)
+    handle = _handle(stream, dev)
+    ws = _workspace(workspace, nbytes, stream, handle, dev)
     st = lib().dpr_layernorm_backward(
         pd, sd, px, sx, ref, rows, width, _code(dy, "dy"), _vector(weight, width, "weight", dev),
         0 if weight is None else _code(weight, "weight"), _statistic(mean, rows, "mean", dev),
         _statistic(rstd, rows, "rstd", dev), po, so, _vector(dweight, width, "dweight", dev),
         _vector(dbias, width, "dbias", dev), _pair_code(dweight, dbias, "dweight and dbias"),
-        1 if accumulate else 0, 0 if ws is None else ws.data_ptr(), nbytes, _stream(stream))
+        1 if accumulate else 0, 0 if ws is None else ws.data_ptr(), nbytes, handle)
     if st:
         _check("dpr_layernorm_backward", st)
 
@@ -271,7 +279,7 @@ def dpr_checkpoint_save(x: torch.Tensor, checkpoint: Checkpoint, stream=None) ->
     px, rows, width, sx = _matrix(x, "x", dev)
     arg = _checkpoint_arg(checkpoint, "checkpoint", rows, width, dev)
     st = lib().dpr_checkpoint_save(px, sx, rows, width, _code(x, "x"), ctypes.byref(arg),
-                                   _stream(stream))
+                                   _handle(stream, dev))
     if st:
         _check("dpr_checkpoint_save", st)
 
@@ -282,7 +290,7 @@ def dpr_checkpoint_load(checkpoint: Checkpoint, out: torch.Tensor, stream=None) 
     po, rows, width, so = _matrix(out, "out", dev)
     arg = _checkpoint_arg(checkpoint, "checkpoint", rows, width, dev)
     st = lib().dpr_checkpoint_load(ctypes.byref(arg), rows, width, po, so, _code(out, "out"),
-                                   _stream(stream))
+                                   _handle(stream, dev))
     if st:
         _check("dpr_checkpoint_load", st)
 
@@ -309,10 +317,11 @@ def dpr_linear_weight_grad(dy: torch.Tensor, x_checkpoint: Checkpoint, dweight: 
     if st:
         _check("dpr_linear_weight_grad", st)
     nbytes = need.value
-    ws = _workspace(workspace, nbytes, stream, dev)
+    handle = _handle(stream, dev)
+    ws = _workspace(workspace, nbytes, stream, handle, dev)
     st = L.dpr_linear_weight_grad(
         pd, sd, ref, rows, out_features, in_features, pw, sw, _code(dweight, "dweight"),
-        1 if accumulate else 0, 0 if ws is None else ws.data_ptr(), nbytes, _stream(stream))
+        1 if accumulate else 0, 0 if ws is None else ws.data_ptr(), nbytes, handle)
     if st:
         _check("dpr_linear_weight_grad", st)
 

@@ -280,7 +280,12 @@ __global__ void __launch_bounds__(1024) norm_long_rows(const __grid_constant__ N
 }
 
 constexpr int kBlock = 128;              // threads of a block, or one row's if more
-constexpr int kBlockAny = 256;           // the same for single elements
+// The same for single elements: a block lives for one row each of its threads,
+// and with smaller blocks starting them takes the time (16384 x 1001 bf16 in
+// blocks of 128, 256 and 512: 51, 32 and 27 us); the checkpoints' registers leave
+// room for fewer of the large ones (100, 64 and 66 us).
+constexpr int kBlockAny = 512;
+constexpr int kBlockAnyCkpt = 256;
 template <typename T, int V, int NV>
 cudaError_t launch_rows(const NormParams& p, cudaStream_t s) {
     const RowShape f = row_shape(p.width, V * NV, kBlockChannels / V, kBlock);
@@ -296,9 +301,10 @@ cudaError_t launch_rows(const NormParams& p, cudaStream_t s) {
 
 template <typename T, int NV>
 cudaError_t launch_rows_any(const NormParams& p, cudaStream_t s) {
-    const RowShape f = row_shape(p.width, NV, 32, kBlockAny);
-    const void* k = p.x_ckpt.codes || p.y_ckpt.codes ? (const void*)norm_rows_any<T, NV, true>
-                                                     : (const void*)norm_rows_any<T, NV, false>;
+    const bool ckpt = p.x_ckpt.codes || p.y_ckpt.codes;
+    const RowShape f = row_shape(p.width, NV, 32, ckpt ? kBlockAnyCkpt : kBlockAny);
+    const void* k = ckpt ? (const void*)norm_rows_any<T, NV, true>
+                         : (const void*)norm_rows_any<T, NV, false>;
     void* args[] = {const_cast<NormParams*>(&p)};
     return launch_grid(k, dim3(unsigned(ceil_div(p.rows, f.per_block))),
                        dim3(f.threads, f.per_block), 0, args, s);
@@ -330,6 +336,8 @@ cudaError_t launch_forward(const NormParams& p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_forward_any(const NormParams& p, cudaStream_t s) {
+    // few rows: more threads for each (300 x 1003 fp32 3.5 -> 2.7 us; 3001 rows 8.6 -> 9.8)
+    if (p.width <= 1024 * 4 && p.rows * p.width < (1 << 19)) return launch_rows_any<T, 4>(p, s);
     if (p.width <= 1024 * 8) return launch_rows_any<T, 8>(p, s);
     if (p.width <= 1024 * 16) return launch_rows_any<T, 16>(p, s);
     return launch_long<T, 1>(p, s);

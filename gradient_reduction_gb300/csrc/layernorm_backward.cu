@@ -749,9 +749,12 @@ cudaError_t launch_backward(NormGradParams& p, cudaStream_t s) {
             return p.width <= 4096 ? launch_fused<T, 8, 1, kSaved>(p, s)
                                    : launch_fused<T, 8, 2, kSaved>(p, s);
         else if constexpr (V == 8) return launch_fused<T, 8, 2, kSaved>(p, s);
-        else
-            return p.width <= 128 ? launch_fused<T, 1, 4, kSaved>(p, s)
-                                  : launch_fused<T, 1, 16, kSaved>(p, s);
+        // 16 single elements a thread spill, more so with codes and steps to hold:
+        // 16384 x 1001 bf16 with 8 and 16: 40 and 32 us, from a checkpoint 35 and 49;
+        // 9000 x 205: 9.4 and 10.6 us, 9.3 and 15
+        else if (p.width <= 128) return launch_fused<T, 1, 4, kSaved>(p, s);
+        else if (p.width <= (kSaved ? 4096 : 256)) return launch_fused<T, 1, 8, kSaved>(p, s);
+        else return launch_fused<T, 1, 16, kSaved>(p, s);
     }
     p.slices = slice_count(p.rows, p.width);
     p.slice_rows = ceil_div(p.rows, p.slices);
@@ -855,6 +858,8 @@ dpr_status dpr_layernorm_backward_workspace(int64_t rows, int64_t width, int64_t
     if (width <= kFusedWidth) {
         slices = std::max({fused_shape(rows, width, 16, 1).blocks,
                            fused_shape(rows, width, 8, 1).blocks,
+                           fused_shape(rows, width, 1, 4).blocks,
+                           fused_shape(rows, width, 1, 8).blocks,
                            fused_shape(rows, width, 1, 16).blocks});
         sums = 0;
     } else if (width <= kPairWidth) {
