@@ -149,8 +149,10 @@ __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormPar
 
 // Single elements: as above, one row (or blockDim.y of them) per block, NV
 // elements a thread in registers, at fixed distances (own_channel).  3001 x
-// 1003 fp32: 8.7 us, 2.8 TB/s; 16384 x 1001 bf16: 32 us, bound by its loads and
-// stores of single elements.
+// 1003 fp32: 7.1 us, 3.4 TB/s; 16384 x 1001 bf16: 27 us, bound by its loads and
+// stores of single elements (64 us with both checkpoints, by quantising them).
+// A persistent loop is slower (34 us): a block that ends makes room at once for
+// one whose loads overlap the others' sums.
 template <typename T, int NV, bool kCkpt>
 __global__ void __launch_bounds__(1024) norm_rows_any(const __grid_constant__ NormParams p) {
     __shared__ float s[2][8][32];

@@ -179,9 +179,9 @@ __device__ __forceinline__ void store_partial(const NormGradParams& p, F2 (&dw)[
 
 // One pass: blockDim.x threads (see row_sum; at most 512) share a row, NV
 // vectors of V channels each; blockDim.y rows at a time per block, the blocks'
-// rows interleaved.  65536 x 128 bf16: 13 us, from a checkpoint 14 us (floors 7.4
-// and 6.2); 16384 x 8192 fp32: 250 us, 6.4 TB/s; single elements, 3001 x 1003
-// fp32: 14.4 us with the join, 16384 x 1001 bf16: 33 us.
+// rows interleaved.  With the join: 65536 x 128 bf16 10.4 us, from a checkpoint
+// 12.2 us (floors 7.4 and 6.2); 16384 x 8192 fp32 256 us, 6.3 TB/s; single
+// elements, 3001 x 1003 fp32 10.7 us, 16384 x 1001 bf16 32 us.
 template <typename T, int V, int NV, bool kSaved>
 __global__ void __launch_bounds__(512) norm_grad_fused(const __grid_constant__ NormGradParams p) {
     constexpr int E = V * NV;
@@ -328,14 +328,14 @@ __device__ __forceinline__ void row_sums4(float (&v)[4], float (*s)[16][4]) {
 // twice, for the sums and for the rest, which leaves the registers to the
 // column sums.  A thread owns 16 channels in 16-byte pieces, piece i at
 // i * blockDim.x + threadIdx.x, which neighbours read without bank conflicts.
-// 16384 x 4096 bf16 with the join: 70 us, 5.7 TB/s (0.84 of the measured copy
+// 16384 x 4096 bf16 with the join: 69 us, 5.8 TB/s (0.86 of the measured copy
 // rate); from a checkpoint 84 us, 4.0 TB/s, where restoring the codes twice
-// makes instructions the bound (418 a warp and row against 333; 57% of the
+// makes instructions the bound (405 a warp and row against 333; 57% of the
 // issue slots, at 16 warps an SM that its 128 registers allow).  One row a turn
 // in registers: 76 and 83 us; 8 channels a thread: 125 and 134 us; deeper
 // staging or loads asked for earlier: no difference.
 // kPair: a row to two CTAs of a cluster, which send each other their half's
-// four sums.  8192 x 11008 bf16: 117 us (two passes: 166), from a checkpoint 138
+// four sums.  8192 x 11008 bf16: 116 us (two passes: 166), from a checkpoint 138
 // (154); 8192 x 12288: 117 and 144 us, 8192 x 12288 fp32: 206 us, 5.9 TB/s.  A
 // turn waits once for the other CTA, with one CTA an SM to fill the gap.
 template <typename T, bool kSaved, bool kPair>
