@@ -20,7 +20,7 @@ namespace {
 // Both directions stream at the rate of memory: 16384 x 4096 bf16 is saved in
 // 29.5 us (6.9 TB/s of 2 + 1 + 1/32 bytes an element) and restored in 30.4 us;
 // 8192 x 11008 in 40.0 and 42.1 us.  Single elements (odd rows): 16384 x 1001 bf16
-// in 18.1 and 13.8 us, bound by one-element accesses.
+// in 13.1 and 13.8 us, bound by one-element accesses.
 //
 // blockDim.x threads along a row (a multiple of the lanes that hold a block
 // of channels, so that its peak is found within a warp), NV vectors of V

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(512) norm_rows(const __grid_constant__ NormPar
 // Single elements: as above, one row (or blockDim.y of them) per block, NV
 // elements a thread in registers, at fixed distances (own_channel).  3001 x
 // 1003 fp32: 7.1 us, 3.4 TB/s; 16384 x 1001 bf16: 27 us, bound by its loads and
-// stores of single elements (64 us with both checkpoints, by quantising them).
+// stores of single elements (54 us with both checkpoints, by quantising them).
 // A persistent loop is slower (34 us): a block that ends makes room at once for
 // one whose loads overlap the others' sums.
 template <typename T, int NV, bool kCkpt>
@@ -285,7 +285,7 @@ constexpr int kBlock = 128;              // threads of a block, or one row's if 
 // The same for single elements: a block lives for one row each of its threads,
 // and with smaller blocks starting them takes the time (16384 x 1001 bf16 in
 // blocks of 128, 256 and 512: 51, 32 and 27 us); the checkpoints' registers leave
-// room for fewer of the large ones (100, 64 and 66 us).
+// room for fewer of the large ones (100, 64 and 66 us when a checkpoint took more instructions).
 constexpr int kBlockAny = 512;
 constexpr int kBlockAnyCkpt = 256;
 template <typename T, int V, int NV>
