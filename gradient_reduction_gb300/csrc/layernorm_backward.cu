@@ -8,7 +8,7 @@
 // registers a row ahead (norm_grad_fused), the others staged in shared memory
 // (norm_grad_staged; fp32 rows too large for that, in registers).  Rows of up
 // to 16384 channels whose parts are aligned take the staged kernel too, a row
-// to two CTAs of a cluster.  All others take two passes, row sums first, then
+// to two CTAs of a cluster, and so do some shorter ones (in_pairs).  All others take two passes, row sums first, then
 // columns.
 #include <algorithm>
 
@@ -328,8 +328,8 @@ __device__ __forceinline__ void row_sums4(float (&v)[4], float (*s)[16][4]) {
 // twice, for the sums and for the rest, which leaves the registers to the
 // column sums.  A thread owns 16 channels in 16-byte pieces, piece i at
 // i * blockDim.x + threadIdx.x, which neighbours read without bank conflicts.
-// 16384 x 4096 bf16 with the join: 69 us, 5.8 TB/s (0.86 of the measured copy
-// rate); from a checkpoint 84 us, 4.0 TB/s, where restoring the codes twice
+// 16384 x 4096 bf16 with the join: 68 us, 5.9 TB/s (0.87 of the measured copy
+// rate); from a checkpoint 82 us, 4.1 TB/s, where restoring the codes twice
 // makes instructions the bound (405 a warp and row against 333; 57% of the
 // issue slots, at 16 warps an SM that its 128 registers allow).  One row a turn
 // in registers: 76 and 83 us; 8 channels a thread: 125 and 134 us; deeper
@@ -780,19 +780,33 @@ int staged_depth(int64_t width, int64_t row_bytes) {
     return int(std::min<int64_t>(kMaxDepth, kShared / (groups * row_bytes)));
 }
 
-// Rows of 8193 to 16384 channels: two CTAs of a cluster share a row, the first
-// takes threads * 16 channels of it.
+// Two CTAs of a cluster share a row, the first takes threads * 16 channels of
+// it: rows of 8193 to 16384 channels, and many rows of 4097 to 5120, of which one
+// CTA an SM would leave over a third of the threads idle, while three halves fit
+// (8192 x 5120 bf16: 56 -> 52 us, from a checkpoint 69 -> 59; 1000 rows 13.7 -> 14.5,
+// 15.2 -> 15.1; 300 rows 9.0 -> 10.9, by the slices to be joined).
 constexpr int kPairWidth = 16384;
+bool in_pairs(int64_t rows, int64_t width) {
+    return (width > kFusedWidth && width <= kPairWidth) ||
+           (width > 4096 && width <= 5120 && rows >= 2048);
+}
 FusedShape pair_shape(int64_t rows, int64_t width) {
-    return FusedShape{int(round_up(ceil_div(width, 32), 32)), 1, std::min<int64_t>(kSms / 2, rows)};
+    const int threads = int(round_up(ceil_div(width, 32), 32));
+    return FusedShape{threads, 1, std::min<int64_t>(kSms * (512 / threads) / 2, rows)};
+}
+int pair_depth(int64_t width, int64_t element_bytes) {
+    const int threads = pair_shape(1, width).threads;
+    return int(std::min<int64_t>(kMaxDepth, kShared / (512 / threads) /
+                                                (int64_t(threads) * 16 * element_bytes)));
 }
 
 template <typename T, bool kSaved>
 cudaError_t launch_pairs(NormGradParams& p, cudaStream_t s) {
     const FusedShape f = pair_shape(p.rows, p.width);
-    const size_t row_bytes = size_t(f.threads) * 16 * (sizeof(T) + (kSaved ? 1 : sizeof(T)));
+    const size_t element_bytes = sizeof(T) + (kSaved ? 1 : sizeof(T));
+    const size_t row_bytes = size_t(f.threads) * 16 * element_bytes;
     p.slices = int(f.blocks);
-    p.depth = int(std::min<int64_t>(kMaxDepth, kShared / int64_t(row_bytes)));
+    p.depth = pair_depth(p.width, element_bytes);
     const void* k = (const void*)norm_grad_staged<T, kSaved, true>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_shared_memory(k, int(kShared), &allowed);
@@ -827,6 +841,13 @@ cudaError_t launch_staged(NormGradParams& p, int depth, cudaStream_t s) {
 
 template <typename T, int V>
 cudaError_t launch_source(NormGradParams& p, cudaStream_t s) {
+    if (V > 1 && in_pairs(p.rows, p.width)) {
+        const bool saved = p.ckpt.codes != nullptr;
+        const bool fits = pair_depth(p.width, sizeof(T) + (saved ? 1 : sizeof(T))) >= 4;
+        if (fits && !saved) return launch_pairs<T, false>(p, s);
+        if (fits && p.width % 16 == 0 && rows_aligned(p.ckpt.codes, p.ckpt.code_stride, 1, 16))
+            return launch_pairs<T, true>(p, s);
+    }
     // bulk copies take whole 16-byte pieces; more than 512 channels are at least
     // 64 threads a row, so at most the 4 groups a block that the kernel has room for
     if (V > 1 && p.width > 512 && p.width <= kFusedWidth) {
@@ -835,15 +856,6 @@ cudaError_t launch_source(NormGradParams& p, cudaStream_t s) {
         if (depth >= 4 && !saved) return launch_staged<T, false>(p, depth, s);
         if (depth >= 4 && p.width % 16 == 0 && rows_aligned(p.ckpt.codes, p.ckpt.code_stride, 1, 16))
             return launch_staged<T, true>(p, depth, s);
-    }
-    if (V > 1 && p.width > kFusedWidth && p.width <= kPairWidth) {
-        const bool saved = p.ckpt.codes != nullptr;
-        const int64_t row_bytes = int64_t(pair_shape(p.rows, p.width).threads) * 16 *
-                                  int64_t(sizeof(T) + (saved ? 1 : sizeof(T)));
-        const bool fits = 4 * row_bytes <= kShared;
-        if (fits && !saved) return launch_pairs<T, false>(p, s);
-        if (fits && p.width % 16 == 0 && rows_aligned(p.ckpt.codes, p.ckpt.code_stride, 1, 16))
-            return launch_pairs<T, true>(p, s);
     }
     return p.ckpt.codes ? launch_backward<T, V, true>(p, s) : launch_backward<T, V, false>(p, s);
 }
@@ -869,9 +881,8 @@ dpr_status dpr_layernorm_backward_workspace(int64_t rows, int64_t width, int64_t
                            fused_shape(rows, width, 1, 8).blocks,
                            fused_shape(rows, width, 1, 16).blocks});
         sums = 0;
-    } else if (width <= kPairWidth) {
-        slices = std::max(slices, pair_shape(rows, width).blocks);
     }
+    if (in_pairs(rows, width)) slices = std::max(slices, pair_shape(rows, width).blocks);
     *bytes = sums + slices * 2 * round_up(width, 4) * 4;
     return DPR_OK;
 }

@@ -231,7 +231,7 @@ def test_norm_at_the_edges_of_the_rules(width, dtype):
 
 
 @pytest.mark.parametrize("rows,width", [(1300, 528), (2500, 1024), (700, 4096), (900, 8192),
-                                        (600, 8208), (500, 11008), (310, 16384), (155, 24576),
+                                        (600, 8208), (500, 11008), (2200, 4128), (2048, 5120), (310, 16384), (155, 24576),
                                         (4000, 64), (1250, 16), (9000, 8)])
 def test_norm_many_rows_per_block(rows, width):
     """Several rows to every block of the GPU: loops, rings and prefetches go round."""
