@@ -203,7 +203,11 @@ def _workspace(t, nbytes: int, stream, handle: int, dev: int):
             t = _scratch.kept[key] = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
         return t
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # 0 and 1 (cudaStreamLegacy) are the default stream; ExternalStream makes a new
+        # stream of PyTorch's pool of 0, and memory freed there would be handed out again
+        # while the default stream still uses it, and takes no 1
+        stream = (torch.cuda.default_stream(dev) if int(stream) in (0, 1)
+                  else torch.cuda.ExternalStream(int(stream)))
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
