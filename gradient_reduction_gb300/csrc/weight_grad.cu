@@ -534,11 +534,12 @@ weight_grad_join(const __grid_constant__ WeightGradParams p, int pairs) {
 }
 
 // Rows copied to 16-byte-aligned ones, for inputs that TMA cannot read; four
-// loads of a thread in flight before its stores.
+// loads of a thread in flight before its stores.  The source is not declared
+// __restrict__: that allows loads that take memory to be unchanged as long as the
+// kernel lives, and a programmatic launch lives while the grid before it writes.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-repack_rows(const T* __restrict__ from, int64_t from_stride, T* __restrict__ to, int64_t to_stride,
-            int64_t rows, int width) {
+repack_rows(const T* from, int64_t from_stride, T* to, int64_t to_stride, int64_t rows, int width) {
     grid_wait();
     grid_release();
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {

@@ -53,3 +53,45 @@ def test_calls_on_the_default_stream_by_its_handle(handle):
 
     for got, want in zip(call(handle), call(None)):
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("programmatic", [True, False])
+def test_unaligned_inputs_rewritten_before_every_weight_gradient(programmatic):
+    """dy, codes and steps of odd strides, which are first copied to aligned rows, rewritten by the
+    call just before (dx and the checkpoints of a layer norm, other values each time) on a side
+    stream without waits: every weight gradient is of the values it was called with."""
+    H.device()
+    rows, o, i, turns = 300, 100, 97, 8
+    old = dpr.dpr_set_programmatic_launch(programmatic)
+    try:
+        g = torch.Generator().manual_seed(3)
+        xs = [torch.randn(rows, i, generator=g).bfloat16().cuda() for _ in range(turns)]
+        dys = [torch.randn(rows, o, generator=g).bfloat16().cuda() for _ in range(turns)]
+        mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+        codes = torch.zeros(rows, i + 2, dtype=torch.int8, device="cuda")
+        steps = torch.zeros(rows, 4 + 3, dtype=torch.uint8, device="cuda")
+        saved = dpr.Checkpoint(codes[:, :i], steps[:, :4])
+        dx = torch.zeros(rows, o + 1, dtype=torch.bfloat16, device="cuda")[:, :o]
+
+        def step(k, out, stream):
+            dpr.dpr_checkpoint_save(xs[k], saved, stream=stream)
+            dpr.dpr_layernorm_backward(dys[k], dys[k], None, mean, rstd, dx, stream=stream)
+            dpr.dpr_linear_weight_grad(dx, saved, out, stream=stream)
+
+        want = []
+        for k in range(turns):
+            out = torch.full((o, i), float("nan"), device="cuda")
+            step(k, out, None)
+            torch.cuda.synchronize()
+            want.append(out)
+        side = torch.cuda.Stream()
+        got = [torch.full((o, i), float("nan"), device="cuda") for _ in range(turns)]
+        torch.cuda.synchronize()
+        for k in range(turns):
+            step(k, got[k], side)
+        torch.cuda.synchronize()
+        for k in range(turns):
+            assert torch.equal(got[k], want[k]), k
+            assert k == 0 or not torch.equal(got[k], got[k - 1])
+    finally:
+        dpr.dpr_set_programmatic_launch(old)

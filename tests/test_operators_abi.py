@@ -233,3 +233,15 @@ def test_format_by_hand():
     codes, steps = R.encode(x)
     assert int(steps[0, 0]) == 255 and not codes.any()
     assert R.decode(codes, steps).isnan().all()
+
+
+def test_no_kernel_takes_a_buffer_as_unchanging():
+    """The kernels are programmatic launches: they are resident while the grid before them still
+    writes what they will read, so no buffer may be read through the non-coherent path, which
+    __restrict__ on a source, __ldg and ld.global.nc allow or ask for."""
+    csrc = os.path.join(ROOT, "gradient_reduction_gb300", "csrc")
+    for name in ("checkpoint.cu", "layernorm.cu", "layernorm_backward.cu", "ops_device.cuh",
+                 "ops_host.cu", "tensor_core.cuh", "weight_grad.cu"):
+        code = re.sub(r"//.*", "", open(os.path.join(csrc, name)).read())
+        for word in ("__restrict__", "__ldg", "global.nc", "ld_nc_", "load_words<"):
+            assert word not in code, f"{name}: {word}"
