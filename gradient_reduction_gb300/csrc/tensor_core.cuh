@@ -1,6 +1,6 @@
 // PTX of asynchronous loads and of the Blackwell tensor-core path: mbarriers
-// with bounded waits, TMA tile loads and bulk copies, tcgen05 matrix instructions over a pair of CTAs (cta_group::2)
-// with their accumulators in tensor memory.
+// with bounded waits, TMA tile loads and bulk copies, tcgen05 matrix instructions
+// over a pair of CTAs (cta_group::2) with their accumulators in tensor memory.
 #pragma once
 
 #include <cstdint>
@@ -70,11 +70,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
                  : "memory");
 }
 
-// Waits until the phase of `parity` has completed.  Gives up after 2^24
-// polls (about a second at the least), far beyond any wait of a working
-// kernel, and returns false.
+// Waits until the phase of `parity` has completed.  Gives up after 2^19 tries,
+// far beyond any wait of a working kernel, and returns false.  PTX leaves open
+// how long a try that fails holds the thread: 20 ns to 7800 cycles on a GB300,
+// by the code around it, so a wait ends after 10 ms at the earliest and two to
+// three seconds at the latest.  (A limit by the clock took 1 to 5% of the time of
+// the kernels that wait.)
+constexpr uint32_t kWaitTries = 1u << 19;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < (1u << 24); ++i) {
+    for (uint32_t i = 0; i < kWaitTries; ++i) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
