@@ -384,9 +384,10 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
                                                               r * p.ckpt.step_stride +
                                                               base / kBlockChannels + at));
     };
-    int64_t asked = row0;               // the next row to be fetched, by the first thread
+    uint32_t asked = 0;                 // rows fetched so far, by the first thread
     if (tx == 0)
-        for (int k = 0; k < p.depth && asked < p.rows; ++k, asked += stride) fetch(asked, k);
+        for (; asked < uint32_t(p.depth) && row0 + asked * stride < p.rows; ++asked)
+            fetch(row0 + asked * stride, asked);
 
     F2 w[E / 2], dw[E / 2], db[E / 2];
     {
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
     for (int j = 0; j < 2; ++j) load_small(row0 + j * stride, j, now[j]);
     T* dx = static_cast<T*>(p.dx) + row0 * p.dx_stride + base + tx * V;
     const int64_t dx_row = stride * p.dx_stride;
-    uint32_t k = 0, parity = 0, turns = 0, last = 0;    // `last`: the first stage of the turn before
+    uint32_t k = 0, parity = 0, last = 0;    // `last`: the first stage of the turn before
     int turn = 0;
     uint32_t sent_parity = 0;
     bool ok = true;
@@ -469,7 +470,6 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
             if (row + j * stride < p.rows) {
                 if (ok) ok = tc::mbar_wait(full + 8 * k, parity);
                 if (++k == uint32_t(p.depth)) { k = 0; parity ^= 1; }
-                ++turns;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     if ((i * threads + tx) * V >= width) continue;
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
             // free again two turns on: the other CTA sends those sums after it
             // has this CTA's of the turn between, which follow all reads here.
             const uint32_t to = tc::smem_addr(other[turn]), bar = tc::smem_addr(&sent[turn]);
-            if (tx == 0) {
+            if (tx == 0 && ok) {
                 tc::mbar_expect(bar, 16);
                 tc::send4(tc::map_to(to, rank ^ 1), sums, tc::map_to(bar, rank ^ 1));
             }
@@ -504,13 +504,14 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
 #pragma unroll
             for (int j = 0; j < 4; ++j) sums[j] = __fadd_rn(sums[j], other[turn][j]);
         }
-        // the whole group is past the turn before: its two stages are free
-        if (tx == 0 && row != row0) {
+        // the whole group is past the turn before: its two stages are free (after a
+        // failed wait they are not known to be)
+        if (tx == 0 && ok && row != row0) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (asked < p.rows) {
-                    fetch(asked, last);
-                    asked += stride;
+                if (row0 + asked * stride < p.rows) {
+                    fetch(row0 + asked * stride, last);
+                    ++asked;
                     if (++last == uint32_t(p.depth)) last = 0;
                 }
         }
@@ -542,18 +543,27 @@ __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ 
 #pragma unroll
         for (int j = 0; j < 2; ++j) now[j] = next[j];
     }
-    if (!ok && tx == 0) {
-        // a wait ran out: count it, and let what is still in flight land first
-        atomicAdd(&g_wait_failures, 1u);
-        for (int j = 0; j < p.depth; ++j) {
-            const uint32_t uses = turns / p.depth + (uint32_t(j) < turns % p.depth);
-            if (uses > 0) tc::mbar_wait(full + 8 * j, (uses - 1) & 1);
+    // One thread's wait may run out where the others' end, so the block counts it
+    // as one, and lets what it has asked for land before the ring's memory is used
+    // again or given up.
+    const bool failed = __syncthreads_or(!ok);
+    if (failed) {
+        if (tx == 0) {
+            if (threadIdx.y == 0) atomicAdd(&g_wait_failures, 1u);
+            for (int j = 0; j < p.depth; ++j) {
+                const uint32_t uses = asked / p.depth + (uint32_t(j) < asked % p.depth);
+                if (uses > 0) tc::mbar_wait(full + 8 * j, (uses - 1) & 1);
+            }
         }
-        if constexpr (kPair)    // the last sums sent here, by the buffer of the last turn
-            tc::mbar_wait(tc::smem_addr(&sent[turn ^ 1]), sent_parity ^ uint32_t(turn ^ 1));
+        __syncthreads();
     }
-    __syncthreads();    // the ring is free: the blocks' sums go through it
-    if constexpr (kPair) tc::cluster_sync();    // neither CTA leaves while the other may send to it
+    if constexpr (kPair) {
+        tc::cluster_sync();    // neither CTA leaves while the other may send to it
+        if (failed) {          // sums sent here that no wait has seen: some 50 us to land
+            const long long start = clock64();
+            while (clock64() - start < 100000) {}
+        }
+    }
     store_partial<V, NV>(p, dw, db, reinterpret_cast<float*>(ring), slice, base, width);
 }
 

@@ -32,3 +32,12 @@ def test_a_wait_ends_by_itself(tmp_path):
     for _, late, _, ms in lines:
         assert float(ms) < (1000 if late == "1" else 4500), lines
         assert late == "1" or float(ms) > 5, lines
+
+
+def test_a_wait_that_runs_out_in_any_thread_is_counted(tmp_path):
+    """The block of the thread counts it once; where the first thread of two CTAs' row gives up, the
+    other CTA gets no more sums and counts too.  The next call is as if nothing had been."""
+    lines = dict(_run(tmp_path, "staged_waits"))
+    assert lines == {"none": "0", "thread": "1", "first-thread": "1", "pair-load": "1",
+                     "pair-sums": "1", "first-thread-of-many": "1",
+                     "first-thread-of-many-pairs": "2"}
