@@ -331,8 +331,8 @@ def dpr_linear_weight_grad(dy: torch.Tensor, x_checkpoint: Checkpoint, dweight: 
 
 
 def dpr_device_wait_failures() -> int:
-    """Waits inside the operators' kernels that have run out (0 in working
-    order); waits for the device."""
+    """How often a wait inside the operators' kernels has run out (0 in working
+    order); waits for all of the device's work, on every stream."""
     n = ctypes.c_uint32()
     _check("dpr_device_wait_failures", lib().dpr_device_wait_failures(ctypes.byref(n)))
     return n.value

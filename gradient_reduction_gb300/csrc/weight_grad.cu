@@ -792,7 +792,8 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
 dpr_status dpr_device_wait_failures(uint32_t* count) {
     if (!count) return DPR_ERR_INVALID_ARG;
     unsigned int v = 0, w = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(&v, g_wait_failures, sizeof(v));
+    cudaError_t e = cudaDeviceSynchronize();   // a copy alone does not wait for non-blocking streams
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_wait_failures, sizeof(v));
     if (e == cudaSuccess) e = norm_wait_failures(&w);
     *count = v + w;
     return record_cuda_status(e);

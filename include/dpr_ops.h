@@ -129,10 +129,11 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
- * How many waits inside these operators' kernels have run out on the current
- * device since the library was loaded (each is bounded; 0 unless the
- * hardware or the library is broken: such a call's result is incomplete).
- * Waits for the device's work.
+ * How often a wait inside these operators' kernels has run out on the current
+ * device since the library was loaded (each wait is bounded; 0 unless the
+ * hardware or the library is broken): at least once for every block in which
+ * one did, whose call's result is incomplete.  Waits for all of the device's
+ * work, on every stream.
  */
 dpr_status dpr_device_wait_failures(uint32_t* count);
 

@@ -95,3 +95,19 @@ def test_unaligned_inputs_rewritten_before_every_weight_gradient(programmatic):
             assert k == 0 or not torch.equal(got[k], got[k - 1])
     finally:
         dpr.dpr_set_programmatic_launch(old)
+
+
+def test_the_count_of_failed_waits_waits_for_side_streams():
+    """The count is read after work on a non-blocking stream has ended, not beside it: some 60 ms of
+    passes over 1 GiB."""
+    H.device()
+    big = torch.zeros(1 << 28, device="cuda")
+    assert dpr.dpr_device_wait_failures() == 0       # the first call also loads the counters
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(200):
+            big.add_(1)
+    pending = not side.query()
+    assert dpr.dpr_device_wait_failures() == 0
+    assert pending and side.query()
