@@ -111,3 +111,158 @@ def test_the_count_of_failed_waits_waits_for_side_streams():
     pending = not side.query()
     assert dpr.dpr_device_wait_failures() == 0
     assert pending and side.query()
+
+
+# --- chains of calls whose buffers hold something else before every call -----
+
+EPS = 1e-5
+
+
+def _buffers(rows, width):
+    e = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device="cuda")
+    return (e(rows, width), e(rows, dtype=torch.float32), e(rows, dtype=torch.float32),
+            dpr.dpr_checkpoint_empty(rows, width), dpr.dpr_checkpoint_empty(rows, width),
+            e(rows, width), e(width), e(width), e(width, width))
+
+
+def _flat(buffers):
+    out = []
+    for t in buffers:
+        out += [t.codes, t.steps] if isinstance(t, dpr.Checkpoint) else [t]
+    return out
+
+
+def _poison(buffers):
+    """0x5A in every byte: 1.5e16 as bf16 and fp32, 90 as a code, a step of 2^-37."""
+    for t in _flat(buffers):
+        if t.is_contiguous():
+            t.view(torch.uint8).fill_(0x5A)
+        else:
+            t.fill_(0x5A)
+
+
+def _chain(stream, inputs, buffers):
+    x, dy, w, b = inputs
+    y, mean, rstd, xs, ys, dx, dw, db, lin = buffers
+    dpr.dpr_layernorm_forward(x, w, b, EPS, y, mean, rstd, xs, ys, stream=stream)
+    dpr.dpr_layernorm_backward(dy, xs, w, mean, rstd, dx, dw, db, stream=stream)
+    dpr.dpr_linear_weight_grad(dx, ys, lin, stream=stream)
+
+
+def _inputs(rows, width, seed):
+    g = torch.Generator().manual_seed(seed)
+    t = [torch.randn(rows, width, generator=g) for _ in range(2)]
+    t += [torch.randn(width, generator=g) for _ in range(2)]
+    return [a.bfloat16().cuda() for a in t]
+
+
+def _same(got, want, what):
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), f"{what}: tensor {i}"
+
+
+# staged, single-element, two CTAs a row, three reads a row and two passes
+@pytest.mark.parametrize("rows,width", [(300, 1056), (77, 100), (64, 97), (20, 8208), (2, 24592)])
+@pytest.mark.parametrize("programmatic", [True, False])
+@pytest.mark.parametrize("handle", ["object", "number"])
+def test_chains_over_spoilt_buffers(rows, width, programmatic, handle):
+    """Each repeat starts from buffers that hold neither its results nor an earlier repeat's, and
+    takes other inputs than the one before; nothing waits between the calls.  A call that ran on
+    another stream, not at all, or before the one it reads from had written would show."""
+    H.device()
+    old = dpr.dpr_set_programmatic_launch(programmatic)
+    try:
+        inputs = [_inputs(rows, width, 50 + k) for k in range(2)]
+        buffers = _buffers(rows, width)
+        want = []
+        for k in range(2):
+            _poison(buffers)
+            torch.cuda.synchronize()
+            _chain(None, inputs[k], buffers)
+            torch.cuda.synchronize()
+            want.append([t.clone() for t in _flat(buffers)])
+        for a, b in zip(*want):
+            assert not torch.equal(a, b)
+        side = torch.cuda.Stream()
+        results = []
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for k in range(6):
+                _poison(buffers)
+                _chain(side if handle == "object" else side.cuda_stream, inputs[k & 1], buffers)
+                results.append([t.clone() for t in _flat(buffers)])
+        torch.cuda.synchronize()
+        for k, got in enumerate(results):
+            _same(got, want[k & 1], f"repeat {k}")
+    finally:
+        dpr.dpr_set_programmatic_launch(old)
+
+
+def test_graph_replays_over_spoilt_buffers():
+    """Replays read the inputs and write the outputs of the time they run."""
+    H.device()
+    rows, width = 77, 1056
+    inputs = [_inputs(rows, width, 60 + k) for k in range(2)]
+    given = [t.clone() for t in inputs[0]]
+    buffers = _buffers(rows, width)
+    want = []
+    for k in range(2):
+        _chain(None, inputs[k], buffers)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in _flat(buffers)])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _chain(None, given, buffers)
+    for k in range(4):
+        for t, v in zip(given, inputs[k & 1]):
+            t.copy_(v)
+        _poison(buffers)
+        graph.replay()
+        torch.cuda.synchronize()
+        _same(_flat(buffers), want[k & 1], f"replay {k}")
+
+
+def test_kept_scratch_memory_over_spoilt_outputs():
+    """Calls of several sizes with the kept scratch memory, on two streams at once and inside a
+    capture, against separate workspaces; every output holds something else before each call."""
+    H.device()
+    sizes = [(40, 1056), (3, 8192), (700, 512), (40, 1056), (64, 4096)]
+    calls, want = [], []
+    for k, (rows, width) in enumerate(sizes):
+        g = torch.Generator().manual_seed(70 + k)
+        x, dy = (torch.randn(rows, width, generator=g).cuda() for _ in range(2))
+        mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+        out = [torch.empty_like(x), torch.empty(width, device="cuda"), torch.empty(width, device="cuda")]
+        calls.append(((dy, x, None, mean, rstd, *out), out))
+        _poison(out)
+        dpr.dpr_layernorm_backward(*calls[-1][0],
+                                   workspace=torch.empty(16 << 20, dtype=torch.uint8, device="cuda"))
+        want.append([t.clone() for t in out])
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        for _, out in calls:
+            _poison(out)
+        torch.cuda.synchronize()
+        for args, _ in calls[:3]:
+            dpr.dpr_layernorm_backward(*args)
+        with torch.cuda.stream(side):
+            for args, _ in calls[3:]:
+                dpr.dpr_layernorm_backward(*args)
+        torch.cuda.synchronize()
+        for (_, out), w in zip(calls, want):
+            _same(out, w, "kept")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for args, _ in calls:
+            dpr.dpr_layernorm_backward(*args)
+    for _ in range(2):
+        for _, out in calls:
+            _poison(out)
+        for args, _ in calls:
+            dpr.dpr_layernorm_backward(*args)
+        for _, out in calls:
+            _poison(out)
+        graph.replay()
+        torch.cuda.synchronize()
+        for (_, out), w in zip(calls, want):
+            _same(out, w, "captured")
