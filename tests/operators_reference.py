@@ -120,6 +120,17 @@ def weight_grad_bounds(dy, restored, dtype):
     return d + ROUND[dtype] * (out.abs() + d) + TINY[dtype]
 
 
+def weight_grad_chunk_bound(rows, parts):
+    """Error of a weight gradient in fp32 relative to the sum of its terms' magnitudes.  Terms are
+    exact; 16 of them at a time are added to an accumulator that truncates, each time off by less
+    than a unit in the last place (2 u) of a running sum that is at most the accumulator's
+    magnitudes; after 1024 tokens the accumulator is added to the sum of its part, rounded (u of a
+    running sum), and the at most `parts` parts to each other likewise.  (First order in u.)"""
+    truncated = -(-min(rows, 1024) // 16)
+    rounded = -(-rows // 1024) + parts + 1
+    return 2 * U * truncated + U * rounded
+
+
 def check(got, want, bound, what):
     """Elementwise |got - want| <= bound; NaN matches NaN, infinities themselves."""
     got = got.detach().cpu().double()

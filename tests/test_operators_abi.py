@@ -245,3 +245,35 @@ def test_no_kernel_takes_a_buffer_as_unchanging():
         code = re.sub(r"//.*", "", open(os.path.join(csrc, name)).read())
         for word in ("__restrict__", "__ldg", "global.nc", "ld_nc_", "load_words<"):
             assert word not in code, f"{name}: {word}"
+
+
+def test_chunk_bound_separates_one_accumulator_from_many():
+    """The summation the weight gradient's precision rests on, in 64 bits on the CPU: 16 exact terms
+    of one sign at a time into an accumulator that truncates to 24 bits.  Emptied every 1024 tokens
+    it stays within half of weight_grad_chunk_bound; run over all of them every sum is out of it."""
+    def truncate(v):
+        m, e = torch.frexp(v)
+        return torch.ldexp(torch.floor(m * 2 ** 24) * 2.0 ** -24, e)
+
+    def total(terms, chunk):
+        out = torch.zeros(terms.shape[1], dtype=torch.float32)
+        for t0 in range(0, terms.shape[0], chunk):
+            acc = torch.zeros(terms.shape[1], dtype=torch.float64)
+            for t in range(t0, min(t0 + chunk, terms.shape[0]), 16):
+                acc = truncate(acc + terms[t:t + 16].sum(0))
+            out = (out.double() + acc).float()
+        return out.double()
+
+    g = torch.Generator().manual_seed(1)
+    for rows in (8192, 16384):
+        dy = (1e-2 * torch.randn(rows, 64, generator=g).abs()).bfloat16().double()
+        codes, steps = R.encode(torch.randn(rows, 64, generator=g).abs().double())
+        terms = dy * R.decode(codes, steps)
+        want = terms.sum(0)
+        bound = R.weight_grad_chunk_bound(rows, 1)
+        error = {c: (total(terms, c) - want).abs() / want for c in (1024, 2048, 4096, rows)}
+        assert bool((error[1024] <= bound / 2).all())
+        assert bool((error[rows] > bound).all())
+        assert float(error[1024].mean()) < float(error[2048].mean()) < float(error[4096].mean())
+        # a term left out or taken twice
+        assert bool(((terms.max(0).values / want) > bound).all())
