@@ -198,10 +198,10 @@ def test_chains_over_spoilt_buffers(rows, width, programmatic, handle):
         dpr.dpr_set_programmatic_launch(old)
 
 
-def test_graph_replays_over_spoilt_buffers():
+@pytest.mark.parametrize("rows,width", [(77, 1056), (64, 97), (20, 8208)])
+def test_graph_replays_over_spoilt_buffers(rows, width):
     """Replays read the inputs and write the outputs of the time they run."""
     H.device()
-    rows, width = 77, 1056
     inputs = [_inputs(rows, width, 60 + k) for k in range(2)]
     given = [t.clone() for t in inputs[0]]
     buffers = _buffers(rows, width)
