@@ -6,6 +6,13 @@ whose leading dimensions merge into one row stride without a copy.  As in
 the rest of the package, the checks here keep a wrongly shaped, typed or
 placed tensor from being read or written out of bounds; libdpr checks
 strides, alignment and overlap, and does all of the computing.
+
+Calls that need scratch memory take it as `workspace`.  Without one they use
+PyTorch's: on the current stream memory that is kept from call to call, for
+each thread and stream the most that a call asked for (up to 64 MiB; larger
+sizes are allocated per call), until the thread ends.  It is known by the
+stream's handle, so a stream made outside PyTorch has to be idle when it is
+destroyed, as PyTorch's own memory on it demands.
 """
 from __future__ import annotations
 

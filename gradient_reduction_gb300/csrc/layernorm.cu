@@ -320,7 +320,8 @@ cudaError_t launch_long(const NormParams& p, cudaStream_t s) {
 }
 
 // Channels per thread: 32, so that a row's sums cross few threads; 48 where
-// that lets an SM hold twice as many rows (8192 x 11008 bf16: 69 us against 89);
+// that lets an SM hold twice as many rows (8192 x 11008 bf16: 69 us against 89; in
+// fp32 8 to 10 registers of a thread spill, in memory's shadow);
 // one vector while 32 would leave the GPU short of threads.
 template <typename T, int V>
 cudaError_t launch_forward(const NormParams& p, cudaStream_t s) {

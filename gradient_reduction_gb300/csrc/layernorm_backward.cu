@@ -57,8 +57,7 @@ struct JoinParams {
 
 namespace {
 
-// V elements of the row's x: the stored activation or its checkpoint.
-constexpr int kMaxDepth = 6;
+constexpr int kMaxDepth = 6;             // rows of a group in shared memory, at most
 __device__ unsigned int g_wait_failures;
 
 __device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&w)[4]) {
@@ -72,6 +71,7 @@ __device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&w)[1]) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
 }
 
+// V elements of the row's x: the stored activation or its checkpoint.
 template <typename T, int V, bool kSaved>
 struct Source {
     Raw<T, V> raw;
@@ -329,14 +329,15 @@ __device__ __forceinline__ void row_sums4(float (&v)[4], float (*s)[16][4]) {
 // column sums.  A thread owns 16 channels in 16-byte pieces, piece i at
 // i * blockDim.x + threadIdx.x, which neighbours read without bank conflicts.
 // 16384 x 4096 bf16 with the join: 68 us, 5.9 TB/s (0.87 of the measured copy
-// rate); from a checkpoint 82 us, 4.1 TB/s, where restoring the codes twice
-// makes instructions the bound (405 a warp and row against 333; 57% of the
-// issue slots, at 16 warps an SM that its 128 registers allow).  One row a turn
-// in registers: 76 and 83 us; 8 channels a thread: 125 and 134 us; deeper
-// staging or loads asked for earlier: no difference.
+// rate); from a checkpoint 80 us, 4.2 TB/s.  There neither memory (48% of DRAM's
+// peak) nor the issue slots (58%) are full: the codes are restored twice, 415
+// instructions a warp and row against 333, and at the 16 warps an SM that its 128
+// registers allow the latencies of a turn's two passes and the barrier between them
+// show.  One row a turn in registers: 76 and 83 us; 8 channels a thread: 125 and
+// 134 us; deeper staging or loads asked for earlier: no difference.
 // kPair: a row to two CTAs of a cluster, which send each other their half's
 // four sums.  8192 x 11008 bf16: 116 us (two passes: 166), from a checkpoint 138
-// (154); 8192 x 12288: 117 and 144 us, 8192 x 12288 fp32: 206 us, 5.9 TB/s.  A
+// (154); 8192 x 12288: 118 and 144 us, 8192 x 12288 fp32: 207 us, 5.8 TB/s.  A
 // turn waits once for the other CTA, with one CTA an SM to fill the gap.
 template <typename T, bool kSaved, bool kPair>
 __global__ void __launch_bounds__(512) norm_grad_staged(const __grid_constant__ NormGradParams p) {
@@ -756,6 +757,7 @@ cudaError_t launch_backward(NormGradParams& p, cudaStream_t s) {
     if (p.width <= kFusedWidth) {
         if constexpr (V == 16) return launch_fused<T, 16, 1, kSaved>(p, s);
         else if constexpr (V == 8 && sizeof(T) == 4)
+            // 16 channels spill 26 registers a thread from x: 16384 x 8192 257 us, 0.92 of the floor
             return p.width <= 4096 ? launch_fused<T, 8, 1, kSaved>(p, s)
                                    : launch_fused<T, 8, 2, kSaved>(p, s);
         else if constexpr (V == 8) return launch_fused<T, 8, 2, kSaved>(p, s);

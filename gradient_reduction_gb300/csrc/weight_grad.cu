@@ -14,11 +14,12 @@
 // registers.
 //
 // The tensor core's fp32 accumulation truncates, an error that grows with the
-// length of the sum (5.7e-6 relative after 8192 tokens, against 5.8e-7 for
-// rounded fp32 sums).  So an accumulator runs over 1024 tokens only; then the
-// other one goes on (two of 256 columns fill the tensor memory) while the
-// first is added, rounded to nearest, to the tile's sums in the registers of
-// eight warps.
+// length of the sum (terms of both signs: 5.7e-6 relative after 8192 tokens,
+// against 5.8e-7 for rounded fp32 sums).  So an accumulator runs over 1024 tokens
+// only; then the other one goes on (two of 256 columns fill the tensor memory)
+// while the first is added, rounded to nearest, to the tile's sums in the
+// registers of eight warps: 5.4e-7, and 8.4e-7 for terms of one sign, where every
+// truncation loses.
 //
 // Warps of a CTA: 0 issues the TMA loads, 1 the matrix instructions (first
 // CTA only), 4-11 keep the sums and store them, 12-19 restore: two groups of
@@ -160,7 +161,9 @@ __device__ __forceinline__ void put_grad(const WeightGradParams& p, int64_t at, 
 // Consecutive rows of dW at one column: `count` of a thread's kN sums, the
 // rows `stride` bytes apart.  The address advances step by step (and is
 // hidden from the compiler, which would otherwise compute all kN at once and
-// spill the sums).
+// spill the sums).  With kAdd every row's load waits for the store before it, kN
+// times the latency of memory for a tile: 8192 tokens, 4096 x 4096, fp32 321 us
+// against 172 without, 16 tokens 137 against 16.
 template <bool kBf16, bool kAdd, int kN>
 __device__ __forceinline__ void store_column(char* d, int64_t stride, int count,
                                              const float (&sum)[kN]) {
