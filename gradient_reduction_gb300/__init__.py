@@ -65,3 +65,8 @@ from ._operators import (  # noqa: F401
     dpr_layernorm_forward,
     dpr_linear_weight_grad,
 )
+from ._step import (  # noqa: F401
+    dpr_grouped_linear,
+    dpr_grouped_linear_input_grad,
+    dpr_grouped_linear_weight_grad,
+)

@@ -94,6 +94,17 @@ _SIGS = {
     "dpr_device_wait_failures": [ctypes.POINTER(ctypes.c_uint32)],
     "dpr_linear_weight_grad": [_c_p, _i64, _c_p, _i64, _i64, _i64, _c_p, _i64, _int, _int, _c_p,
                                _i64, _c_p],
+    "dpr_grouped_linear_workspace": [_c_p, _i64, _i64, _i64, _c_p, _i64, _i64, _i64, _i64, _i64p],
+    "dpr_grouped_linear": [_c_p, _i64, _i64, _c_p, _i64, _c_p, _i64, _i64, _i64, _i64, _c_p, _i64,
+                           _int, _c_p, _i64, _c_p],
+    "dpr_grouped_linear_input_grad_workspace": [_c_p, _i64, _i64, _i64, _c_p, _i64, _i64, _i64,
+                                                _i64, _i64p],
+    "dpr_grouped_linear_input_grad": [_c_p, _i64, _i64, _c_p, _i64, _c_p, _i64, _i64, _i64, _i64,
+                                      _c_p, _i64, _int, _c_p, _i64, _c_p],
+    "dpr_grouped_linear_weight_grad_workspace": [_c_p, _i64, _c_p, _i64, _c_p, _i64, _i64, _i64,
+                                                 _i64, _i64p],
+    "dpr_grouped_linear_weight_grad": [_c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p, _i64, _i64, _i64,
+                                       _c_p, _i64, _i64, _int, _int, _c_p, _i64, _c_p],
     "dpr_strerror": [ctypes.c_int],
     "dpr_last_cuda_error": [],
     "dpr_version": [],

@@ -24,7 +24,7 @@ LIB = os.path.join(LIBDIR, "libdpr.so")
 SOURCES = ["dpr_api.cu", "reduce_kernels.cu", "gather_kernels.cu", "coalesced.cu",
            "pipeline.cu", "cost_model.cpp", "flatten_noalloc.cu", "fragments.cu", "requests.cu",
            "ops_host.cu", "layernorm.cu", "layernorm_backward.cu", "checkpoint.cu",
-           "weight_grad.cu"]
+           "weight_grad.cu", "grouped.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC,-O2",
          "-I", os.path.join(ROOT, "include")]
@@ -39,7 +39,7 @@ def _nvcc() -> str:
 
 def _newest_input() -> float:
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    paths += [os.path.join(ROOT, "include", h) for h in ("dpr.h", "dpr_ops.h")]
+    paths += [os.path.join(ROOT, "include", h) for h in ("dpr.h", "dpr_ops.h", "dpr_step.h")]
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths)
 

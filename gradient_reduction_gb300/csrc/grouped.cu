@@ -1,0 +1,889 @@
+// Linear layers of experts over tokens sorted by expert: the product, its input
+// gradient and its weight gradients, on the tensor cores.
+//
+// A pair of CTAs computes a tile of 256 features (the M of the instruction, 128
+// in each CTA) by up to 256 columns (N) with cta_group::2 instructions:
+//   product          D[o][t] = sum_i W[o][i] x[t][i]    both operands along K
+//   input gradient   D[i][t] = sum_o W[o][i] dy[t][o]   W along M, dy along K
+//   weight gradient  D[i][o] = sum_t x[t][i] dy[t][o]   both along M and N
+// The weights are the M side: an expert's tokens, of whatever number, are the N
+// side, whose extent an instruction may choose in steps of 32, so few tokens
+// waste little.  Features on the lanes of the accumulator also mean that a warp
+// stores 32 consecutive elements of an output row straight from registers.
+//
+// Ragged edges: features and weights end with their tensor maps, which read
+// zeros outside.  A tile of tokens reaches into the next expert's rows, whose
+// columns of D are not stored.  The sum of a weight gradient runs along the
+// tokens: there the rows behind the expert's last one are overwritten with
+// zeros in shared memory, in both operands, since a NaN times 0 would not be 0.
+//
+// Sums run over 1024 elements in tensor memory, whose accumulation truncates,
+// and are then added, rounded, to fp32 sums in registers.
+#include <algorithm>
+#include <atomic>
+
+#include "ops_device.cuh"
+#include "ops_kernels.h"
+#include "tensor_core.cuh"
+
+namespace dpr {
+
+namespace {
+
+enum Product { kForward, kInputGrad, kWeightGrad, kWeightGradSaved };
+
+constexpr int kTile = 256;               // features, and columns at most, of a tile
+constexpr int kHalf = 128;               // of each CTA
+constexpr int kDepth = 64;               // elements of the sum per step
+constexpr int kChunk = 16;               // steps per accumulator
+constexpr int kOperandBytes = kHalf * kDepth * 2;
+constexpr int kGroupBytes = 64 * kDepth * 2;     // 64 channels of an operand along M or N
+constexpr int kCodeBytes = kHalf * kDepth;
+constexpr int kStepBytes = 16 * kDepth;  // 16 step bytes a token, 4 of them used
+constexpr int kPiece = 16;               // rows of a load of part of a tile's tokens
+constexpr int kSumWarps = 8;
+constexpr int kRestoreWarps = 4;         // of each of the two groups
+constexpr int kPairs = 76;               // of a GB300's 152 SMs
+
+__host__ __device__ constexpr bool is_weight_grad(int kind) { return kind >= kWeightGrad; }
+__host__ __device__ constexpr int stages(int kind) { return kind == kWeightGradSaved ? 5 : 6; }
+__host__ __device__ constexpr int threads(int kind) { return kind == kWeightGradSaved ? 640 : 384; }
+constexpr int smem_bytes(int kind) {
+    return 1024 + stages(kind) * (2 * kOperandBytes +
+                                  (kind == kWeightGradSaved ? kCodeBytes + kStepBytes : 0));
+}
+// Registers per thread after the split of the restoring kernel (as in the
+// weight gradient of one layer); together no more than the launch's.
+constexpr int kIssueRegs = 40, kSumRegs = 160, kRestoreRegs = 56;
+static_assert(kIssueRegs + 2 * kSumRegs + 2 * kRestoreRegs <= 5 * 96, "the block's registers");
+
+}  // namespace
+
+struct GroupedParams {
+    CUtensorMap a;           // W, or x (or its codes): the M side
+    CUtensorMap b;           // x or dy: the N side
+    CUtensorMap b_piece;     // the same in pieces of kPiece rows (product, input gradient)
+    CUtensorMap steps;
+    const int32_t* offsets;
+    int experts;
+    int rows;
+    int m_size;              // features along M
+    int m_tiles;
+    int n_size;              // weight gradients: features along N
+    int n_tiles;
+    int k_size;              // else: length of the sum
+    void* out;
+    int64_t out_stride;
+    int64_t out_expert_stride;   // weight gradients
+    int out_bf16;
+    int accumulate;
+};
+
+namespace {
+
+__device__ unsigned int g_wait_failures;
+
+// The experts' tokens and tiles, worked out by every block.
+struct Experts {
+    int begin[DPR_MAX_EXPERTS];
+    int count[DPR_MAX_EXPERTS];
+    int tile0[DPR_MAX_EXPERTS + 1];      // tiles of the experts before
+};
+
+__host__ __device__ inline int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+
+template <int kKind>
+__device__ void make_table(const GroupedParams& p, Experts& t) {
+    for (int e = int(threadIdx.x); e < p.experts; e += int(blockDim.x)) {
+        const int b = min(max(p.offsets[e], 0), p.rows);
+        const int end = min(max(p.offsets[e + 1], b), p.rows);
+        t.begin[e] = b;
+        t.count[e] = end - b;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {              // tiles, summed 32 experts at a time
+        const int lane = int(threadIdx.x);
+        int before = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < p.experts)
+                n = p.m_tiles * (is_weight_grad(kKind) ? p.n_tiles : tiles_of(t.count[e]));
+            int upto = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+                if (lane >= d) upto += v;
+            }
+            if (e < p.experts) t.tile0[e] = before + upto - n;
+            before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+        }
+        if (lane == 0) t.tile0[p.experts] = before;
+    }
+    __syncthreads();
+}
+
+struct Tile {
+    int e;                   // advances from call to call
+    int m, n;                // first feature, first column (row of the tokens, or feature)
+    int columns;             // columns that are stored
+    int size;                // columns of the instruction: the same up to a multiple of 32
+    int steps;
+    int k, k_count;          // weight gradients: first token and how many
+};
+
+// The n-th tile of a pair; false when there is none.  An expert's tiles run in
+// columns of 8 along N, so that the tiles at work at one time share inputs.
+template <int kKind>
+__device__ __forceinline__ bool tile_at(const GroupedParams& p, const Experts& t, int index, Tile& s) {
+    if (index >= t.tile0[p.experts]) return false;
+    while (index >= t.tile0[s.e + 1]) ++s.e;
+    const int local = index - t.tile0[s.e];
+    const int count = t.count[s.e];
+    const int n_tiles = is_weight_grad(kKind) ? p.n_tiles : tiles_of(count);
+    const int group = local / (8 * p.m_tiles);
+    const int rest = local - group * 8 * p.m_tiles;
+    const int height = min(8, n_tiles - group * 8);
+    s.m = rest / height * kTile;
+    const int n = group * 8 + rest % height;
+    if constexpr (is_weight_grad(kKind)) {
+        s.n = n * kTile;
+        s.columns = min(kTile, p.n_size - s.n);
+        s.size = (s.columns + 31) & ~31;
+        s.k = t.begin[s.e];
+        s.k_count = count;
+        s.steps = (count + kDepth - 1) / kDepth;
+    } else {
+        // an expert's tokens in tiles of even size
+        s.size = ((count + n_tiles - 1) / n_tiles + 31) & ~31;
+        s.n = t.begin[s.e] + n * s.size;
+        s.columns = min(s.size, count - n * s.size);
+        s.k = 0;
+        s.k_count = p.k_size;
+        s.steps = (p.k_size + kDepth - 1) / kDepth;
+    }
+    return true;
+}
+
+// Two codes, in the low bytes of the halves of `w`, as bf16: the seven low
+// bits on top of 128, less 128 or (sign bit) 256, times the step.
+__device__ __forceinline__ uint32_t restore_pair(uint32_t w, uint32_t step2) {
+    const uint32_t low = (w & 0x007F007Fu) | 0x43004300u;
+    const uint32_t base = (w & 0x00800080u) | 0x43004300u;
+    uint32_t v, r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(low), "r"(base));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(step2));
+    return r;
+}
+
+__device__ __forceinline__ void store_shared(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+                 "r"(d) : "memory");
+}
+
+// Consecutive rows of the output at one column: `count` of a thread's kN sums,
+// the rows `stride` bytes apart.  With kAdd the old values of 16 rows are
+// loaded together.  The address advances step by step and is hidden from the
+// compiler, which would otherwise compute all of them at once and spill the sums.
+template <bool kBf16, bool kAdd, int kN>
+__device__ __forceinline__ void store_column(char* d, int64_t stride, int count,
+                                             const float (&sum)[kN]) {
+#pragma unroll
+    for (int j0 = 0; j0 < kN; j0 += 16) {
+        float old[16];
+        if constexpr (kAdd) {
+            const char* q = d;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                old[j] = 0.0f;
+                if (j0 + j < count) {
+                    if constexpr (kBf16) {
+                        uint16_t h;
+                        asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(q) : "memory");
+                        old[j] = bf_1(h);
+                    } else {
+                        asm volatile("ld.global.f32 %0, [%1];" : "=f"(old[j]) : "l"(q) : "memory");
+                    }
+                }
+                q += stride;
+                asm volatile("" : "+l"(q));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (j0 + j < count) {
+                const float v = kAdd ? __fadd_rn(old[j], sum[j0 + j]) : sum[j0 + j];
+                if constexpr (kBf16)
+                    asm volatile("st.global.u16 [%0], %1;" ::"l"(d), "h"(to_bf16(v)) : "memory");
+                else
+                    asm volatile("st.global.f32 [%0], %1;" ::"l"(d), "f"(v) : "memory");
+            }
+            d += stride;
+            asm volatile("" : "+l"(d));
+        }
+    }
+}
+
+// Warps of a CTA: 0 issues the TMA loads, 1 the matrix instructions (first CTA
+// only), 4-11 keep the sums and store them.  2 passes a loaded stage on to the
+// first CTA (and writes the zeros behind an expert's last token); with
+// checkpoints 12-19 do, which restore x on the way, in two groups that take turns.
+template <int kKind>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kKind), 1)
+grouped_pairs(const __grid_constant__ GroupedParams p) {
+    constexpr bool kGrad = is_weight_grad(kKind);
+    constexpr bool kSaved = kKind == kWeightGradSaved;
+    constexpr int kStages = stages(kKind);
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[3 * kStages + 4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ Experts table;
+
+    const uint32_t base = (tc::smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t a_at = base;                                  // [kStages], 1024-byte aligned
+    const uint32_t b_at = base + kStages * kOperandBytes;        // [kStages]
+    const uint32_t codes = base + 2 * kStages * kOperandBytes;   // [kStages], with checkpoints
+    const uint32_t steps = codes + kStages * kCodeBytes;         // [kStages]
+    const uint32_t bar0 = tc::smem_addr(bars);
+    const auto full = [&](int s) { return bar0 + 8u * s; };                      // loads landed
+    const auto free_ = [&](int s) { return bar0 + 8u * (kStages + s); };         // stage consumed
+    const auto ready = [&](int s) { return bar0 + 8u * (2 * kStages + s); };     // in both CTAs
+    const auto summed = [&](int a) { return bar0 + 8u * (3 * kStages + a); };
+    const auto stored = [&](int a) { return bar0 + 8u * (3 * kStages + 2 + a); };
+
+    const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int pairs = int(gridDim.x) >> 1, pair = int(blockIdx.x) >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tc::mbar_init(full(s), 1);
+            tc::mbar_init(free_(s), 1);
+            tc::mbar_init(ready(s), kSaved ? 2 * kRestoreWarps : 2);
+        }
+        for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(summed(a), 1);
+            tc::mbar_init(stored(a), 2 * kSumWarps);
+        }
+        tc::mbar_init_fence();
+        if (p.rows > 0) {                // else the maps are empty
+            tc::tma_prefetch_map(&p.a);
+            tc::tma_prefetch_map(&p.b);
+        }
+        if constexpr (!kGrad) tc::tma_prefetch_map(&p.b_piece);
+        if constexpr (kSaved) tc::tma_prefetch_map(&p.steps);
+    }
+    if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    grid_wait();
+    grid_release();
+    make_table<kKind>(p, table);
+
+    bool ok = true;
+    Tile s;
+    s.e = 0;
+    if constexpr (kSaved)
+        if (warp < 4) tc::give_registers<kIssueRegs>();
+    if (warp == 0) {
+        if (tc::elect_one()) {
+            int st = 0;
+            uint32_t round = 0;
+            for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+                const int m = s.m + int(rank) * kHalf;
+                const int half = s.size >> 1, c = s.n + int(rank) * half;
+                for (int k = 0; k < s.steps; ++k) {
+                    if (!(ok = tc::mbar_wait(free_(st), (round & 1) ^ 1))) break;
+                    const uint32_t a = a_at + st * kOperandBytes, b = b_at + st * kOperandBytes;
+                    const int d = k * kDepth;
+                    if constexpr (kGrad) {
+                        const int t = s.k + d;
+                        if constexpr (kSaved) {
+                            tc::mbar_expect(full(st), kOperandBytes + kCodeBytes + kStepBytes);
+                            tc::tma_load(codes + st * kCodeBytes, &p.a, m, t, full(st));
+                            tc::tma_load(codes + st * kCodeBytes + kCodeBytes / 2, &p.a, m + 64, t,
+                                         full(st));
+                            tc::tma_load(steps + st * kStepBytes, &p.steps,
+                                         (m / kBlockChannels) & ~15, t, full(st));
+                        } else {
+                            tc::mbar_expect(full(st), 2 * kOperandBytes);
+                            tc::tma_load(a, &p.a, m, t, full(st));
+                            tc::tma_load(a + kGroupBytes, &p.a, m + 64, t, full(st));
+                        }
+                        tc::tma_load(b, &p.b, c, t, full(st));
+                        tc::tma_load(b + kGroupBytes, &p.b, c + 64, t, full(st));
+                    } else {
+                        tc::mbar_expect(full(st), kOperandBytes + half * kDepth * 2);
+                        if constexpr (kKind == kForward) {
+                            tc::tma_load(a, &p.a, d, m, s.e, full(st));
+                        } else {
+                            tc::tma_load(a, &p.a, m, d, s.e, full(st));
+                            tc::tma_load(a + kGroupBytes, &p.a, m + 64, d, s.e, full(st));
+                        }
+                        if (half == kHalf) {
+                            tc::tma_load(b, &p.b, d, c, full(st));
+                        } else {
+                            for (int r = 0; r < half; r += kPiece)
+                                tc::tma_load(b + r * kDepth * 2, &p.b_piece, d, c + r, full(st));
+                        }
+                    }
+                    if (++st == kStages) { st = 0; ++round; }
+                }
+            }
+            // every load has landed and every signal of the matrix instructions has arrived
+            // here before the CTA may leave: the last use of each stage
+            const uint32_t total = round * kStages + st;
+            for (int k = 0; k < kStages; ++k) {
+                const uint32_t uses = total / kStages + (uint32_t(k) < total % kStages);
+                if (uses == 0) continue;
+                ok &= tc::mbar_wait(full(k), (uses - 1) & 1);
+                if (ok) ok = tc::mbar_wait(free_(k), (uses - 1) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && tc::elect_one()) {
+            constexpr bool kAlongM = kKind != kForward, kAlongN = kGrad;
+            // 16 elements further along the sum
+            constexpr uint32_t a_next = (kAlongM ? 2048 : 32) >> 4;
+            constexpr uint32_t b_next = (kAlongN ? 2048 : 32) >> 4;
+            const uint64_t a0 = kAlongM ? tc::operand(a_at, kGroupBytes, 1024)
+                                        : tc::operand_along_k(a_at);
+            const uint64_t b0 = kAlongN ? tc::operand(b_at, kGroupBytes, 1024)
+                                        : tc::operand_along_k(b_at);
+            uint32_t st = 0, round = 0, acc = 0, acc_round = 0;
+            for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+                const uint32_t instruction = tc::bf16_instruction(kTile, s.size, kAlongM, kAlongN);
+                for (int left = s.steps; ok && left > 0; left -= kChunk) {
+                    if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
+                    const uint32_t d = tmem + acc * kTile;
+                    bool add = false;
+                    for (int k = min(left, kChunk); k > 0; --k) {
+                        if (!(ok = tc::mbar_wait(ready(st), round & 1))) break;
+                        tc::fence_after_sync();
+                        const uint64_t a = a0 + st * (kOperandBytes >> 4);
+                        const uint64_t b = b0 + st * (kOperandBytes >> 4);
+#pragma unroll
+                        for (int j = 0; j < kDepth / 16; ++j) {
+                            tc::mma(d, a + j * a_next, b + j * b_next, instruction, add);
+                            add = true;
+                        }
+                        tc::commit_both(free_(st));
+                        if (++st == kStages) { st = 0; ++round; }
+                    }
+                    if (!ok) break;
+                    tc::commit_both(summed(acc));
+                    if (++acc == 2) { acc = 0; ++acc_round; }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2 && !kSaved) {
+        int st = 0;
+        uint32_t round = 0;
+        for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+            for (int k = 0; k < s.steps; ++k) {
+                if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
+                const int valid = s.k_count - k * kDepth;
+                if (kGrad && valid < kDepth) {
+                    // rows of the step that belong to no token of the expert: 128 bytes in
+                    // each group of 64 channels, whatever the order of the pieces in them
+                    for (int r = valid + (lane >> 3); r < kDepth; r += 4) {
+                        const uint32_t at = st * kOperandBytes + r * 128 + (lane & 7) * 16;
+                        store_shared(a_at + at, 0, 0, 0, 0);
+                        store_shared(a_at + at + kGroupBytes, 0, 0, 0, 0);
+                        store_shared(b_at + at, 0, 0, 0, 0);
+                        store_shared(b_at + at + kGroupBytes, 0, 0, 0, 0);
+                    }
+                    tc::fence_to_async();
+                    __syncwarp();
+                }
+                if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(st), 0));
+                if (++st == kStages) { st = 0; ++round; }
+            }
+        }
+    } else if (warp >= 4 && warp < 4 + kSumWarps) {
+        if constexpr (kSaved) tc::take_registers<kSumRegs>();
+        constexpr int kColumns = kTile / 2;
+        const int quarter = warp & 3;               // the lanes this warp may read
+        const int side = (warp - 4) >> 2;           // half of the columns
+        int acc = 0;
+        uint32_t acc_round = 0;
+        float sum[kColumns];
+        for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+            const int half = s.size >> 1;           // a multiple of 16
+#pragma unroll
+            for (int j = 0; j < kColumns; ++j) sum[j] = 0.0f;
+            for (int k = 0; k < s.steps; k += kChunk) {
+                if (!(ok = tc::mbar_wait_warp(summed(acc), acc_round & 1))) break;
+                tc::fence_after_sync();
+                const uint32_t from = tmem + acc * kTile + side * half + (uint32_t(quarter) << 21);
+#pragma unroll
+                for (int c = 0; c < kColumns; c += 16) {
+                    if (c < half) {
+                        uint32_t v[16];
+                        tc::tmem_load16(from + c, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[c + j] = __fadd_rn(sum[c + j], __uint_as_float(v[j]));
+                    }
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(stored(acc), 0));
+                if (++acc == 2) { acc = 0; ++acc_round; }
+            }
+            if (!ok) break;
+            const int f = s.m + int(rank) * kHalf + quarter * 32 + lane;
+            const int count = min(half, s.columns - side * half);
+            if (f < p.m_size && count > 0 && (s.steps > 0 || !p.accumulate)) {
+                const int64_t size = p.out_bf16 ? 2 : 4;
+                int64_t at = int64_t(s.n + side * half) * p.out_stride + f;
+                if constexpr (kGrad) at += int64_t(s.e) * p.out_expert_stride;
+                char* d = static_cast<char*>(p.out) + at * size;
+                const int64_t stride = p.out_stride * size;
+                if (p.out_bf16) {
+                    if (kGrad && p.accumulate) store_column<true, true>(d, stride, count, sum);
+                    else store_column<true, false>(d, stride, count, sum);
+                } else {
+                    if (kGrad && p.accumulate) store_column<false, true>(d, stride, count, sum);
+                    else store_column<false, false>(d, stride, count, sum);
+                }
+            }
+        }
+    } else if (kSaved && warp >= 12) {
+        tc::give_registers<kRestoreRegs>();
+        const int turn = (warp - 12) >> 2;          // of the two groups
+        const int group = warp & 1;                 // 64 channels of the operand
+        const int chunk = lane & 3;                 // 16 channels of those
+        // 8 neighbouring lanes are 4 chunks of two rows: they read 128 consecutive bytes, and
+        // as the 16-byte pieces of a row are permuted by the row's number, write all 32 banks
+        const int row = ((warp & 2) << 4) + (lane >> 2);
+        const uint32_t read = uint32_t(group * (kCodeBytes / 2) + row * 64 + chunk * 16);
+        const uint32_t write = uint32_t(group * kGroupBytes + row * 128);
+        const uint32_t piece0 = uint32_t((chunk * 2) ^ (row & 7)) * 16;
+        const uint32_t piece1 = uint32_t((chunk * 2 + 1) ^ (row & 7)) * 16;
+        uint32_t step0 = 0;                         // steps of the tiles before
+        for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+            const uint32_t block = uint32_t(((s.m + int(rank) * kHalf) / kBlockChannels & 15) +
+                                            group * 2 + (chunk >> 1));
+            for (int k = (step0 & 1) ^ turn; k < s.steps; k += 2) {
+                const uint32_t st = (step0 + k) % kStages, round = (step0 + k) / kStages;
+                if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
+                const int valid = s.k_count - k * kDepth;
+                uint32_t w[4][4], step[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[h][0]), "=r"(w[h][1]), "=r"(w[h][2]), "=r"(w[h][3])
+                                 : "r"(codes + st * kCodeBytes + read + h * 8 * 64));
+                    asm volatile("ld.shared.u8 %0, [%1];"
+                                 : "=r"(step[h])
+                                 : "r"(steps + st * kStepBytes + (row + 8 * h) * 16 + block));
+                    if (row + 8 * h >= valid) {     // behind the expert's last token
+                        w[h][0] = w[h][1] = w[h][2] = w[h][3] = 0;
+                        step[h] = 0;
+                    }
+                }
+                const uint32_t at = a_at + st * kOperandBytes + write;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t step2 = step[h] * 0x00800080u;   // the byte as a bf16 exponent
+                    uint32_t v[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[2 * j] = restore_pair(__byte_perm(w[h][j], 0, 0x4140), step2);
+                        v[2 * j + 1] = restore_pair(__byte_perm(w[h][j], 0, 0x4342), step2);
+                    }
+                    store_shared(at + piece0 + h * 8 * 128, v[0], v[1], v[2], v[3]);
+                    store_shared(at + piece1 + h * 8 * 128, v[4], v[5], v[6], v[7]);
+                }
+                if (valid < kDepth) {
+                    const uint32_t to = b_at + st * kOperandBytes + write;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        if (row + 8 * h >= valid) {
+                            store_shared(to + piece0 + h * 8 * 128, 0, 0, 0, 0);
+                            store_shared(to + piece1 + h * 8 * 128, 0, 0, 0, 0);
+                        }
+                }
+                tc::fence_to_async();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(st), 0));
+            }
+            step0 += uint32_t(s.steps);
+        }
+    }
+    if (!ok) atomicAdd(&g_wait_failures, 1u);
+    __syncwarp();
+    // nobody leaves while the other CTA may still signal or read this one
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_free(tmem, 512);
+}
+
+// Rows copied to 16-byte-aligned ones, for inputs that TMA cannot read.  Row r
+// of `rows` is row r % inner of matrix r / inner; four loads of a thread in
+// flight before its stores.  The source is not declared __restrict__: a
+// programmatic launch lives while the grid before it writes.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+repack_matrices(const T* from, int64_t from_stride, int64_t from_outer, T* to, int64_t to_stride,
+                int64_t rows, int64_t inner, int width) {
+    grid_wait();
+    grid_release();
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T* f = from + r / inner * from_outer + r % inner * from_stride;
+        T* t = to + r * to_stride;
+        for (int c0 = int(threadIdx.x); c0 < width; c0 += 4 * kThreads) {
+            T v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j * kThreads < width) v[j] = f[c0 + j * kThreads];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j * kThreads < width) t[c0 + j * kThreads] = v[j];
+        }
+    }
+}
+
+template <typename T>
+cudaError_t repack(const void* from, int64_t from_stride, int64_t from_outer, void* to,
+                   int64_t to_stride, int64_t rows, int64_t inner, int64_t width, cudaStream_t s) {
+    const T* f = static_cast<const T*>(from);
+    T* t = static_cast<T*>(to);
+    int w = int(width);
+    void* args[] = {&f, &from_stride, &from_outer, &t, &to_stride, &rows, &inner, &w};
+    return launch_grid((const void*)repack_matrices<T>,
+                       dim3(unsigned(std::min<int64_t>(rows, 152 * 16))), dim3(kThreads), 0, args,
+                       s);
+}
+
+// Can TMA read these rows where they are?
+bool tma_rows(const void* p, int64_t stride, int64_t size, int64_t width) {
+    return aligned(p, 16) && stride >= width && stride * size % 16 == 0;
+}
+
+// An operand as the call gives it, and how it is read: where it is or copied.
+struct Operand {
+    const void* p;
+    int64_t stride, outer;       // in elements; `outer` from matrix to matrix
+    int64_t size, rows, inner, width;
+    bool copy = false;
+    int64_t bytes() const {      // in the workspace
+        return copy ? round_up(rows * round_up(width, 16 / size) * size, 16) : 0;
+    }
+};
+
+Operand operand(const void* p, int64_t stride, int64_t outer, int64_t size, int64_t matrices,
+                int64_t inner, int64_t width) {
+    Operand o{p, stride, outer, size, matrices * inner, inner, width};
+    o.copy = o.rows > 0 && (!tma_rows(p, stride, size, width) ||
+                            (matrices > 1 && (outer * size % 16 != 0 || outer < 0)));
+    return o;
+}
+
+// Copies an operand that TMA cannot read to `ws`, which moves on.
+cudaError_t place(Operand& o, char*& ws, cudaStream_t s) {
+    if (!o.copy) return cudaSuccess;
+    const int64_t stride = round_up(o.width, 16 / o.size);
+    const cudaError_t e =
+        o.size == 2 ? repack<uint16_t>(o.p, o.stride, o.outer, ws, stride, o.rows, o.inner, o.width, s)
+                    : repack<uint8_t>(o.p, o.stride, o.outer, ws, stride, o.rows, o.inner, o.width, s);
+    o.p = ws;
+    o.stride = stride;
+    o.outer = o.inner * stride;
+    ws += o.bytes();
+    return e;
+}
+
+cudaError_t encode(CUtensorMap* map, const Operand& o, int box_x, int box_y) {
+    const bool bytes = o.size == 1;
+    const int64_t dims[2] = {o.width, o.rows}, strides[1] = {o.stride * o.size};
+    const int box[2] = {box_x, box_y};
+    return encode_tensor_map(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                             o.p, 2, dims, strides, box,
+                             bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+cudaError_t encode_experts(CUtensorMap* map, const Operand& o, int box_x, int box_y) {
+    const int64_t experts = o.rows / o.inner;
+    const int64_t outer = experts > 1 ? o.outer : o.inner * o.stride;
+    const int64_t dims[3] = {o.width, o.inner, experts};
+    const int64_t strides[2] = {o.stride * 2, outer * 2};
+    const int box[3] = {box_x, box_y, 1};
+    return encode_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.p, 3, dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int kKind>
+cudaError_t launch_pairs(GroupedParams& p, int64_t tiles, cudaStream_t s) {
+    static std::atomic<uint64_t> allowed{0};
+    const void* k = (const void*)grouped_pairs<kKind>;
+    const cudaError_t e = allow_shared_memory(k, smem_bytes(kKind), &allowed);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&p};
+    return launch_grid(k, dim3(unsigned(2 * std::min<int64_t>(tiles, kPairs))), dim3(threads(kKind)),
+                       smem_bytes(kKind), args, s);
+}
+
+dpr_status check_sizes(int64_t rows, int64_t experts, int64_t out_features, int64_t in_features) {
+    dpr_status st = check_matrix_size(rows, out_features);
+    if (st == DPR_OK) st = check_matrix_size(rows, in_features);
+    if (st != DPR_OK) return st;
+    if (experts < 1) return DPR_ERR_INVALID_ARG;
+    if (rows > DPR_MAX_GRAD_ROWS || experts > DPR_MAX_EXPERTS) return DPR_ERR_UNSUPPORTED;
+    // tiles are counted in 31 bits
+    const int64_t m = ceil_div(out_features, kTile), n = ceil_div(in_features, kTile);
+    if (experts * m * n > (int64_t(1) << 30) ||
+        (ceil_div(rows, kTile) + experts) * std::max(m, n) > (int64_t(1) << 30))
+        return DPR_ERR_UNSUPPORTED;
+    return DPR_OK;
+}
+
+// Elements from the first to one past the last of the experts' matrices.
+int64_t experts_span(int64_t experts, int64_t outer, int64_t rows, int64_t stride, int64_t width) {
+    return (experts - 1) * outer + (rows - 1) * stride + width;
+}
+
+dpr_status check_experts(const void* p, int64_t stride, int64_t outer, int64_t experts,
+                         int64_t rows, int64_t width, int dtype, bool written) {
+    const dpr_status st = check_matrix(p, stride, width, dtype, written);
+    if (st != DPR_OK) return st;
+    if (outer < 0 || (written && experts > 1 && outer < (rows - 1) * stride + width))
+        return DPR_ERR_INVALID_ARG;
+    // TMA's strides end at 2^40 bytes
+    return outer > (int64_t(1) << 38) ? DPR_ERR_UNSUPPORTED : DPR_OK;
+}
+
+dpr_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
+    if (need == 0) return DPR_OK;
+    if (!ws || bytes < need) return DPR_ERR_INVALID_ARG;
+    return aligned(ws, 16) ? DPR_OK : DPR_ERR_ALIGNMENT;
+}
+
+// The operands of the product (x) or of the input gradient (dy).
+void operands(bool input_grad, const void* x, int64_t x_stride, int64_t rows, int64_t experts,
+              const void* weight, int64_t weight_stride, int64_t expert_stride,
+              int64_t out_features, int64_t in_features, Operand* a, Operand* b) {
+    *a = operand(weight, weight_stride, expert_stride, 2, experts, out_features, in_features);
+    *b = operand(x, x_stride, 0, 2, 1, rows, input_grad ? out_features : in_features);
+}
+
+dpr_status product_workspace(bool input_grad, const void* x, int64_t x_stride, int64_t rows,
+                             int64_t experts, const void* weight, int64_t weight_stride,
+                             int64_t expert_stride, int64_t out_features, int64_t in_features,
+                             int64_t* bytes) {
+    if (!bytes) return DPR_ERR_INVALID_ARG;
+    *bytes = 0;
+    const dpr_status st = check_sizes(rows, experts, out_features, in_features);
+    if (st != DPR_OK || rows == 0) return st;
+    Operand a, b;
+    operands(input_grad, x, x_stride, rows, experts, weight, weight_stride, expert_stride,
+             out_features, in_features, &a, &b);
+    *bytes = a.bytes() + b.bytes();
+    return DPR_OK;
+}
+
+dpr_status product(bool input_grad, const void* x, int64_t x_stride, int64_t rows,
+                   const int32_t* offsets, int64_t experts, const void* weight,
+                   int64_t weight_stride, int64_t expert_stride, int64_t out_features,
+                   int64_t in_features, void* out, int64_t out_stride, int dtype, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+    int64_t need = 0;
+    dpr_status st = product_workspace(input_grad, x, x_stride, rows, experts, weight, weight_stride,
+                                      expert_stride, out_features, in_features, &need);
+    if (st != DPR_OK) return st;
+    if (!dtype_ok(dtype)) return DPR_ERR_INVALID_ARG;
+    if (rows == 0) return DPR_OK;
+    const int64_t from = input_grad ? out_features : in_features;
+    const int64_t to = input_grad ? in_features : out_features;
+    if ((st = check_matrix(x, x_stride, from, DPR_BF16, false)) != DPR_OK) return st;
+    if ((st = check_matrix(out, out_stride, to, dtype, true)) != DPR_OK) return st;
+    if ((st = check_experts(weight, weight_stride, expert_stride, experts, out_features,
+                            in_features, DPR_BF16, false)) != DPR_OK) return st;
+    if (!offsets) return DPR_ERR_INVALID_ARG;
+    if (!aligned(offsets, 4)) return DPR_ERR_ALIGNMENT;
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != DPR_OK) return st;
+    SpanList outs, ins;
+    outs.add(out, matrix_bytes(rows, to, out_stride, dtype_size(dtype)));
+    if (need > 0) outs.add(workspace, uint64_t(need));
+    ins.add(x, matrix_bytes(rows, from, x_stride, 2));
+    ins.add(weight, 2 * uint64_t(experts_span(experts, expert_stride, out_features, weight_stride,
+                                              in_features)));
+    ins.add(offsets, 4 * uint64_t(experts + 1));
+    if (!outs.disjoint() || outs.meets(ins)) return DPR_ERR_ALIAS;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    Operand a, b;
+    operands(input_grad, x, x_stride, rows, experts, weight, weight_stride, expert_stride,
+             out_features, in_features, &a, &b);
+    GroupedParams p = {};
+    p.offsets = offsets; p.experts = int(experts); p.rows = int(rows);
+    p.m_size = int(to); p.m_tiles = int(ceil_div(to, kTile));
+    p.k_size = int(from);
+    p.out = out; p.out_stride = out_stride; p.out_bf16 = dtype == DPR_BF16;
+    cudaError_t e = place(a, ws, s);
+    if (e == cudaSuccess) e = place(b, ws, s);
+    if (e == cudaSuccess) e = encode_experts(&p.a, a, 64, input_grad ? kDepth : kHalf);
+    if (e == cudaSuccess) e = encode(&p.b, b, kDepth, kHalf);
+    if (e == cudaSuccess) e = encode(&p.b_piece, b, kDepth, kPiece);
+    if (e != cudaSuccess) return record_cuda_status(e);
+    // at most: every expert's last tile may be short
+    const int64_t tiles = p.m_tiles * (rows / kTile + std::min(rows, experts));
+    e = input_grad ? launch_pairs<kInputGrad>(p, tiles, s) : launch_pairs<kForward>(p, tiles, s);
+    return record_cuda_status(e);
+}
+
+// The operands of the weight gradients: x, or its codes and steps; dy.
+void grad_operands(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                   const dpr_checkpoint* c, int64_t rows, int64_t out_features,
+                   int64_t in_features, Operand* a, Operand* steps, Operand* b) {
+    *b = operand(dy, dy_stride, 0, 2, 1, rows, out_features);
+    if (c) {
+        *a = operand(c->codes, c->code_stride, 0, 1, 1, rows, in_features);
+        *steps = operand(c->steps, c->step_stride, 0, 1, 1, rows,
+                         ceil_div(in_features, kBlockChannels));
+    } else {
+        *a = operand(x, x_stride, 0, 2, 1, rows, in_features);
+        *steps = operand(nullptr, 0, 0, 1, 0, 1, 1);
+    }
+}
+
+}  // namespace
+
+cudaError_t grouped_wait_failures(unsigned int* count) {
+    return cudaMemcpyFromSymbol(count, g_wait_failures, sizeof(*count));
+}
+
+}  // namespace dpr
+
+using namespace dpr;
+
+extern "C" {
+
+dpr_status dpr_grouped_linear_workspace(const void* x, int64_t x_stride, int64_t rows,
+                                        int64_t experts, const void* weight,
+                                        int64_t weight_stride, int64_t expert_stride,
+                                        int64_t out_features, int64_t in_features, int64_t* bytes) {
+    return product_workspace(false, x, x_stride, rows, experts, weight, weight_stride,
+                             expert_stride, out_features, in_features, bytes);
+}
+
+dpr_status dpr_grouped_linear(const void* x, int64_t x_stride, int64_t rows,
+                              const int32_t* offsets, int64_t experts, const void* weight,
+                              int64_t weight_stride, int64_t expert_stride, int64_t out_features,
+                              int64_t in_features, void* y, int64_t y_stride, int dtype,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
+    return product(false, x, x_stride, rows, offsets, experts, weight, weight_stride, expert_stride,
+                   out_features, in_features, y, y_stride, dtype, workspace, workspace_bytes,
+                   stream);
+}
+
+dpr_status dpr_grouped_linear_input_grad_workspace(const void* dy, int64_t dy_stride, int64_t rows,
+                                                   int64_t experts, const void* weight,
+                                                   int64_t weight_stride, int64_t expert_stride,
+                                                   int64_t out_features, int64_t in_features,
+                                                   int64_t* bytes) {
+    return product_workspace(true, dy, dy_stride, rows, experts, weight, weight_stride,
+                             expert_stride, out_features, in_features, bytes);
+}
+
+dpr_status dpr_grouped_linear_input_grad(const void* dy, int64_t dy_stride, int64_t rows,
+                                         const int32_t* offsets, int64_t experts,
+                                         const void* weight, int64_t weight_stride,
+                                         int64_t expert_stride, int64_t out_features,
+                                         int64_t in_features, void* dx, int64_t dx_stride,
+                                         int dtype, void* workspace, int64_t workspace_bytes,
+                                         void* stream) {
+    return product(true, dy, dy_stride, rows, offsets, experts, weight, weight_stride, expert_stride,
+                   out_features, in_features, dx, dx_stride, dtype, workspace, workspace_bytes,
+                   stream);
+}
+
+dpr_status dpr_grouped_linear_weight_grad_workspace(const void* dy, int64_t dy_stride,
+                                                    const void* x, int64_t x_stride,
+                                                    const dpr_checkpoint* x_ckpt, int64_t rows,
+                                                    int64_t experts, int64_t out_features,
+                                                    int64_t in_features, int64_t* bytes) {
+    if (!bytes) return DPR_ERR_INVALID_ARG;
+    *bytes = 0;
+    const dpr_status st = check_sizes(rows, experts, out_features, in_features);
+    if (st != DPR_OK || rows == 0) return st;
+    Operand a, steps, b;
+    grad_operands(dy, dy_stride, x, x_stride, x_ckpt, rows, out_features, in_features, &a, &steps,
+                  &b);
+    *bytes = a.bytes() + steps.bytes() + b.bytes();
+    return DPR_OK;
+}
+
+dpr_status dpr_grouped_linear_weight_grad(const void* dy, int64_t dy_stride, const void* x,
+                                          int64_t x_stride, const dpr_checkpoint* x_ckpt,
+                                          int64_t rows, const int32_t* offsets, int64_t experts,
+                                          int64_t out_features, int64_t in_features, void* dweight,
+                                          int64_t dweight_stride, int64_t expert_stride, int dtype,
+                                          int accumulate, void* workspace, int64_t workspace_bytes,
+                                          void* stream) {
+    int64_t need = 0;
+    dpr_status st = dpr_grouped_linear_weight_grad_workspace(
+        dy, dy_stride, x, x_stride, x_ckpt, rows, experts, out_features, in_features, &need);
+    if (st != DPR_OK) return st;
+    if (!dtype_ok(dtype)) return DPR_ERR_INVALID_ARG;
+    if ((st = check_experts(dweight, dweight_stride, expert_stride, experts, out_features,
+                            in_features, dtype, true)) != DPR_OK) return st;
+    if (!offsets) return DPR_ERR_INVALID_ARG;
+    if (!aligned(offsets, 4)) return DPR_ERR_ALIGNMENT;
+    SpanList outs, ins;
+    outs.add(dweight, uint64_t(dtype_size(dtype)) *
+                          uint64_t(experts_span(experts, expert_stride, out_features,
+                                                dweight_stride, in_features)));
+    ins.add(offsets, 4 * uint64_t(experts + 1));
+    if (rows > 0) {
+        if ((st = check_matrix(dy, dy_stride, out_features, DPR_BF16, false)) != DPR_OK) return st;
+        st = x_ckpt ? check_checkpoint(x_ckpt, in_features)
+                    : check_matrix(x, x_stride, in_features, DPR_BF16, false);
+        if (st != DPR_OK) return st;
+        if ((st = check_workspace(workspace, workspace_bytes, need)) != DPR_OK) return st;
+        if (need > 0) outs.add(workspace, uint64_t(need));
+        ins.add(dy, matrix_bytes(rows, out_features, dy_stride, 2));
+        if (x_ckpt) ins.add(*x_ckpt, rows, in_features);
+        else ins.add(x, matrix_bytes(rows, in_features, x_stride, 2));
+    }
+    if (!outs.disjoint() || outs.meets(ins)) return DPR_ERR_ALIAS;
+    if (rows == 0 && accumulate) return DPR_OK;
+
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    GroupedParams p = {};
+    p.offsets = offsets; p.experts = int(experts); p.rows = int(rows);
+    p.m_size = int(in_features); p.m_tiles = int(ceil_div(in_features, kTile));
+    p.n_size = int(out_features); p.n_tiles = int(ceil_div(out_features, kTile));
+    p.out = dweight; p.out_stride = dweight_stride; p.out_expert_stride = expert_stride;
+    p.out_bf16 = dtype == DPR_BF16; p.accumulate = accumulate != 0;
+    cudaError_t e = cudaSuccess;
+    if (rows > 0) {       // without tokens no tile loads anything
+        Operand a, steps, b;
+        grad_operands(dy, dy_stride, x, x_stride, x_ckpt, rows, out_features, in_features, &a,
+                      &steps, &b);
+        e = place(a, ws, s);
+        if (e == cudaSuccess) e = place(steps, ws, s);
+        if (e == cudaSuccess) e = place(b, ws, s);
+        if (e == cudaSuccess) e = encode(&p.a, a, 64, kDepth);
+        if (e == cudaSuccess && x_ckpt) e = encode(&p.steps, steps, 16, kDepth);
+        if (e == cudaSuccess) e = encode(&p.b, b, 64, kDepth);
+        if (e != cudaSuccess) return record_cuda_status(e);
+    }
+    const int64_t tiles = experts * p.m_tiles * p.n_tiles;
+    e = x_ckpt && rows > 0 ? launch_pairs<kWeightGradSaved>(p, tiles, s)
+                           : launch_pairs<kWeightGrad>(p, tiles, s);
+    return record_cuda_status(e);
+}
+
+}  // extern "C"

@@ -65,6 +65,50 @@ cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint6
     return e;
 }
 
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's function, without linking against the driver's library.
+cudaError_t encoder(EncodeTiled* fn) {
+    static std::atomic<void*> cached{nullptr};
+    void* f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                               cudaEnableDefault, &found);
+        if (e != cudaSuccess) return e;
+        if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+        cached.store(f, std::memory_order_release);
+    }
+    *fn = reinterpret_cast<EncodeTiled>(f);
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, int rank,
+                              const int64_t* dims, const int64_t* strides, const int* box,
+                              CUtensorMapSwizzle swizzle) {
+    EncodeTiled fn = nullptr;
+    const cudaError_t e = encoder(&fn);
+    if (e != cudaSuccess) return e;
+    cuuint64_t d[3] = {}, s[2] = {};
+    cuuint32_t b[3] = {}, ones[3] = {1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        d[i] = cuuint64_t(dims[i]);
+        b[i] = cuuint32_t(box[i]);
+        if (i > 0) s[i - 1] = cuuint64_t(strides[i - 1]);
+    }
+    const CUresult r = fn(map, type, cuuint32_t(rank), const_cast<void*>(p), d, s, b, ones,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 dpr_status check_matrix_size(int64_t rows, int64_t width) {
     if (rows < 0 || width < 1) return DPR_ERR_INVALID_ARG;
     if (rows > DPR_MAX_ROWS || width > DPR_MAX_WIDTH) return DPR_ERR_UNSUPPORTED;

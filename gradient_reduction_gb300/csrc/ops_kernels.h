@@ -4,9 +4,10 @@
 
 #include <atomic>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
-#include "../../include/dpr_ops.h"
+#include "../../include/dpr_step.h"
 #include "dpr_kernels.h"
 #include "host_checks.h"
 
@@ -21,6 +22,8 @@ bool programmatic_launch_enabled();   // defined beside launch_kernel
 
 // Waits that have run out in the layer norm's backward kernels.
 cudaError_t norm_wait_failures(unsigned int* count);
+// And in the products grouped by expert.
+cudaError_t grouped_wait_failures(unsigned int* count);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -79,6 +82,13 @@ cudaError_t resident_blocks(const void* kernel, int threads, int64_t* blocks);
 // Allows `kernel` that much dynamic shared memory, once per device (`done`: a
 // bit for each, the kernel's own).
 cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>* done);
+
+// The map of a tensor in memory that TMA reads in boxes: `rank` (2 or 3) sizes
+// and box sizes in elements from the innermost on, strides in bytes (multiples
+// of 16) from the second dimension on.  Outside the tensor zeros are read.
+cudaError_t encode_tensor_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, int rank,
+                              const int64_t* dims, const int64_t* strides, const int* box,
+                              CUtensorMapSwizzle swizzle);
 
 // Threads that share a row of `width` channels at `elems` per thread, and rows
 // per block of at least `block` threads: a power of two below 32 (at least

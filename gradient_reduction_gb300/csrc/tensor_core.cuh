@@ -108,6 +108,15 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// The same for a three-dimensional tensor.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                         uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 // Bulk copy of `bytes` (a multiple of 16) from a 16-byte aligned address.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -189,11 +198,17 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_
            (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// Instruction descriptor of kind::f16 with bf16 operands, fp32 accumulators
-// and both operands laid out along M and N (not K).
-__host__ __device__ constexpr uint32_t bf16_instruction(int m, int n) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | (uint32_t(n >> 3) << 17) |
-           (uint32_t(m >> 4) << 24);
+// Shared-memory operand whose rows are of M or N and hold 64 consecutive
+// elements along K in 128 swizzled bytes, 8 rows every 1024 bytes.  16 elements
+// further along K are 32 bytes further in every row.
+__device__ __forceinline__ uint64_t operand_along_k(uint32_t addr) { return operand(addr, 16, 1024); }
+
+// Instruction descriptor of kind::f16 with bf16 operands and fp32 accumulators;
+// the operands laid out along M and N, or along K.
+__host__ __device__ constexpr uint32_t bf16_instruction(int m, int n, bool a_along_m = true,
+                                                        bool b_along_n = true) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_along_m) << 15) |
+           (uint32_t(b_along_n) << 16) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
 }
 
 // D (+)= A B over both CTAs of the pair, issued by one thread of the first.

@@ -569,38 +569,13 @@ __global__ void __launch_bounds__(kThreads) zero_rows(const __grid_constant__ We
             put_grad(p, int64_t(o) * p.dw_stride + i, 0.0f);
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t encoder(EncodeTiled* fn) {
-    static std::atomic<void*> cached{nullptr};
-    void* f = cached.load(std::memory_order_acquire);
-    if (!f) {
-        cudaDriverEntryPointQueryResult found;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                                               cudaEnableDefault, &found);
-        if (e != cudaSuccess) return e;
-        if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
-        cached.store(f, std::memory_order_release);
-    }
-    *fn = reinterpret_cast<EncodeTiled>(f);
-    return cudaSuccess;
-}
-
 // A [rows, width] tensor read in boxes of `box` elements by kTokens rows.
-cudaError_t encode(EncodeTiled fn, CUtensorMap* map, CUtensorMapDataType type, int64_t size,
-                   const void* p, int64_t stride, int64_t rows, int64_t width, int box,
+cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, int64_t size, const void* p,
+                   int64_t stride, int64_t rows, int64_t width, int box,
                    CUtensorMapSwizzle swizzle) {
-    const cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(stride * size)};
-    const cuuint32_t boxes[2] = {cuuint32_t(box), cuuint32_t(kTokens)};
-    const cuuint32_t ones[2] = {1, 1};
-    const CUresult r = fn(map, type, 2, const_cast<void*>(p), dims, strides, boxes, ones,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    const int64_t dims[2] = {width, rows}, strides[1] = {stride * size};
+    const int boxes[2] = {box, kTokens};
+    return encode_tensor_map(map, type, p, 2, dims, strides, boxes, swizzle);
 }
 
 struct Plan {
@@ -761,16 +736,14 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
             e = repack<uint8_t>(x.steps, x.step_stride, ws, ss, rows, int(blocks), s);
         x.steps = reinterpret_cast<uint8_t*>(ws); x.step_stride = ss;
     }
-    EncodeTiled fn = nullptr;
-    if (e == cudaSuccess) e = encoder(&fn);
     if (e == cudaSuccess)
-        e = encode(fn, &p.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, dy_stride, rows,
-                   out_features, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+        e = encode(&p.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dy, dy_stride, rows, out_features,
+                   64, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e == cudaSuccess)
-        e = encode(fn, &p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.codes, x.code_stride, rows,
+        e = encode(&p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.codes, x.code_stride, rows,
                    in_features, 64, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (e == cudaSuccess)
-        e = encode(fn, &p.steps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.steps, x.step_stride, rows,
+        e = encode(&p.steps, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x.steps, x.step_stride, rows,
                    ceil_div(in_features, kBlockChannels), 16, CU_TENSOR_MAP_SWIZZLE_NONE);
     static std::atomic<uint64_t> allowed{0};
     if (e == cudaSuccess)
@@ -794,11 +767,12 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
 
 dpr_status dpr_device_wait_failures(uint32_t* count) {
     if (!count) return DPR_ERR_INVALID_ARG;
-    unsigned int v = 0, w = 0;
+    unsigned int v = 0, w = 0, g = 0;
     cudaError_t e = cudaDeviceSynchronize();   // a copy alone does not wait for non-blocking streams
     if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_wait_failures, sizeof(v));
     if (e == cudaSuccess) e = norm_wait_failures(&w);
-    *count = v + w;
+    if (e == cudaSuccess) e = grouped_wait_failures(&g);
+    *count = v + w + g;
     return record_cuda_status(e);
 }
 
