@@ -66,7 +66,15 @@ from ._operators import (  # noqa: F401
     dpr_linear_weight_grad,
 )
 from ._step import (  # noqa: F401
+    GradPlan,
+    dpr_grad_clip,
+    dpr_grad_norm,
+    dpr_grad_norm_clip,
+    dpr_grad_plan_create,
+    dpr_grad_plan_destroy,
     dpr_grouped_linear,
     dpr_grouped_linear_input_grad,
     dpr_grouped_linear_weight_grad,
+    dpr_rmsnorm_backward,
+    dpr_rmsnorm_forward,
 )

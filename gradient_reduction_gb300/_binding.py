@@ -1,4 +1,4 @@
-"""ctypes binding of libdpr (include/dpr.h, include/dpr_ops.h), with the same entry-point names.
+"""ctypes binding of libdpr (include/dpr.h, dpr_ops.h and dpr_step.h), with the same entry-point names.
 
 Argument marshalling only: tensors are turned into device pointers and sizes,
 the current CUDA stream is passed along, and a non-zero status becomes a
@@ -94,6 +94,18 @@ _SIGS = {
     "dpr_device_wait_failures": [ctypes.POINTER(ctypes.c_uint32)],
     "dpr_linear_weight_grad": [_c_p, _i64, _c_p, _i64, _i64, _i64, _c_p, _i64, _int, _int, _c_p,
                                _i64, _c_p],
+    "dpr_rmsnorm_forward": [_c_p, _i64, _c_p, _i64, _i64, _i64, _int, _c_p, _int, ctypes.c_float,
+                            _c_p, _i64, _c_p, _i64, _c_p, _c_p, _c_p, _c_p],
+    "dpr_rmsnorm_backward_workspace": [_i64, _i64, _i64p],
+    "dpr_rmsnorm_backward": [_c_p, _i64, _c_p, _i64, _c_p, _i64, _c_p, _i64, _i64, _int, _c_p, _int,
+                             _c_p, _c_p, _i64, _c_p, _int, _int, _c_p, _i64, _c_p],
+    "dpr_grad_plan_create": [ctypes.POINTER(_c_p), _int, _pp, ctypes.POINTER(_int), _pp,
+                             ctypes.POINTER(_int), _i64p, _c_p],
+    "dpr_grad_plan_destroy": [_c_p],
+    "dpr_grad_norm_workspace": [_c_p, _i64p],
+    "dpr_grad_norm": [_c_p, ctypes.c_float, _c_p, _c_p, _i64, _c_p],
+    "dpr_grad_clip": [_c_p, ctypes.c_float, ctypes.c_float, _c_p, _c_p],
+    "dpr_grad_norm_clip": [_c_p, ctypes.c_float, ctypes.c_float, _c_p, _c_p, _i64, _c_p],
     "dpr_grouped_linear_workspace": [_c_p, _i64, _i64, _i64, _c_p, _i64, _i64, _i64, _i64, _i64p],
     "dpr_grouped_linear": [_c_p, _i64, _i64, _c_p, _i64, _c_p, _i64, _i64, _i64, _i64, _c_p, _i64,
                            _int, _c_p, _i64, _c_p],

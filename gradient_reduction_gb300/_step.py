@@ -15,6 +15,79 @@ from ._operators import (_DTYPES, _checkpoint_arg, _code, _device, _handle, _mat
                          _vector, _workspace, _workspace_bytes, _wrong_device, _wrong_shape)
 
 
+def _optional(t, rows: int, width: int, dtype, what: str, dev: int):
+    """(address, row stride) of a matrix of this shape and type; zeros for None."""
+    if t is None:
+        return 0, 0
+    p, r, w, stride = _matrix(t, what, dev)
+    if r != rows or w != width:
+        _wrong_shape(what, r, w, rows, width)
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: need {dtype}, got {t.dtype}")
+    return p, stride
+
+
+def _saved(c, what: str, rows: int, width: int, dev: int):
+    return None if c is None else ctypes.byref(_checkpoint_arg(c, what, rows, width, dev))
+
+
+def dpr_rmsnorm_forward(x: torch.Tensor, weight, eps: float, y=None, rstd=None, residual=None,
+                        h=None, h_checkpoint=None, y_checkpoint=None, stream=None) -> None:
+    """h = x + residual (rounded to their type; x without a residual) and y = h *
+    rstd * weight, rstd = 1 / sqrt(mean(h^2) + eps), along the last dimension;
+    weight (bf16 or fp32) may be None.  h, where the residual stream goes on,
+    may be x or residual; y may be x or residual too.  rstd ([rows] fp32) is
+    what the backward pass needs.  The checkpoints are written in the same pass
+    as dpr_checkpoint_save(h) and (y) would; with y_checkpoint y may be None."""
+    dev = _device(x, "x")
+    px, rows, width, sx = _matrix(x, "x", dev)
+    pr, sr = _optional(residual, rows, width, x.dtype, "residual", dev)
+    ph, sh = _optional(h, rows, width, x.dtype, "h", dev)
+    py, sy = _optional(y, rows, width, x.dtype, "y", dev)
+    st = lib().dpr_rmsnorm_forward(
+        px, sx, pr, sr, rows, width, _code(x, "x"), _vector(weight, width, "weight", dev),
+        0 if weight is None else _code(weight, "weight"), eps, ph, sh, py, sy,
+        _statistic(rstd, rows, "rstd", dev), _saved(h_checkpoint, "h_checkpoint", rows, width, dev),
+        _saved(y_checkpoint, "y_checkpoint", rows, width, dev), _handle(stream, dev))
+    if st:
+        _check("dpr_rmsnorm_forward", st)
+
+
+def dpr_rmsnorm_backward(dy: torch.Tensor, h, weight, rstd: torch.Tensor, dx: torch.Tensor,
+                         dweight=None, dh=None, accumulate: bool = False, workspace=None,
+                         stream=None) -> None:
+    """dx and dweight of dpr_rmsnorm_forward.  `h` is the forward's sum (its x
+    without a residual) or its Checkpoint; `dh` the gradient that reaches h
+    past the norm, added to dx.  dx, the gradient of x and of the residual, may
+    be dy, dh or h.  dweight (bf16 or fp32 [width]) is added to with
+    `accumulate`."""
+    dev = _device(dy, "dy")
+    pd, rows, width, sd = _matrix(dy, "dy", dev)
+    po, so = _optional(dx, rows, width, dy.dtype, "dx", dev)
+    if not po and rows > 0:
+        raise ValueError("dx is needed")
+    pe, se = _optional(dh, rows, width, dy.dtype, "dh", dev)
+    ph = sh = 0
+    ref = None
+    if isinstance(h, torch.Tensor):
+        ph, sh = _optional(h, rows, width, dy.dtype, "h", dev)
+    else:
+        ref = ctypes.byref(_checkpoint_arg(h, "h", rows, width, dev))
+    if rstd is None:
+        raise ValueError("rstd of the forward pass is needed")
+    nbytes = _workspace_bytes("dpr_rmsnorm_backward_workspace", rows, width)
+    handle = _handle(stream, dev)
+    ws = _workspace(workspace, nbytes, stream, handle, dev)
+    st = lib().dpr_rmsnorm_backward(
+        pd, sd, pe, se, ph, sh, ref, rows, width, _code(dy, "dy"),
+        _vector(weight, width, "weight", dev), 0 if weight is None else _code(weight, "weight"),
+        _statistic(rstd, rows, "rstd", dev), po, so, _vector(dweight, width, "dweight", dev),
+        0 if dweight is None else _code(dweight, "dweight"), 1 if accumulate else 0,
+        0 if ws is None else ws.data_ptr(), nbytes, handle)
+    if st:
+        _check("dpr_rmsnorm_backward", st)
+
+
 def _experts(t: torch.Tensor, what: str, dev: int):
     """(address, experts, rows, width, row stride, expert stride) of [experts, rows, width]."""
     if t.get_device() != dev:
@@ -125,3 +198,118 @@ def dpr_grouped_linear_weight_grad(dy: torch.Tensor, offsets: torch.Tensor, x,
         nbytes, handle)
     if st:
         _check("dpr_grouped_linear_weight_grad", st)
+
+
+class GradPlan:
+    """Owns a dpr_grad_plan and keeps its tensors alive."""
+
+    def __init__(self, handle: int, device: int, workspace_bytes: int, tensors: tuple):
+        self.handle = handle
+        self.device = device
+        self.workspace_bytes = workspace_bytes
+        self._tensors = tensors
+
+    def close(self):
+        if self.handle:
+            h, self.handle = self.handle, None
+            _check("dpr_grad_plan_destroy", lib().dpr_grad_plan_destroy(h))
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _dtypes(ts: Sequence[torch.Tensor], what: str, dev: int):
+    """Type codes of contiguous tensors on the current device."""
+    codes = (ctypes.c_int * len(ts))()
+    for i, t in enumerate(ts):
+        if t.get_device() != dev:
+            _wrong_device(t, what)
+        c = _DTYPES.get(t.dtype)
+        if c is None or not t.is_contiguous():
+            raise ValueError(f"{what}: need contiguous torch.bfloat16 or torch.float32 tensors")
+        codes[i] = c
+    return codes
+
+
+def dpr_grad_plan_create(grads: Sequence[torch.Tensor], outs=None, stream=None) -> GradPlan:
+    """A list of gradients (contiguous, bf16 or fp32, any shapes) whose norm is
+    taken and that are clipped into `outs` (as many elements each, bf16 or
+    fp32; without it, in place)."""
+    grads = list(grads)
+    n = len(grads)
+    dev = _device(grads[0], "grads") if n else torch.cuda.current_device()
+    src = _dtypes(grads, "grads", dev)
+    numel = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
+    dst = to = None
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError(f"outs: expected {n} tensors, got {len(outs)}")
+        to = _dtypes(outs, "outs", dev)
+        for g, o in zip(grads, outs):
+            if o.numel() != g.numel():
+                raise ValueError(f"outs: need {g.numel()} elements, got {o.numel()}")
+        dst = _ptrs(outs)
+    h = ctypes.c_void_p()
+    _check("dpr_grad_plan_create",
+           lib().dpr_grad_plan_create(ctypes.byref(h), n, _ptrs(grads), src, dst, to, numel,
+                                      _stream(stream)))
+    nbytes = ctypes.c_int64()
+    plan = GradPlan(h.value, dev, 0, (grads, outs))
+    _check("dpr_grad_norm_workspace", lib().dpr_grad_norm_workspace(h, ctypes.byref(nbytes)))
+    plan.workspace_bytes = nbytes.value
+    return plan
+
+
+def dpr_grad_plan_destroy(plan: GradPlan) -> None:
+    plan.close()
+
+
+def _norm(plan: GradPlan, norm: torch.Tensor) -> int:
+    if plan.handle is None:
+        raise ValueError("the plan is closed")
+    return _statistic(norm, 1, "norm", _device(norm, "norm"))
+
+
+def dpr_grad_norm(plan: GradPlan, norm: torch.Tensor, scale: float = 1.0, workspace=None,
+                  stream=None) -> None:
+    """norm (one fp32 number on the device) = scale * sqrt(sum of squares of all
+    elements of the plan's gradients)."""
+    pn = _norm(plan, norm)
+    handle = _handle(stream, plan.device)
+    ws = _workspace(workspace, plan.workspace_bytes, stream, handle, plan.device)
+    st = lib().dpr_grad_norm(plan.handle, scale, pn, 0 if ws is None else ws.data_ptr(),
+                             plan.workspace_bytes, handle)
+    if st:
+        _check("dpr_grad_norm", st)
+
+
+def dpr_grad_clip(plan: GradPlan, norm: torch.Tensor, max_norm: float, scale: float = 1.0,
+                  stream=None) -> None:
+    """Every gradient times scale, and times max_norm / norm where norm is larger
+    than max_norm; `norm` as dpr_grad_norm leaves it, or joined with others'."""
+    pn = _norm(plan, norm)
+    st = lib().dpr_grad_clip(plan.handle, scale, max_norm, pn, _handle(stream, plan.device))
+    if st:
+        _check("dpr_grad_clip", st)
+
+
+def dpr_grad_norm_clip(plan: GradPlan, norm: torch.Tensor, max_norm: float, scale: float = 1.0,
+                       workspace=None, stream=None) -> None:
+    """dpr_grad_norm and dpr_grad_clip in one call."""
+    pn = _norm(plan, norm)
+    handle = _handle(stream, plan.device)
+    ws = _workspace(workspace, plan.workspace_bytes, stream, handle, plan.device)
+    st = lib().dpr_grad_norm_clip(plan.handle, scale, max_norm, pn,
+                                  0 if ws is None else ws.data_ptr(), plan.workspace_bytes, handle)
+    if st:
+        _check("dpr_grad_norm_clip", st)

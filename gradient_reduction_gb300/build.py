@@ -24,7 +24,8 @@ LIB = os.path.join(LIBDIR, "libdpr.so")
 SOURCES = ["dpr_api.cu", "reduce_kernels.cu", "gather_kernels.cu", "coalesced.cu",
            "pipeline.cu", "cost_model.cpp", "flatten_noalloc.cu", "fragments.cu", "requests.cu",
            "ops_host.cu", "layernorm.cu", "layernorm_backward.cu", "checkpoint.cu",
-           "weight_grad.cu", "grouped.cu"]
+           "weight_grad.cu", "grouped.cu", "rmsnorm.cu", "rmsnorm_backward.cu",
+           "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC,-O2",
          "-I", os.path.join(ROOT, "include")]

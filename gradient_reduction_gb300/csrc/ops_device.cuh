@@ -463,6 +463,17 @@ __device__ __forceinline__ void save_row(const Raw<T, V> (&raw)[NV], int width, 
     }
 }
 
+// Two codes, in the low bytes of the halves of `w`, as bf16: the seven low
+// bits on top of 128, less 128 or (sign bit) 256, times the step.
+__device__ __forceinline__ uint32_t restore_pair(uint32_t w, uint32_t step2) {
+    const uint32_t low = (w & 0x007F007Fu) | 0x43004300u;
+    const uint32_t base = (w & 0x00800080u) | 0x43004300u;
+    uint32_t v, r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(low), "r"(base));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(step2));
+    return r;
+}
+
 // V codes of a row.
 template <int V>
 struct CodeRaw {

@@ -22,7 +22,8 @@ bool programmatic_launch_enabled();   // defined beside launch_kernel
 
 // Waits that have run out in the layer norm's backward kernels.
 cudaError_t norm_wait_failures(unsigned int* count);
-// And in the products grouped by expert.
+// And in the RMS norm's, and in the products grouped by expert.
+cudaError_t rms_wait_failures(unsigned int* count);
 cudaError_t grouped_wait_failures(unsigned int* count);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

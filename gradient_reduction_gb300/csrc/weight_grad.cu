@@ -137,17 +137,6 @@ __device__ __forceinline__ void tile_origin(const WeightGradParams& p, int tile,
     o = (group * 8 + rest % height) * kTile;
 }
 
-// Two codes, in the low bytes of the halves of `w`, as bf16: the seven low
-// bits on top of 128, less 128 or (sign bit) 256, times the step.
-__device__ __forceinline__ uint32_t restore_pair(uint32_t w, uint32_t step2) {
-    const uint32_t low = (w & 0x007F007Fu) | 0x43004300u;
-    const uint32_t base = (w & 0x00800080u) | 0x43004300u;
-    uint32_t v, r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(low), "r"(base));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(step2));
-    return r;
-}
-
 __device__ __forceinline__ void put_grad(const WeightGradParams& p, int64_t at, float v) {
     if (p.dw_bf16) {
         uint16_t* d = static_cast<uint16_t*>(p.dw) + at;
@@ -767,12 +756,13 @@ dpr_status dpr_linear_weight_grad(const void* dy, int64_t dy_stride, const dpr_c
 
 dpr_status dpr_device_wait_failures(uint32_t* count) {
     if (!count) return DPR_ERR_INVALID_ARG;
-    unsigned int v = 0, w = 0, g = 0;
+    unsigned int v = 0, w = 0, r = 0, g = 0;
     cudaError_t e = cudaDeviceSynchronize();   // a copy alone does not wait for non-blocking streams
     if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_wait_failures, sizeof(v));
     if (e == cudaSuccess) e = norm_wait_failures(&w);
+    if (e == cudaSuccess) e = rms_wait_failures(&r);
     if (e == cudaSuccess) e = grouped_wait_failures(&g);
-    *count = v + w + g;
+    *count = v + w + r + g;
     return record_cuda_status(e);
 }
 

@@ -130,7 +130,7 @@ dpr_status dpr_grouped_linear_weight_grad(const void* dy, int64_t dy_stride, con
  *   out     = g * factor
  * `scale` (positive, finite) undoes a loss scale or averages; `norm` is one
  * fp32 number on the device.  The sum neither overflows nor underflows,
- * whatever the elements' magnitudes.  An infinite norm clips to zero (and the
+ * whatever the elements' magnitudes (a norm beyond fp32 is infinite).  An infinite norm clips to zero (and the
  * infinities to NaN), a NaN makes every gradient NaN: a diverged step shows.
  *
  * The list is recorded once: n tensors of numel[i] elements (0 allowed) at
