@@ -126,15 +126,17 @@ struct Squares {
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) any |= __float_as_uint(f[i]) << 1;
         if (any == 0) return;             // zeros
-        const bool small = s < 1.0f;      // else huge, infinite or NaN
-        const float by = small ? 0x1p96f : 0x1p-96f;
+        // All below 2^-50 then, and 2^-53 at least after scaling; or (huge, infinite or NaN) one of
+        // 2^28 at least, whose square is 2^-88 after scaling, and the largest squares' sum 2^116.
+        const bool small = s < 1.0f;
+        const float by = small ? 0x1p96f : 0x1p-72f;
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
             const float v = __fmul_rn(f[i], by);
             sum = __fmaf_rn(v, v, sum);
         }
-        rest += double(sum) * (small ? 0x1p-192 : 0x1p192);
+        rest += double(sum) * (small ? 0x1p-192 : 0x1p144);
     }
     __device__ __forceinline__ double value() const { return double(hi) + double(lo) + rest; }
 };

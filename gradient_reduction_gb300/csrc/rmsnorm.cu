@@ -230,9 +230,9 @@ extern "C" dpr_status dpr_rmsnorm_forward(const void* x, int64_t x_stride, const
     dpr_status st = check_matrix_size(rows, width);
     if (st != DPR_OK) return st;
     if (!dtype_ok(dtype) || !dtype_ok(param_dtype) || !(eps >= 0.0f)) return DPR_ERR_INVALID_ARG;
+    if (rows == 0) return DPR_OK;
     if (h && !residual) return DPR_ERR_INVALID_ARG;
     if (!y && !y_ckpt) return DPR_ERR_INVALID_ARG;
-    if (rows == 0) return DPR_OK;
     const int64_t ps = dtype_size(param_dtype), es = dtype_size(dtype);
     if ((st = check_matrix(x, x_stride, width, dtype, false)) != DPR_OK) return st;
     if (residual && (st = check_matrix(residual, residual_stride, width, dtype, false)) != DPR_OK)

@@ -1,0 +1,257 @@
+"""Linear layers of experts against their definitions in 64 bits (tests/step_reference.py): sizes
+that end inside tiles, experts without tokens, rows that belong to nobody (left as they were,
+whatever they hold), odd strides and addresses, checkpoints, accumulation, empty calls."""
+import pytest
+import torch
+
+import gradient_reduction_gb300 as dpr
+from tests import gpu_helpers as H
+from tests import operators_reference as R
+from tests import step_reference as S
+from tests.test_gpu_operators import BF, F32, Placed, checkpoint, gen
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+def offsets_of(counts, first=0):
+    out = [first]
+    for c in counts:
+        out.append(out[-1] + c)
+    return out
+
+
+def device_offsets(offs):
+    return torch.tensor(offs, dtype=torch.int32, device="cuda")
+
+
+def randn(*shape, seed=0, scale=1.0):
+    return (scale * torch.randn(*shape, generator=gen(seed))).to(BF)
+
+
+# (tokens of each expert, out_features, in_features): one token, tiles that end inside, several
+# tiles an expert, empty experts at both ends, sums of several accumulators
+SIZES = [
+    ((1,), 8, 8), ((1,), 1, 1), ((3,), 40, 72), ((64,), 256, 64), ((65, 1), 264, 120),
+    ((0, 5, 0, 0, 257, 31, 0), 136, 200), ((256, 256), 512, 256), ((513, 100), 96, 1032),
+    ((33,) * 9, 300, 24), ((1000, 24), 256, 2056), ((2, 3000), 72, 64), ((0, 0, 7), 1001, 1003),
+    ((129, 0, 1), 67, 515),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("counts,o,i", SIZES)
+@pytest.mark.parametrize("input_grad", [False, True], ids=["product", "input_grad"])
+def test_product(input_grad, counts, o, i, dtype):
+    H.device()
+    offs = offsets_of(counts, 2)
+    rows = offs[-1] + 3                      # rows in front of the first expert and behind the last
+    have, give = (o, i) if input_grad else (i, o)
+    x, w = randn(rows, have, seed=1), randn(len(counts), o, i, seed=2)
+    x[:2] = NAN
+    x[offs[-1]:] = NAN
+    for e, c in enumerate(counts):
+        if c == 0:
+            w[e] = NAN
+    px, pw = Placed(rows, have, BF, -have % 8, 0, x), Placed(len(counts) * o, i, BF, -i % 8, 0,
+                                                             w.view(-1, i))
+    py = Placed(rows, give, dtype, 3)
+    py.view.fill_(7)
+    f = dpr.dpr_grouped_linear_input_grad if input_grad else dpr.dpr_grouped_linear
+    f(px.view, device_offsets(offs), pw.view.unflatten(0, (len(counts), o)), py.view)
+    want, size = S.product(x, offs, w, input_grad)
+    mine = slice(offs[0], offs[-1])
+    R.check(py.view[mine], want[mine], S.sum_bound(want, size, have, dtype)[mine], "out")
+    assert bool((py.view[:2] == 7).all()) and bool((py.view[offs[-1]:] == 7).all())
+    for p, what in ((px, "x"), (pw, "weight"), (py, "out")):
+        p.check_guards(what)
+
+
+@pytest.mark.parametrize("saved", [False, True], ids=["stored", "saved"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("counts,o,i", SIZES)
+def test_weight_gradient(counts, o, i, dtype, saved):
+    H.device()
+    offs = offsets_of(counts, 2)
+    rows, experts = offs[-1] + 3, len(counts)
+    dy, x = randn(rows, o, seed=1), randn(rows, i, seed=2)
+    for t in (dy, x):
+        t[:2] = NAN
+        t[offs[-1]:] = NAN
+    pd, px = Placed(rows, o, BF, -o % 8, 0, dy), Placed(rows, i, BF, -i % 8, 0, x)
+    source, xx = px.view, x.double()
+    if saved:
+        pc, ps, source = checkpoint(rows, i)
+        codes, steps = R.encode(x.double())
+        pc.view.copy_(codes)
+        ps.view.copy_(steps)
+        xx = R.decode(codes, steps)
+    pw = Placed(experts * o, i, dtype, 5)
+    dw = pw.view.unflatten(0, (experts, o))
+    dw.fill_(NAN)
+    dpr.dpr_grouped_linear_weight_grad(pd.view, device_offsets(offs), source, dw)
+    want, size = S.weight_grads(dy, offs, xx)
+    bound = S.sum_bound(want, size, max(counts), dtype)
+    R.check(dw, want, bound, "dweight")
+    old = torch.randn(experts, o, i, generator=gen(3)).to(dtype)
+    dw.copy_(old)
+    dpr.dpr_grouped_linear_weight_grad(pd.view, device_offsets(offs), source, dw, accumulate=True)
+    total = want + old.double()
+    R.check(dw, total, bound + (R.ROUND[dtype] + R.U) * (total.abs() + old.double().abs()), "added")
+    for e, c in enumerate(counts):
+        if c == 0:
+            assert torch.equal(dw[e].cpu(), old[e])
+    for p, what in ((pd, "dy"), (px, "x"), (pw, "dweight")):
+        p.check_guards(what)
+
+
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (3, 0), (0, 1), (5, 7)])
+def test_strides_and_addresses(pad, shift):
+    """Rows that TMA reads where they are and rows that are copied first, for every operand; weights
+    whose matrices lie apart, and one matrix for all experts."""
+    H.device()
+    counts, o, i = (70, 0, 9), 136, 264
+    offs, rows, experts = offsets_of(counts), sum(counts), len(counts)
+    x, dy, w = randn(rows, i, seed=1), randn(rows, o, seed=2), randn(experts, o, i, seed=3)
+    px, pd = Placed(rows, i, BF, pad, shift, x), Placed(rows, o, BF, pad, shift, dy)
+    apart = Placed(experts, (o + 1) * (i + pad), BF, 16, shift)
+    pw = apart.view.unflatten(1, (o + 1, i + pad))[:, 1:, :i]
+    pw.copy_(w)
+    at = device_offsets(offs)
+    for f, p, tr, give in ((dpr.dpr_grouped_linear, px, False, o),
+                           (dpr.dpr_grouped_linear_input_grad, pd, True, i)):
+        out = Placed(rows, give, F32, pad, shift)
+        f(p.view, at, pw, out.view)
+        want, size = S.product(p.view.cpu(), offs, w, tr)
+        R.check(out.view, want, S.sum_bound(want, size, 264, F32), "out")
+        out.check_guards("out")
+        f(p.view, at, pw[:1].expand(experts, o, i), out.view)
+        want, size = S.product(p.view.cpu(), offs, w[:1].expand(experts, o, i), tr)
+        R.check(out.view, want, S.sum_bound(want, size, 264, F32), "shared weight")
+    pc, ps, saved = checkpoint(rows, i, pad, shift)
+    codes, steps = R.encode(x.double())
+    pc.view.copy_(codes)
+    ps.view.copy_(steps)
+    for source, xx in ((px.view, x.double()), (saved, R.decode(codes, steps))):
+        dw = apart.view.unflatten(1, (o + 1, i + pad))[:, :o, :i]
+        dpr.dpr_grouped_linear_weight_grad(pd.view, at, source, dw)
+        want, size = S.weight_grads(dy, offs, xx)
+        R.check(dw, want, S.sum_bound(want, size, 70, BF), "dweight")
+    apart.check_guards("weights")
+
+
+def test_one_row_for_all_tokens():
+    H.device()
+    w, x = randn(2, 72, 64, seed=1), randn(1, 64, seed=2)
+    out = torch.empty(40, 72, device="cuda")
+    dpr.dpr_grouped_linear(x.cuda().expand(40, 64), device_offsets([0, 10, 40]), w.cuda(), out)
+    want, size = S.product(x.expand(40, 64), [0, 10, 40], w, False)
+    R.check(out, want, S.sum_bound(want, size, 64, F32), "out")
+
+
+def test_offsets_are_limited_to_the_rows():
+    """What a broken router leaves is read and written within the rows that there are."""
+    H.device()
+    x, w = randn(10, 64, seed=1), randn(5, 72, 64, seed=2)
+    for offs in ([-5, 3, 3, 100, 50, 2 ** 31 - 1], [-2 ** 31, -1, 0, 10, 10, 10], [20, 30, 5, 5, 5, 5]):
+        out = Placed(10, 72, F32)
+        out.view.fill_(7)
+        dpr.dpr_grouped_linear(x.cuda(), device_offsets(offs), w.cuda(), out.view)
+        want, size = S.product(x, offs, w, False)
+        owned = ~want[:, 0].isnan()
+        R.check(out.view[owned.cuda()], want[owned], S.sum_bound(want, size, 64, F32)[owned], "out")
+        assert bool((out.view[~owned.cuda()] == 7).all())
+        out.check_guards("out")
+        dw = torch.empty(5, 72, 64, device="cuda")
+        dpr.dpr_grouped_linear_weight_grad(out.view.to(BF), device_offsets(offs), x.cuda(), dw)
+        want, size = S.weight_grads(out.view.to(BF).cpu(), offs, x)
+        R.check(dw, want, S.sum_bound(want, size, 10, F32), "dweight")
+
+
+def test_infinities_and_nan_stay_with_their_tokens():
+    """A token's NaN reaches its own output row alone, and of the weight gradients its expert's
+    alone, also where its neighbours share the step of the sum that the experts' border cuts."""
+    H.device()
+    offs = [0, 70, 100, 130]
+    x, dy, w = randn(130, 72, seed=1), randn(130, 80, seed=2), randn(3, 80, 72, seed=3)
+    x[75, 3], x[80, 5], dy[90, 7] = NAN, float("inf"), NAN
+    out = torch.empty(130, 80, device="cuda")
+    dpr.dpr_grouped_linear(x.cuda(), device_offsets(offs), w.cuda(), out)
+    want, size = S.product(x, offs, w, False)
+    ok = torch.ones(130, dtype=torch.bool)
+    ok[[75, 80]] = False
+    R.check(out.cpu()[ok], want[ok], S.sum_bound(want, size, 72, F32)[ok], "out")
+    assert bool(out[75].isnan().all()) and not bool(out[80].isfinite().any())
+    dw = torch.empty(3, 80, 72, device="cuda")
+    saved = dpr.dpr_checkpoint_empty(130, 72)
+    dpr.dpr_checkpoint_save(x.cuda(), saved)
+    restored = torch.empty(130, 72, dtype=BF, device="cuda")
+    dpr.dpr_checkpoint_load(saved, restored)
+    for source, xx in ((x.cuda(), x), (saved, restored.cpu())):
+        dpr.dpr_grouped_linear_weight_grad(dy.cuda(), device_offsets(offs), source, dw)
+        want, size = S.weight_grads(dy, offs, xx)
+        for e in (0, 2):
+            R.check(dw[e], want[e], S.sum_bound(want[e], size[e], 70, F32), f"expert {e}")
+        assert bool(dw[1, 7].isnan().all()) and bool(dw[1, :, 3].isnan().all())
+
+
+def test_calls_without_tokens():
+    H.device()
+    w = randn(3, 72, 64).cuda()
+    at = device_offsets([0, 0, 0, 0])
+    none, y = torch.empty(0, 64, dtype=BF, device="cuda"), torch.empty(0, 72, device="cuda")
+    dpr.dpr_grouped_linear(none, at, w, y)
+    dpr.dpr_grouped_linear_input_grad(y.to(BF), at, w, none)
+    dw = torch.full((3, 72, 64), 5.0, device="cuda")
+    dpr.dpr_grouped_linear_weight_grad(y.to(BF), at, none, dw, accumulate=True)
+    assert bool((dw == 5).all())
+    dpr.dpr_grouped_linear_weight_grad(y.to(BF), at, none, dw)
+    assert not dw.any()
+    # rows, but no expert has any
+    x = torch.full((40, 64), NAN, dtype=BF, device="cuda")
+    y = torch.full((40, 72), 7.0, device="cuda")
+    dpr.dpr_grouped_linear(x, at, w, y)
+    assert bool((y == 7).all())
+    for source in (x, dpr.dpr_checkpoint_empty(40, 64)):
+        dw.fill_(5)
+        dpr.dpr_grouped_linear_weight_grad(y.to(BF), at, source, dw)
+        assert not dw.any()
+
+
+def test_many_experts():
+    """The most that a call takes, most of them with a token or none."""
+    H.device()
+    counts = [(e * 7) % 4 for e in range(1024)]
+    offs = offsets_of(counts)
+    x, w = randn(offs[-1], 64, seed=1), randn(1024, 72, 64, seed=2)
+    out = torch.empty(offs[-1], 72, device="cuda")
+    dpr.dpr_grouped_linear(x.cuda(), device_offsets(offs), w.cuda(), out)
+    want, size = S.product(x, offs, w, False)
+    R.check(out, want, S.sum_bound(want, size, 64, F32), "out")
+    dw = torch.empty(1024, 72, 64, device="cuda")
+    dpr.dpr_grouped_linear_weight_grad(out.to(BF), device_offsets(offs), x.cuda(), dw)
+    want, size = S.weight_grads(out.to(BF).cpu(), offs, x)
+    R.check(dw, want, S.sum_bound(want, size, 3, F32), "dweight")
+
+
+def test_binding_refusals():
+    H.device()
+    x, w = randn(8, 64).cuda(), randn(2, 72, 64).cuda()
+    y, at = torch.empty(8, 72, device="cuda"), device_offsets([0, 3, 8])
+    for bad in ((x, at.long(), w, y), (x, at[:2], w, y), (x, at, w[0], y), (x[:, :63], at, w, y),
+                (x, at, w, y[:7]), (x, at, w, y[:, :71]), (x.float(), at, w, y),
+                (x, at, w.float(), y), (x, at, w, y.half()), (x, at.cpu(), w, y)):
+        with pytest.raises(ValueError):
+            dpr.dpr_grouped_linear(*bad)
+    dw = torch.empty(2, 72, 64, device="cuda")
+    dy = torch.empty(8, 72, dtype=BF, device="cuda")
+    for bad in ((dy, at, x[:7], dw), (dy, at, x.float(), dw), (dy[:, :71], at, x, dw),
+                (dy, at, x, dw[:1]), (dy, at, x, dw.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            dpr.dpr_grouped_linear_weight_grad(*bad)
+
+
+def test_no_wait_ran_out():
+    H.device()
+    assert dpr.dpr_device_wait_failures() == 0
