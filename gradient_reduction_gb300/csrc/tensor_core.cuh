@@ -135,6 +135,12 @@ __device__ __forceinline__ void send4(uint32_t to, const float (&v)[4], uint32_t
         : "memory");
 }
 
+// A double to shared memory of a CTA of the cluster (an address from map_to),
+// there for the others after the next cluster_sync.
+__device__ __forceinline__ void send_double(uint32_t to, double v) {
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(v) : "memory");
+}
+
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

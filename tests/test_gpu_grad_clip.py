@@ -181,10 +181,15 @@ def test_refusals():
             dpr.dpr_grad_norm(plan, bad)
     with pytest.raises(dpr.DprError):
         dpr.dpr_grad_clip(plan, out[7:8], 1.0)
-    with pytest.raises(dpr.DprError):
-        dpr.dpr_grad_norm(plan, norm, workspace=out)
+    # a list of more tiles than one launch takes needs a workspace
+    large, result = torch.ones(1 << 20, device="cuda"), torch.empty(1 << 20, device="cuda")
+    needs = dpr.dpr_grad_plan_create([large], [result])
+    assert plan.workspace_bytes == 0 and 0 < needs.workspace_bytes <= 1 << 16
+    for bad in (large, result):
+        with pytest.raises(dpr.DprError):
+            dpr.dpr_grad_norm(needs, norm, workspace=bad)
     with pytest.raises(ValueError):
-        dpr.dpr_grad_norm(plan, norm, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        dpr.dpr_grad_norm(needs, norm, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     for bad in (norm.double(), torch.empty(2, device="cuda"), torch.empty(1)):
         with pytest.raises(ValueError):
             dpr.dpr_grad_norm(plan, bad)
