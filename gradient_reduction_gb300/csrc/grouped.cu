@@ -517,41 +517,82 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     if (warp == 1) tc::tmem_free(tmem, 512);
 }
 
-// Rows copied to 16-byte-aligned ones, for inputs that TMA cannot read.  Row r
-// of `rows` is row r % inner of matrix r / inner; four loads of a thread in
-// flight before its stores.  The source is not declared __restrict__: a
-// programmatic launch lives while the grid before it writes.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-repack_matrices(const T* from, int64_t from_stride, int64_t from_outer, T* to, int64_t to_stride,
-                int64_t rows, int64_t inner, int width) {
+// An operand copied to 16-byte-aligned rows, for inputs that TMA cannot read.
+// Row r is row r % inner of matrix r / inner.
+struct Copy {
+    const void* from;
+    int64_t stride, outer;       // bytes, from row to row and from matrix to matrix
+    void* to;
+    int64_t to_stride;           // bytes, a multiple of 16
+    int64_t rows, inner;
+    int64_t row0;                // of the call's rows: the operands copied before
+    int bytes;                   // of a row
+    int weights;                 // matrix e is not read when expert e has no tokens
+};
+struct CopyParams {
+    Copy op[3];
+    int64_t rows;                // of all operands
+    const int32_t* offsets;
+    int tokens;
+};
+
+// A warp copies a row: 16 bytes a lane and turn, from the aligned 16 bytes that
+// hold their beginning and (the next lane's) their end.  Only those that hold a
+// byte of the row are read.  Behind the row, up to the next 16 bytes, follows
+// what was there: TMA's maps end with the row.  All operands of a call in one
+// launch: 2047 tokens, 5 x 1001 x 1003 from the checkpoint, 21.3 us with a launch for
+// each and single elements.  No source is declared __restrict__: a programmatic
+// launch lives while the grid before it writes.
+constexpr int kCopyAhead = 4;            // loads of a lane in flight
+__global__ void __launch_bounds__(kThreads) copy_rows(const __grid_constant__ CopyParams p) {
     grid_wait();
     grid_release();
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T* f = from + r / inner * from_outer + r % inner * from_stride;
-        T* t = to + r * to_stride;
-        for (int c0 = int(threadIdx.x); c0 < width; c0 += 4 * kThreads) {
-            T v[4];
+    const int lane = int(threadIdx.x) & 31;
+    const int64_t warps = int64_t(gridDim.x) * (kThreads / 32);
+    for (int64_t r = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < p.rows; r += warps) {
+        const Copy& c = r >= p.op[2].row0 ? p.op[2] : r >= p.op[1].row0 ? p.op[1] : p.op[0];
+        const int64_t row = r - c.row0, e = row / c.inner;
+        if (c.weights) {
+            const int b = min(max(p.offsets[e], 0), p.tokens);
+            if (min(p.offsets[e + 1], p.tokens) <= b) continue;
+        }
+        const char* from = static_cast<const char*>(c.from) + e * c.outer + (row - e * c.inner) * c.stride;
+        char* to = static_cast<char*>(c.to) + row * c.to_stride;
+        const int shift = int(reinterpret_cast<uintptr_t>(from) & 15);
+        const char* base = from - shift;
+        const int span = shift + c.bytes;        // bytes from the first aligned 16 on
+        const int words = shift >> 2, bits = (shift & 3) * 8;
+        for (int v0 = 0; v0 * 16 < c.bytes; v0 += 32 * kCopyAhead) {
+            uint4 own[kCopyAhead], after[kCopyAhead];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c0 + j * kThreads < width) v[j] = f[c0 + j * kThreads];
+            for (int j = 0; j < kCopyAhead; ++j) {
+                const int v = v0 + j * 32 + lane;
+                own[j] = after[j] = make_uint4(0, 0, 0, 0);
+                if (v * 16 < span) own[j] = ld_v4(base + int64_t(v) * 16);
+                if (lane == 31 && (v + 1) * 16 < span) after[j] = ld_v4(base + int64_t(v + 1) * 16);
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c0 + j * kThreads < width) t[c0 + j * kThreads] = v[j];
+            for (int j = 0; j < kCopyAhead; ++j) {
+                const int v = v0 + j * 32 + lane;
+                uint32_t w[8] = {own[j].x, own[j].y, own[j].z, own[j].w};
+                w[4] = __shfl_down_sync(0xFFFFFFFFu, own[j].x, 1);
+                w[5] = __shfl_down_sync(0xFFFFFFFFu, own[j].y, 1);
+                w[6] = __shfl_down_sync(0xFFFFFFFFu, own[j].z, 1);
+                w[7] = __shfl_down_sync(0xFFFFFFFFu, own[j].w, 1);
+                if (lane == 31) {
+                    w[4] = after[j].x; w[5] = after[j].y; w[6] = after[j].z; w[7] = after[j].w;
+                }
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t lo = words == 0 ? w[k] : words == 1 ? w[k + 1] : words == 2 ? w[k + 2] : w[k + 3];
+                    const uint32_t hi = words == 0 ? w[k + 1] : words == 1 ? w[k + 2] : words == 2 ? w[k + 3] : w[k + 4];
+                    o[k] = __funnelshift_r(lo, hi, bits);
+                }
+                if (v * 16 < c.bytes) st_v4(to + int64_t(v) * 16, make_uint4(o[0], o[1], o[2], o[3]));
+            }
         }
     }
-}
-
-template <typename T>
-cudaError_t repack(const void* from, int64_t from_stride, int64_t from_outer, void* to,
-                   int64_t to_stride, int64_t rows, int64_t inner, int64_t width, cudaStream_t s) {
-    const T* f = static_cast<const T*>(from);
-    T* t = static_cast<T*>(to);
-    int w = int(width);
-    void* args[] = {&f, &from_stride, &from_outer, &t, &to_stride, &rows, &inner, &w};
-    return launch_grid((const void*)repack_matrices<T>,
-                       dim3(unsigned(std::min<int64_t>(rows, 152 * 16))), dim3(kThreads), 0, args,
-                       s);
 }
 
 // Can TMA read these rows where they are?
@@ -578,19 +619,37 @@ Operand operand(const void* p, int64_t stride, int64_t outer, int64_t size, int6
     return o;
 }
 
-// Copies an operand that TMA cannot read to `ws`, which moves on.
-cudaError_t place(Operand& o, char*& ws, cudaStream_t s) {
-    if (!o.copy) return cudaSuccess;
-    const int64_t stride = round_up(o.width, 16 / o.size);
-    const cudaError_t e =
-        o.size == 2 ? repack<uint16_t>(o.p, o.stride, o.outer, ws, stride, o.rows, o.inner, o.width, s)
-                    : repack<uint8_t>(o.p, o.stride, o.outer, ws, stride, o.rows, o.inner, o.width, s);
-    o.p = ws;
-    o.stride = stride;
-    o.outer = o.inner * stride;
-    ws += o.bytes();
-    return e;
-}
+// The copies of a call's operands that TMA cannot read, into `ws`; the operands
+// are then where they were copied to.
+struct Copies {
+    CopyParams p = {};
+    int n = 0;
+
+    void add(Operand& o, char*& ws, bool weights) {
+        if (!o.copy) return;
+        Copy& c = p.op[n++];
+        c.from = o.p; c.stride = o.stride * o.size; c.outer = o.outer * o.size;
+        o.stride = round_up(o.width, 16 / o.size);
+        o.outer = o.inner * o.stride;
+        o.p = ws;
+        c.to = ws; c.to_stride = o.stride * o.size;
+        c.rows = o.rows; c.inner = o.inner; c.row0 = p.rows;
+        c.bytes = int(o.width * o.size);
+        c.weights = weights;
+        p.rows += o.rows;
+        ws += o.bytes();
+    }
+    cudaError_t launch(const int32_t* offsets, int64_t tokens, cudaStream_t s) {
+        if (n == 0) return cudaSuccess;
+        for (int i = n; i < 3; ++i) p.op[i].row0 = INT64_MAX;
+        p.offsets = offsets;
+        p.tokens = int(tokens);
+        void* args[] = {&p};
+        return launch_grid((const void*)copy_rows,
+                           dim3(unsigned(std::min<int64_t>(ceil_div(p.rows, kThreads / 32), 152 * 8))),
+                           dim3(kThreads), 0, args, s);
+    }
+};
 
 cudaError_t encode(CUtensorMap* map, const Operand& o, int box_x, int box_y) {
     const bool bytes = o.size == 1;
@@ -719,8 +778,10 @@ dpr_status product(bool input_grad, const void* x, int64_t x_stride, int64_t row
     p.m_size = int(to); p.m_tiles = int(ceil_div(to, kTile));
     p.k_size = int(from);
     p.out = out; p.out_stride = out_stride; p.out_bf16 = dtype == DPR_BF16;
-    cudaError_t e = place(a, ws, s);
-    if (e == cudaSuccess) e = place(b, ws, s);
+    Copies copies;
+    copies.add(a, ws, true);
+    copies.add(b, ws, false);
+    cudaError_t e = copies.launch(offsets, rows, s);
     if (e == cudaSuccess) e = encode_experts(&p.a, a, 64, input_grad ? kDepth : kHalf);
     if (e == cudaSuccess) e = encode(&p.b, b, kDepth, kHalf);
     if (e == cudaSuccess) e = encode(&p.b_piece, b, kDepth, kPiece);
@@ -861,9 +922,11 @@ dpr_status dpr_grouped_linear_weight_grad(const void* dy, int64_t dy_stride, con
         Operand a, steps, b;
         grad_operands(dy, dy_stride, x, x_stride, x_ckpt, rows, out_features, in_features, &a,
                       &steps, &b);
-        e = place(a, ws, s);
-        if (e == cudaSuccess) e = place(steps, ws, s);
-        if (e == cudaSuccess) e = place(b, ws, s);
+        Copies copies;
+        copies.add(a, ws, false);
+        copies.add(steps, ws, false);
+        copies.add(b, ws, false);
+        e = copies.launch(offsets, rows, s);
         if (e == cudaSuccess) e = encode(&p.a, a, 64, kDepth);
         if (e == cudaSuccess && x_ckpt) e = encode(&p.steps, steps, 16, kDepth);
         if (e == cudaSuccess) e = encode(&p.b, b, 64, kDepth);
