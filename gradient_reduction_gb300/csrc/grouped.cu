@@ -180,6 +180,7 @@ __device__ __forceinline__ void store_column(char* d, int64_t stride, int count,
                                              const float (&sum)[kN]) {
 #pragma unroll
     for (int j0 = 0; j0 < kN; j0 += 16) {
+        if (j0 >= count) break;
         float old[16];
         if constexpr (kAdd) {
             const char* q = d;
@@ -245,17 +246,18 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     const uint32_t rank = tc::cluster_rank();
     const int pairs = int(gridDim.x) >> 1, pair = int(blockIdx.x) >> 1;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            tc::mbar_init(full(s), 1);
-            tc::mbar_init(free_(s), 1);
-            tc::mbar_init(ready(s), kSaved ? 2 * kRestoreWarps : 2);
-        }
-        for (int a = 0; a < 2; ++a) {
-            tc::mbar_init(summed(a), 1);
-            tc::mbar_init(stored(a), 2 * kSumWarps);
+    if (warp == 0) {                     // a barrier to a lane
+        if (lane < 3 * kStages + 4) {
+            const int of = lane / kStages;
+            tc::mbar_init(bar0 + 8u * lane,
+                          of < 2                    ? 1
+                          : of == 2                 ? (kSaved ? 2 * kRestoreWarps : 2)
+                          : lane < 3 * kStages + 2  ? 1
+                                                    : 2 * kSumWarps);
         }
         tc::mbar_init_fence();
+    }
+    if (threadIdx.x == 64) {
         if (p.rows > 0) {                // else the maps are empty
             tc::tma_prefetch_map(&p.a);
             tc::tma_prefetch_map(&p.b);
@@ -512,7 +514,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     // nobody leaves while the other CTA may still signal or read this one
     tc::fence_before_sync();
     __syncthreads();
-    tc::cluster_sync();
+    tc::cluster_meet();
     tc::fence_after_sync();
     if (warp == 1) tc::tmem_free(tmem, 512);
 }

@@ -25,6 +25,12 @@ __device__ __forceinline__ void cluster_sync() {
                  ::: "memory");
 }
 
+// The same without ordering memory: the stores before it need not have arrived
+// (which takes about a microsecond).
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // True in one lane of a converged warp.  Loads and matrix instructions are
 // issued behind this: the compiler knows that one thread is left and feeds
 // them from uniform registers.  Behind `lane == 0` it builds a loop over the
