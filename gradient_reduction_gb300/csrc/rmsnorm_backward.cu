@@ -66,9 +66,9 @@ __device__ __forceinline__ void load_weight(const RmsGradParams& p, int c, float
     }
 }
 
-// rstd^3 avg(g h) from the row's sum of g h.
+// rstd^3 avg(g h) from the row's sum of rstd g h.
 __device__ __forceinline__ float along(const RmsGradParams& p, float sum, float rstd) {
-    return __fmul_rn(__fmul_rn(divide(__fmul_rn(sum, rstd), p.count, p.inv_width), rstd), rstd);
+    return __fmul_rn(__fmul_rn(divide(sum, p.count, p.inv_width), rstd), rstd);
 }
 
 // V elements of the row's h: the stored one or its checkpoint.
@@ -232,11 +232,11 @@ __global__ void __launch_bounds__(512) rms_grad_rows(const __grid_constant__ Rms
 #pragma unroll
             for (int k = 0; k < E / 2; ++k) {
                 // a channel past the row's end has d = 0
-                const F2 dk = f2(d[2 * k], d[2 * k + 1]);
+                const F2 dr = mul2(f2(d[2 * k], d[2 * k + 1]), r2);
                 x[k] = f2(f[2 * k], f[2 * k + 1]);
-                g[k] = mul2(dk, w[k]);
+                g[k] = mul2(dr, w[k]);
                 sum = fma2(g[k], x[k], sum);
-                dw[k] = fma2(dk, mul2(x[k], r2), dw[k]);
+                dw[k] = fma2(dr, x[k], dw[k]);
             }
         }
         if (p.dh) {
@@ -251,11 +251,11 @@ __global__ void __launch_bounds__(512) rms_grad_rows(const __grid_constant__ Rms
         load(row + stride);
         const float a = row_sum(total(sum), s[turn]);
         if (live) {
-            const F2 minus = f2(-along(p, a, r)), r2 = f2(r);
+            const F2 minus = f2(-along(p, a, r));
             float d[E];
 #pragma unroll
             for (int k = 0; k < E / 2; ++k)
-                halves(fma2(x[k], minus, mul2(g[k], r2)), d[2 * k], d[2 * k + 1]);
+                halves(fma2(x[k], minus, g[k]), d[2 * k], d[2 * k + 1]);
             T* dx = static_cast<T*>(p.dx) + row * p.dx_stride;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -291,39 +291,33 @@ __device__ __forceinline__ void load_shared(uint32_t at, uint32_t (&w)[1]) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
 }
 
-// kR (1 or 2) sums over the blockDim.x threads (64 to 512) that share
-// threadIdx.y, with one barrier.  Two calls in a row need different `s`.
-template <int kR>
-__device__ __forceinline__ void group_sums(float (&v)[kR], float (*s)[16][2]) {
-    const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5, nw = int(blockDim.x) >> 5;
-    const bool upper = lane & 16;
-    float t;
-    if constexpr (kR == 2)   // the lower lanes go on with the first sum, the upper ones with the second
-        t = __fadd_rn(upper ? v[1] : v[0], __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[1], 16));
-    else
-        t = __fadd_rn(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 16));
-    t = group_sum(t, 16);
-    if ((lane & 15) == 0) s[threadIdx.y][warp][lane >> 4] = t;
+// Sum over the blockDim.x threads (64 to 512) that share threadIdx.y, with one
+// barrier.  Two calls in a row need different `s`.
+__device__ __forceinline__ float group_sum_all(float v, float (*s)[16]) {
+    const int lane = int(threadIdx.x) & 31, nw = int(blockDim.x) >> 5, w = lane & 15;
+    v = warp_sum(v);
+    if (lane == 0) s[threadIdx.y][threadIdx.x >> 5] = v;
     row_barrier();
-    const int w = lane & 15;
-    t = group_sum(w < nw ? s[threadIdx.y][w][lane >> 4] : 0.0f, 16);
-    v[0] = kR == 2 ? __shfl_sync(0xFFFFFFFFu, t, 0) : t;
-    if constexpr (kR == 2) v[1] = __shfl_sync(0xFFFFFFFFu, t, 16);
+    return group_sum(w < nw ? s[threadIdx.y][w] : 0.0f, 16);
 }
 
 // As rms_grad_rows, for rows whose parts are 16-byte aligned.  One thread of
 // each group of blockDim.x (at least 64) has its rows bulk-copied into shared
-// memory, p.depth of them in all.  The group takes kR rows a turn, which share
-// one barrier.  A thread owns 16-byte pieces of the row, piece i at i *
-// blockDim.x + threadIdx.x, and keeps a turn's dy and h as they are stored
-// (codes as the bf16 numbers that they stand for) between the sum and the rest.
+// memory, p.depth of them in all.  A thread owns 16-byte pieces of the row, piece i
+// at i * blockDim.x + threadIdx.x; with 32 channels a thread there is no room for
+// their weights in its registers, and it loads them for every row.
+// 16384 x 4096 bf16 with dh and the join: 84 us, 6.4 TB/s (0.95 of the measured
+// copy rate); from a checkpoint 84 us, 5.6 TB/s; without dh 72 and 78 us.  A row's
+// chain of loads, sum, barrier and second half bounds the last three, with 16 warps an
+// SM.  What was tried: dy and h unpacked again after the sum 91 and 96 us (22 and 31
+// instructions an element); two rows a turn with their values in registers, the
+// weights in shared memory, 86 and 111 us (fewer rows in flight).
 constexpr int kMaxDepth = 8;
 constexpr int kMaxGroups = 4;
-template <typename T, bool kSaved, int kR, int NV>
+template <typename T, bool kSaved, int NV>
 __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ RmsGradParams p) {
     constexpr int V = 16 / int(sizeof(T)), E = V * NV;
-    using H = typename std::conditional<kSaved, uint16_t, T>::type;   // h between the passes
-    __shared__ float s[2][kMaxGroups][16][2];
+    __shared__ float s[2][kMaxGroups][16];
     __shared__ __align__(8) uint64_t bars[kMaxGroups][kMaxDepth];
     extern __shared__ __align__(16) uint8_t ring[];
     const int tx = int(threadIdx.x), threads = int(blockDim.x);
@@ -361,29 +355,26 @@ __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ R
         for (; asked < uint32_t(p.depth) && row0 + asked * stride < p.rows; ++asked)
             fetch(row0 + asked * stride, asked);
 
-    F2 w[E / 2], dw[E / 2];
-    {
-        float f[E];
+    constexpr bool kKeep = E <= 16;
+    F2 w[kKeep ? E / 2 : 1], dw[E / 2];
+    const auto weights = [&](int i, F2* to) {
+        const int c = (i * threads + tx) * V;
+        float v[V] = {};
+        if (c < p.width) load_weight<V>(p, c, v);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * threads + tx) * V;
-            float v[V] = {};
-            if (c < p.width) load_weight<V>(p, c, v);
+        for (int e = 0; e < V / 2; ++e) to[e] = f2(v[2 * e], v[2 * e + 1]);
+    };
+    if constexpr (kKeep) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) f[i * V + k] = v[k];
-        }
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k) {
-            w[k] = f2(f[2 * k], f[2 * k + 1]);
-            dw[k] = f2(0.0f);
-        }
+        for (int i = 0; i < NV; ++i) weights(i, w + i * V / 2);
     }
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) dw[k] = f2(0.0f);
     // what does not come in 16-byte rows is loaded a turn ahead
     struct Small {
-        float rstd;
-        uint32_t step[NV];
+        float rstd, step[NV];
     };
-    Small now[kR], next[kR];
+    Small now, next;
     const auto load_small = [&](int64_t r, Small& m) {
         if (r >= p.rows) return;
         m.rstd = p.rstd[r];
@@ -392,103 +383,85 @@ __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ R
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * threads + tx) * V;
                 if (c < p.width)
-                    m.step[i] = p.ckpt.steps[r * p.ckpt.step_stride + c / kBlockChannels];
+                    m.step[i] = step_value(p.ckpt.steps[r * p.ckpt.step_stride + c / kBlockChannels]);
             }
         }
     };
-#pragma unroll
-    for (int j = 0; j < kR; ++j) load_small(row0 + j * stride, now[j]);
+    load_small(row0, now);
     T* dx = static_cast<T*>(p.dx) + row0 * p.dx_stride + tx * V;
     const int64_t dx_row = stride * p.dx_stride;
-    uint32_t k = 0, parity = 0, last = 0;    // `last`: the first stage of the turn before
+    uint32_t k = 0, parity = 0, last = 0;    // `last`: the stage of the turn before
     int turn = 0;
     bool ok = true;
-    for (int64_t row = row0; row < p.rows; row += kR * stride, dx += kR * dx_row, turn ^= 1) {
-        uint32_t at[kR];
-        Raw<T, V> d[kR][NV];
-        Raw<H, V> h[kR][NV];
-        float sums[kR];
-        const uint32_t first = k;
-#pragma unroll
-        for (int j = 0; j < kR; ++j) {
-            F2 sum = f2(0.0f);
-            at[j] = mine + k * stage;
-            if (row + j * stride < p.rows) {
-                if (ok) ok = tc::mbar_wait(full + 8 * k, parity);
-                if (++k == uint32_t(p.depth)) { k = 0; parity ^= 1; }
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const uint32_t piece = uint32_t(i * threads + tx);
-                    if (int(piece) * V >= p.width) continue;
-                    load_shared(at[j] + piece * 16, d[j][i].w);
-                    if constexpr (kSaved) {
-                        CodeRaw<V> c;
-                        load_shared(at[j] + dy_bytes + piece * V, c.w);
-                        const uint32_t step2 = now[j].step[i] * 0x00800080u;
-#pragma unroll
-                        for (int q = 0; q < V / 4; ++q) {
-                            h[j][i].w[2 * q] = restore_pair(__byte_perm(c.w[q], 0, 0x4140), step2);
-                            h[j][i].w[2 * q + 1] = restore_pair(__byte_perm(c.w[q], 0, 0x4342), step2);
-                        }
-                    } else {
-                        load_shared(at[j] + dy_bytes + piece * 16, h[j][i].w);
-                    }
-                    F2 dv[V / 2], hv[V / 2];
-                    unpack2(d[j][i], dv);
-                    unpack2(h[j][i], hv);
-#pragma unroll
-                    for (int e = 0; e < V / 2; ++e)
-                        sum = fma2(mul2(dv[e], w[i * V / 2 + e]), hv[e], sum);
-                }
-            }
-            sums[j] = total(sum);
-        }
-#pragma unroll
-        for (int j = 0; j < kR; ++j) load_small(row + (kR + j) * stride, next[j]);
-        group_sums<kR>(sums, s[turn]);
-        // the whole group is past the turn before: its stages are free (after a failed
-        // wait they are not known to be)
-        if (tx == 0 && ok && row != row0) {
-#pragma unroll
-            for (int j = 0; j < kR; ++j)
-                if (row0 + asked * stride < p.rows) {
-                    fetch(row0 + asked * stride, last);
-                    ++asked;
-                    if (++last == uint32_t(p.depth)) last = 0;
-                }
-        }
-        last = first;
-#pragma unroll
-        for (int j = 0; j < kR; ++j) {
-            if (row + j * stride >= p.rows) break;
-            const F2 minus = f2(-along(p, sums[j], now[j].rstd)), r2 = f2(now[j].rstd);
+    for (int64_t row = row0; row < p.rows; row += stride, dx += dx_row, turn ^= 1) {
+        F2 g[E / 2], h[E / 2];               // rstd dy weight, and h
+        F2 sum = f2(0.0f);
+        const F2 r2 = f2(now.rstd);
+        const uint32_t at = mine + k * stage, first = k;
+        // The condition always holds.  As a branch it makes the compiler finish this half before
+        // the sum's exchanges: 84 us instead of 92 (without dh 72 instead of 85).
+        if (row < p.rows) {
+            if (ok) ok = tc::mbar_wait(full + 8 * k, parity);
+            if (++k == uint32_t(p.depth)) { k = 0; parity ^= 1; }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const uint32_t piece = uint32_t(i * threads + tx);
                 if (int(piece) * V >= p.width) continue;
-                F2 dv[V / 2], hv[V / 2], add[V / 2];
-                unpack2(d[j][i], dv);
-                unpack2(h[j][i], hv);
-                if (p.dh) {
-                    Raw<T, V> raw;
-                    load_shared(at[j] + dy_bytes + h_bytes + piece * 16, raw.w);
-                    unpack2(raw, add);
+                Raw<T, V> raw;
+                F2 d[V / 2], x[V / 2], mine_w[V / 2];
+                if constexpr (kSaved) {
+                    CodeRaw<V> c;
+                    load_shared(at + dy_bytes + piece * V, c.w);
+                    decode2<V>(c, now.step[i], x);
+                } else {
+                    load_shared(at + dy_bytes + piece * 16, raw.w);
+                    unpack2(raw, x);
                 }
+                load_shared(at + piece * 16, raw.w);
+                unpack2(raw, d);
+                if constexpr (!kKeep) weights(i, mine_w);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
                     const int q = i * V / 2 + e;
-                    dw[q] = fma2(dv[e], mul2(hv[e], r2), dw[q]);
-                    dv[e] = fma2(hv[e], minus, mul2(mul2(dv[e], w[q]), r2));
-                    if (p.dh) dv[e] = add2(dv[e], add[e]);
+                    const F2 dr = mul2(d[e], r2);
+                    g[q] = mul2(dr, kKeep ? w[kKeep ? q : 0] : mine_w[e]);
+                    h[q] = x[e];
+                    sum = fma2(g[q], x[e], sum);
+                    dw[q] = fma2(dr, x[e], dw[q]);
                 }
-                Raw<T, V> out;
-                pack2(dv, out);
-                st_v4(dx + j * dx_row + i * threads * V,
-                      make_uint4(out.w[0], out.w[1], out.w[2], out.w[3]));
             }
         }
+        load_small(row + stride, next);
+        const float total_sum = group_sum_all(total(sum), s[turn]);
+        // the whole group is past the turn before: its stage is free (after a failed
+        // wait it is not known to be)
+        if (tx == 0 && ok && row != row0 && row0 + asked * stride < p.rows) {
+            fetch(row0 + asked * stride, last);
+            ++asked;
+        }
+        last = first;
+        const F2 minus = f2(-along(p, total_sum, now.rstd));
 #pragma unroll
-        for (int j = 0; j < kR; ++j) now[j] = next[j];
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t piece = uint32_t(i * threads + tx);
+            if (int(piece) * V >= p.width) continue;
+            Raw<T, V> raw;
+            F2 o[V / 2];
+            if (p.dh) {
+                load_shared(at + dy_bytes + h_bytes + piece * 16, raw.w);
+                unpack2(raw, o);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) o[e] = fma2(h[i * V / 2 + e], minus, o[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) o[e] = mul2(h[i * V / 2 + e], minus);
+            }
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) o[e] = add2(g[i * V / 2 + e], o[e]);
+            pack2(o, raw);
+            st_v4(dx + i * threads * V, make_uint4(raw.w[0], raw.w[1], raw.w[2], raw.w[3]));
+        }
+        now = next;
     }
     // One thread's wait may run out where the others' end, so the block counts it
     // as one, and lets what it has asked for land before the ring's memory is used
@@ -531,7 +504,7 @@ __global__ void __launch_bounds__(256) rms_grad_sums(const __grid_constant__ Rms
         }
     }
     a = row_sum(a, s);
-    if (live && threadIdx.x == 0) p.row_avg[row] = along(p, a, p.rstd[row]);
+    if (live && threadIdx.x == 0) p.row_avg[row] = along(p, __fmul_rn(a, p.rstd[row]), p.rstd[row]);
 }
 
 // dx of a tile of 32 V columns by a slice of the rows, and the tile's column
@@ -625,13 +598,15 @@ __global__ void __launch_bounds__(1024) rms_grad_join(const __grid_constant__ Rm
 constexpr int kSms = 152;
 constexpr int kRowsWidth = 8192;         // longest rows of the one-pass kernels, but
 constexpr int kStagedWidth = 16384;      // in bf16, staged
+// fp32, 8192 rows with dh, staged and in registers: 2048 channels 50 and 55 us, 4096 89 and 107,
+// 5120 106 and 105, 6144 166 and 119, 8192 188 and 155
+constexpr int kStagedWidthFp32 = 4608;
 constexpr int64_t kShared = 200 * 1024;  // of an SM, for staged rows
 
 // How a call is done; the same for its workspace and its launch.
 struct Shape {
     enum Kind { kStaged, kRows, kTwoPasses } kind;
     int nv;                  // vectors (pieces) a thread
-    int rows_a_turn;         // staged
     int depth;
     int threads, per_block;
     int64_t slices;          // blocks of the one-pass kernels
@@ -652,7 +627,7 @@ void one_pass(Shape& q, int64_t rows, int64_t width, int elems, int least, int b
 Shape shape_of(int64_t rows, int64_t width, int dtype, bool saved, bool with_dh, int v, bool pieces) {
     Shape q = {};
     const int64_t es = dtype_size(dtype);
-    if (pieces && width > 512 && width <= (dtype == DPR_BF16 ? kStagedWidth : kRowsWidth)) {
+    if (pieces && width > 512 && width <= (dtype == DPR_BF16 ? kStagedWidth : kStagedWidthFp32)) {
         const int elems = width > kRowsWidth ? 32 : 16;
         // one block an SM for long rows, whose groups' column sums meet in shared
         // memory; few rows spread over more SMs in small blocks
@@ -660,7 +635,6 @@ Shape shape_of(int64_t rows, int64_t width, int dtype, bool saved, bool with_dh,
         const int64_t groups = 512 / (q.threads * q.per_block) * q.per_block;
         const int64_t row_bytes = width * (es + (saved ? 1 : es) + (with_dh ? es : 0));
         q.depth = int(std::min<int64_t>(kMaxDepth, kShared / (groups * row_bytes)));
-        q.rows_a_turn = q.depth >= 4 && elems == 16 ? 2 : 1;
         if (q.depth >= 2) {
             q.kind = Shape::kStaged;
             q.nv = int(elems * es / 16);
@@ -689,11 +663,11 @@ int64_t shape_bytes(const Shape& q, int64_t rows, int64_t width) {
            q.slices * round_up(width, 4) * 4;
 }
 
-template <typename T, bool kSaved, int kR, int NV>
+template <typename T, bool kSaved, int NV>
 cudaError_t launch_staged(RmsGradParams& p, const Shape& q, cudaStream_t s) {
     const size_t row_bytes = size_t(p.width) * (sizeof(T) + (kSaved ? 1 : sizeof(T)) + (p.dh ? sizeof(T) : 0));
     const size_t sums = size_t(q.per_block - 1) * q.threads * NV * 16 / sizeof(T) * 4;
-    const void* k = (const void*)rms_grad_staged<T, kSaved, kR, NV>;
+    const void* k = (const void*)rms_grad_staged<T, kSaved, NV>;
     static std::atomic<uint64_t> allowed{0};   // of this kernel: one per instantiation
     const cudaError_t e = allow_shared_memory(k, int(kShared), &allowed);
     if (e != cudaSuccess) return e;
@@ -706,9 +680,8 @@ template <typename T, bool kSaved>
 cudaError_t launch_any_staged(RmsGradParams& p, const Shape& q, cudaStream_t s) {
     constexpr int kPieces = int(sizeof(T));     // of 16 channels
     if constexpr (sizeof(T) == 2)
-        if (q.nv == 4) return launch_staged<T, kSaved, 1, 4>(p, q, s);
-    return q.rows_a_turn == 2 ? launch_staged<T, kSaved, 2, kPieces>(p, q, s)
-                              : launch_staged<T, kSaved, 1, kPieces>(p, q, s);
+        if (q.nv == 4) return launch_staged<T, kSaved, 4>(p, q, s);
+    return launch_staged<T, kSaved, kPieces>(p, q, s);
 }
 
 template <typename T, int V, int NV, bool kSaved>
