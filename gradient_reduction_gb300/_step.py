@@ -6,12 +6,13 @@ of the backward-pass operators (_operators.py).
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Sequence
 
 import torch
 
 from ._binding import _check, _ptrs, _stream, lib
-from ._operators import (_DTYPES, _checkpoint_arg, _code, _device, _handle, _matrix, _statistic,
+from ._operators import (_DTYPES, _CheckpointArg, _checkpoint_arg, _code, _device, _handle, _matrix, _statistic,
                          _vector, _workspace, _workspace_bytes, _wrong_device, _wrong_shape)
 
 
@@ -130,16 +131,12 @@ def _grouped_product(fn: str, x, what: str, offsets, weight, out, out_what: str,
     if r != rows or w != give:
         _wrong_shape(out_what, r, w, rows, give)
     offs = _offsets(offsets, experts, dev)
-    need = ctypes.c_int64()
-    L = lib()
-    st = getattr(L, fn + "_workspace")(px, sx, rows, experts, pw, sw, ew, o, i, ctypes.byref(need))
-    if st:
-        _check(fn, st)
-    nbytes = need.value
+    # of the addresses only their alignment counts
+    nbytes = _workspace_bytes(fn + "_workspace", px & 15, sx, rows, experts, pw & 15, sw, ew, o, i)
     handle = _handle(stream, dev)
     ws = _workspace(workspace, nbytes, stream, handle, dev)
-    st = getattr(L, fn)(px, sx, rows, offs, experts, pw, sw, ew, o, i, po, so, _code(out, out_what),
-                        0 if ws is None else ws.data_ptr(), nbytes, handle)
+    st = getattr(lib(), fn)(px, sx, rows, offs, experts, pw, sw, ew, o, i, po, so, _code(out, out_what),
+                            0 if ws is None else ws.data_ptr(), nbytes, handle)
     if st:
         _check(fn, st)
 
@@ -180,24 +177,36 @@ def dpr_grouped_linear_weight_grad(dy: torch.Tensor, offsets: torch.Tensor, x,
         _bf16(x, "x")
         if r != rows or w != in_features:
             _wrong_shape("x", r, w, rows, in_features)
+        layout = (px & 15, sx)
     else:
-        ref = ctypes.byref(_checkpoint_arg(x, "x", rows, in_features, dev))
+        c = _checkpoint_arg(x, "x", rows, in_features, dev)
+        ref = ctypes.byref(c)
+        layout = ((c.codes or 0) & 15, c.code_stride, (c.steps or 0) & 15, c.step_stride)
     offs = _offsets(offsets, experts, dev)
-    need = ctypes.c_int64()
-    L = lib()
-    st = L.dpr_grouped_linear_weight_grad_workspace(pd, sd, px, sx, ref, rows, experts, out_features,
-                                                    in_features, ctypes.byref(need))
-    if st:
-        _check("dpr_grouped_linear_weight_grad", st)
-    nbytes = need.value
+    nbytes = _weight_grad_bytes(pd & 15, sd, layout, rows, experts, out_features, in_features)
     handle = _handle(stream, dev)
     ws = _workspace(workspace, nbytes, stream, handle, dev)
-    st = L.dpr_grouped_linear_weight_grad(
+    st = lib().dpr_grouped_linear_weight_grad(
         pd, sd, px, sx, ref, rows, offs, experts, out_features, in_features, pw, sw, ew,
         _code(dweight, "dweight"), 1 if accumulate else 0, 0 if ws is None else ws.data_ptr(),
         nbytes, handle)
     if st:
         _check("dpr_grouped_linear_weight_grad", st)
+
+
+@functools.lru_cache(maxsize=1024)
+def _weight_grad_bytes(dy: int, dy_stride: int, x: tuple, rows: int, experts: int, out_features: int,
+                       in_features: int) -> int:
+    """Scratch memory by sizes and strides; of the addresses only their alignment counts."""
+    px, sx, ref = x[0], x[1], None
+    if len(x) == 4:
+        px = sx = 0
+        ref = ctypes.byref(_CheckpointArg(*x))
+    n = ctypes.c_int64()
+    _check("dpr_grouped_linear_weight_grad",
+           lib().dpr_grouped_linear_weight_grad_workspace(dy, dy_stride, px, sx, ref, rows, experts,
+                                                          out_features, in_features, ctypes.byref(n)))
+    return n.value
 
 
 class GradPlan:
