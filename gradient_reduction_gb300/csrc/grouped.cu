@@ -54,7 +54,7 @@ constexpr int smem_bytes(int kind) {
 }
 // Registers per thread after the split of the restoring kernel (as in the
 // weight gradient of one layer); together no more than the launch's.
-constexpr int kIssueRegs = 40, kSumRegs = 160, kRestoreRegs = 56;
+constexpr int kIssueRegs = 24, kSumRegs = 168, kRestoreRegs = 56;
 static_assert(kIssueRegs + 2 * kSumRegs + 2 * kRestoreRegs <= 5 * 96, "the block's registers");
 
 }  // namespace
@@ -77,48 +77,105 @@ struct GroupedParams {
     int64_t out_expert_stride;   // weight gradients
     int out_bf16;
     int accumulate;
+    // work dealt out by steps: parts of tiles are summed here
+    int slot_columns;        // columns of a part's room, which has kTile features
+    float* partial;          // [2 * pairs][slot_columns][kTile]
+    struct GroupedPart* parts;   // [2 * pairs]
+};
+
+// A part of a tile that begins its sum; the next pairs' first parts follow it.
+struct GroupedPart {
+    int64_t at;              // of the tile in the output, in elements
+    int features, columns;
+    int count;               // parts in all; 0: nothing to join
+    int pad;
 };
 
 namespace {
 
 __device__ unsigned int g_wait_failures;
 
-// The experts' tokens and tiles, worked out by every block.
+// The experts' tokens and work, worked out by every block.
 struct Experts {
-    int begin[DPR_MAX_EXPERTS];
-    int count[DPR_MAX_EXPERTS];
-    int tile0[DPR_MAX_EXPERTS + 1];      // tiles of the experts before
+    int edge[DPR_MAX_EXPERTS + 1];       // expert e has the rows edge[e] .. edge[e + 1] - 1
+    int work0[DPR_MAX_EXPERTS + 1];      // of the experts before: tiles, or their steps
 };
 
 __host__ __device__ inline int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 
+// Steps of a tile of an expert; a tile without a step counts as one where
+// steps are dealt out, for it has to be written.
 template <int kKind>
+__device__ __forceinline__ int steps_of(const GroupedParams& p, int count) {
+    return ((is_weight_grad(kKind) ? count : p.k_size) + kDepth - 1) / kDepth;
+}
+
+// Offsets are limited to the rows there are and to no less than those before, so
+// that whatever they hold no row has two experts and the work keeps its bounds.
+template <int kKind, bool kSplit>
+__device__ __forceinline__ int work_of_expert(const GroupedParams& p, int count) {
+    const int n = p.m_tiles * (is_weight_grad(kKind) ? p.n_tiles : tiles_of(count));
+    return kSplit ? n * max(steps_of<kKind>(p, count), 1) : n;
+}
+
+template <int kKind, bool kSplit>
 __device__ void make_table(const GroupedParams& p, Experts& t) {
-    for (int e = int(threadIdx.x); e < p.experts; e += int(blockDim.x)) {
-        const int b = min(max(p.offsets[e], 0), p.rows);
-        const int end = min(max(p.offsets[e + 1], b), p.rows);
-        t.begin[e] = b;
-        t.count[e] = end - b;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {              // tiles, summed 32 experts at a time
-        const int lane = int(threadIdx.x);
-        int before = 0;
-        for (int e0 = 0; e0 < p.experts; e0 += 32) {
-            const int e = e0 + lane;
-            int n = 0;
-            if (e < p.experts)
-                n = p.m_tiles * (is_weight_grad(kKind) ? p.n_tiles : tiles_of(t.count[e]));
-            int upto = n;
+    const int lane = int(threadIdx.x) & 31;
+    if (p.experts < 32) {                // an expert to a lane of the first warp
+        if (threadIdx.x < 32) {
+            int edge = lane <= p.experts ? min(max(p.offsets[lane], 0), p.rows) : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, edge, d);
+                if (lane >= d) edge = max(edge, v);
+            }
+            const int count = __shfl_down_sync(0xFFFFFFFFu, edge, 1) - edge;
+            const int mine = lane < p.experts ? work_of_expert<kKind, kSplit>(p, count) : 0;
+            int upto = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
                 if (lane >= d) upto += v;
             }
-            if (e < p.experts) t.tile0[e] = before + upto - n;
-            before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            if (lane <= p.experts) {
+                t.edge[lane] = edge;
+                t.work0[lane] = upto - mine;
+            }
         }
-        if (lane == 0) t.tile0[p.experts] = before;
+        __syncthreads();
+        return;
+    }
+    for (int e = int(threadIdx.x); e <= p.experts; e += int(blockDim.x))
+        t.edge[e] = min(max(p.offsets[e], 0), p.rows);
+    __syncthreads();
+    if (threadIdx.x < 32) {              // a run of experts to a lane
+        const int run = (p.experts + 32) / 32, first = lane * run;
+        const int last = min(first + run, p.experts + 1);
+        int top = 0;
+        for (int e = first; e < last; ++e) top = max(top, t.edge[e]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, top, d);
+            if (lane >= d) top = max(top, v);
+        }
+        top = __shfl_up_sync(0xFFFFFFFFu, top, 1);
+        if (lane == 0) top = 0;
+        for (int e = first; e < last; ++e) t.edge[e] = top = max(top, t.edge[e]);
+        __syncwarp();
+        int sum = 0;
+        for (int e = first; e < min(last, p.experts); ++e)
+            sum += work_of_expert<kKind, kSplit>(p, t.edge[e + 1] - t.edge[e]);
+        int before = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, before, d);
+            if (lane >= d) before += v;
+        }
+        before -= sum;
+        for (int e = first; e < last; ++e) {
+            t.work0[e] = before;
+            if (e < p.experts) before += work_of_expert<kKind, kSplit>(p, t.edge[e + 1] - t.edge[e]);
+        }
     }
     __syncthreads();
 }
@@ -128,18 +185,47 @@ struct Tile {
     int m, n;                // first feature, first column (row of the tokens, or feature)
     int columns;             // columns that are stored
     int size;                // columns of the instruction: the same up to a multiple of 32
-    int steps;
+    int steps;               // of the whole tile
+    int first, last;         // those of this piece of work
+    int next;                // where the work goes on
     int k, k_count;          // weight gradients: first token and how many
 };
 
-// The n-th tile of a pair; false when there is none.  An expert's tiles run in
+// A pair's work: every pairs-th tile, or a range of all tiles' steps.
+struct Work {
+    int begin, end;
+    int step;                // pairs, or steps of a range
+};
+constexpr int kMinPart = 8;              // steps of a part, at least
+template <bool kSplit>
+__device__ __forceinline__ Work work_of(const GroupedParams& p, const Experts& t, int pair, int pairs) {
+    const int total = t.work0[p.experts];
+    if (!kSplit) return Work{pair, total, pairs};
+    const int part = max((total + pairs - 1) / pairs, kMinPart);
+    return Work{min(pair * part, total), min((pair + 1) * part, total), part};
+}
+
+// The piece of work at `at`; false when there is none.  An expert's tiles run in
 // columns of 8 along N, so that the tiles at work at one time share inputs.
-template <int kKind>
-__device__ __forceinline__ bool tile_at(const GroupedParams& p, const Experts& t, int index, Tile& s) {
-    if (index >= t.tile0[p.experts]) return false;
-    while (index >= t.tile0[s.e + 1]) ++s.e;
-    const int local = index - t.tile0[s.e];
-    const int count = t.count[s.e];
+template <int kKind, bool kSplit>
+__device__ __forceinline__ bool tile_at(const GroupedParams& p, const Experts& t, const Work& w, int at,
+                                        Tile& s) {
+    if (at >= w.end) return false;
+    while (at >= t.work0[s.e + 1]) ++s.e;
+    int local = at - t.work0[s.e];
+    const int count = t.edge[s.e + 1] - t.edge[s.e];
+    s.steps = steps_of<kKind>(p, count);
+    if constexpr (kSplit) {
+        const int each = max(s.steps, 1), tile = local / each;
+        s.first = local - tile * each;
+        s.next = min(at - s.first + each, w.end);
+        s.last = min(s.first + s.next - at, s.steps);
+        local = tile;
+    } else {
+        s.first = 0;
+        s.last = s.steps;
+        s.next = at + w.step;
+    }
     const int n_tiles = is_weight_grad(kKind) ? p.n_tiles : tiles_of(count);
     const int group = local / (8 * p.m_tiles);
     const int rest = local - group * 8 * p.m_tiles;
@@ -150,17 +236,15 @@ __device__ __forceinline__ bool tile_at(const GroupedParams& p, const Experts& t
         s.n = n * kTile;
         s.columns = min(kTile, p.n_size - s.n);
         s.size = (s.columns + 31) & ~31;
-        s.k = t.begin[s.e];
+        s.k = t.edge[s.e];
         s.k_count = count;
-        s.steps = (count + kDepth - 1) / kDepth;
     } else {
         // an expert's tokens in tiles of even size
         s.size = ((count + n_tiles - 1) / n_tiles + 31) & ~31;
-        s.n = t.begin[s.e] + n * s.size;
+        s.n = t.edge[s.e] + n * s.size;
         s.columns = min(s.size, count - n * s.size);
         s.k = 0;
         s.k_count = p.k_size;
-        s.steps = (p.k_size + kDepth - 1) / kDepth;
     }
     return true;
 }
@@ -219,7 +303,7 @@ __device__ __forceinline__ void store_column(char* d, int64_t stride, int count,
 // only), 4-11 keep the sums and store them.  2 passes a loaded stage on to the
 // first CTA (and writes the zeros behind an expert's last token); with
 // checkpoints 12-19 do, which restore x on the way, in two groups that take turns.
-template <int kKind>
+template <int kKind, bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kKind), 1)
 grouped_pairs(const __grid_constant__ GroupedParams p) {
     constexpr bool kGrad = is_weight_grad(kKind);
@@ -229,6 +313,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     __shared__ __align__(8) uint64_t bars[3 * kStages + 4];
     __shared__ uint32_t tmem_slot;
     __shared__ Experts table;
+    __shared__ GroupedPart parts[2];             // what the pair's parts begin
 
     const uint32_t base = (tc::smem_addr(raw) + 1023u) & ~1023u;
     const uint32_t a_at = base;                                  // [kStages], 1024-byte aligned
@@ -246,6 +331,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     const uint32_t rank = tc::cluster_rank();
     const int pairs = int(gridDim.x) >> 1, pair = int(blockIdx.x) >> 1;
 
+    if (kSplit && threadIdx.x == 128) parts[0].count = parts[1].count = 0;
     if (warp == 0) {                     // a barrier to a lane
         if (lane < 3 * kStages + 4) {
             const int of = lane / kStages;
@@ -273,21 +359,22 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     const uint32_t tmem = tmem_slot;
     grid_wait();
     grid_release();
-    make_table<kKind>(p, table);
+    make_table<kKind, kSplit>(p, table);
 
     bool ok = true;
     Tile s;
     s.e = 0;
+    const Work work = work_of<kSplit>(p, table, pair, pairs);
     if constexpr (kSaved)
         if (warp < 4) tc::give_registers<kIssueRegs>();
     if (warp == 0) {
         if (tc::elect_one()) {
             int st = 0;
             uint32_t round = 0;
-            for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+            for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
                 const int m = s.m + int(rank) * kHalf;
                 const int half = s.size >> 1, c = s.n + int(rank) * half;
-                for (int k = 0; k < s.steps; ++k) {
+                for (int k = s.first; k < s.last; ++k) {
                     if (!(ok = tc::mbar_wait(free_(st), (round & 1) ^ 1))) break;
                     const uint32_t a = a_at + st * kOperandBytes, b = b_at + st * kOperandBytes;
                     const int d = k * kDepth;
@@ -347,9 +434,9 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
             const uint64_t b0 = kAlongN ? tc::operand(b_at, kGroupBytes, 1024)
                                         : tc::operand_along_k(b_at);
             uint32_t st = 0, round = 0, acc = 0, acc_round = 0;
-            for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+            for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
                 const uint32_t instruction = tc::bf16_instruction(kTile, s.size, kAlongM, kAlongN);
-                for (int left = s.steps; ok && left > 0; left -= kChunk) {
+                for (int left = s.last - s.first; ok && left > 0; left -= kChunk) {
                     if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
                     const uint32_t d = tmem + acc * kTile;
                     bool add = false;
@@ -376,8 +463,8 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     } else if (warp == 2 && !kSaved) {
         int st = 0;
         uint32_t round = 0;
-        for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
-            for (int k = 0; k < s.steps; ++k) {
+        for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
+            for (int k = s.first; k < s.last; ++k) {
                 if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
                 const int valid = s.k_count - k * kDepth;
                 if (kGrad && valid < kDepth) {
@@ -405,11 +492,12 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
         int acc = 0;
         uint32_t acc_round = 0;
         float sum[kColumns];
-        for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+        for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
             const int half = s.size >> 1;           // a multiple of 16
+            const int last = s.last;
 #pragma unroll
             for (int j = 0; j < kColumns; ++j) sum[j] = 0.0f;
-            for (int k = 0; k < s.steps; k += kChunk) {
+            for (int k = s.first; k < last; k += kChunk) {
                 if (!(ok = tc::mbar_wait_warp(summed(acc), acc_round & 1))) break;
                 tc::fence_after_sync();
                 const uint32_t from = tmem + acc * kTile + side * half + (uint32_t(quarter) << 21);
@@ -429,13 +517,26 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
                 if (++acc == 2) { acc = 0; ++acc_round; }
             }
             if (!ok) break;
+            // again: kept, it would cost the sums registers
+            if constexpr (kSplit) tile_at<kKind, kSplit>(p, table, work, n, s);
             const int f = s.m + int(rank) * kHalf + quarter * 32 + lane;
             const int count = min(half, s.columns - side * half);
-            if (f < p.m_size && count > 0 && (s.steps > 0 || !p.accumulate)) {
+            int64_t at = int64_t(s.n) * p.out_stride;
+            if constexpr (kGrad) at += int64_t(s.e) * p.out_expert_stride;
+            if (kSplit && s.last - s.first < s.steps) {   // a part: its sums to the workspace
+                const int slot = n == work.begin ? 0 : 1;
+                float* to = p.partial + (int64_t(2 * pair + slot) * p.slot_columns + side * half) * kTile +
+                            (f - s.m);
+                store_column<false, false>(reinterpret_cast<char*>(to), kTile * 4, count, sum);
+                if (s.first == 0 && threadIdx.x == 128) {
+                    parts[slot].at = at + s.m;
+                    parts[slot].features = min(kTile, p.m_size - s.m);
+                    parts[slot].columns = s.columns;
+                    parts[slot].count = 1 + (n + s.steps - work.end + work.step - 1) / work.step;
+                }
+            } else if (f < p.m_size && count > 0 && (s.steps > 0 || !p.accumulate)) {
                 const int64_t size = p.out_bf16 ? 2 : 4;
-                int64_t at = int64_t(s.n + side * half) * p.out_stride + f;
-                if constexpr (kGrad) at += int64_t(s.e) * p.out_expert_stride;
-                char* d = static_cast<char*>(p.out) + at * size;
+                char* d = static_cast<char*>(p.out) + (at + int64_t(side * half) * p.out_stride + f) * size;
                 const int64_t stride = p.out_stride * size;
                 if (p.out_bf16) {
                     if (kGrad && p.accumulate) store_column<true, true>(d, stride, count, sum);
@@ -445,6 +546,10 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
                     else store_column<false, false>(d, stride, count, sum);
                 }
             }
+        }
+        if (kSplit && rank == 0 && threadIdx.x == 128) {
+            p.parts[2 * pair] = parts[0];
+            p.parts[2 * pair + 1] = parts[1];
         }
     } else if (kSaved && warp >= 12) {
         tc::give_registers<kRestoreRegs>();
@@ -459,13 +564,14 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
         const uint32_t piece0 = uint32_t((chunk * 2) ^ (row & 7)) * 16;
         const uint32_t piece1 = uint32_t((chunk * 2 + 1) ^ (row & 7)) * 16;
         uint32_t step0 = 0;                         // steps of the tiles before
-        for (int n = pair; ok && tile_at<kKind>(p, table, n, s); n += pairs) {
+        for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
             const uint32_t block = uint32_t(((s.m + int(rank) * kHalf) / kBlockChannels & 15) +
                                             group * 2 + (chunk >> 1));
-            for (int k = (step0 & 1) ^ turn; k < s.steps; k += 2) {
+            const int count = s.last - s.first;
+            for (int k = (step0 & 1) ^ turn; k < count; k += 2) {
                 const uint32_t st = (step0 + k) % kStages, round = (step0 + k) / kStages;
                 if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
-                const int valid = s.k_count - k * kDepth;
+                const int valid = s.k_count - (s.first + k) * kDepth;
                 uint32_t w[4][4], step[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -506,7 +612,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(st), 0));
             }
-            step0 += uint32_t(s.steps);
+            step0 += uint32_t(count);
         }
     }
     if (!ok) atomicAdd(&g_wait_failures, 1u);
@@ -517,6 +623,47 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     tc::cluster_meet();
     tc::fence_after_sync();
     if (warp == 1) tc::tmem_free(tmem, 512);
+}
+
+// Tiles summed in parts: the parts in order, rounded once.  A block joins
+// kJoinColumns columns of the tile that a part begins, a feature a thread.
+constexpr int kJoinColumns = 8, kJoinAhead = 4;
+__global__ void __launch_bounds__(kTile) grouped_join(const __grid_constant__ GroupedParams p) {
+    grid_wait();
+    grid_release();
+    const int slot = int(blockIdx.x), column = int(blockIdx.y) * kJoinColumns, f = int(threadIdx.x);
+    const GroupedPart q = p.parts[slot];
+    if (q.count == 0 || column >= q.columns || f >= q.features) return;
+    const int64_t room = int64_t(p.slot_columns) * kTile;
+    float sum[kJoinColumns] = {};
+    for (int i = 0; i < q.count; i += kJoinAhead) {
+        float v[kJoinAhead][kJoinColumns];
+#pragma unroll
+        for (int a = 0; a < kJoinAhead; ++a) {
+            // the first part may be its pair's last piece, every later one is its pair's first
+            const int from = i + a == 0 ? slot : 2 * ((slot >> 1) + i + a);
+            const float* part = p.partial + from * room + int64_t(column) * kTile + f;
+#pragma unroll
+            for (int c = 0; c < kJoinColumns; ++c)
+                v[a][c] = i + a < q.count && column + c < q.columns ? part[c * kTile] : 0.0f;
+        }
+#pragma unroll
+        for (int a = 0; a < kJoinAhead; ++a)
+#pragma unroll
+            for (int c = 0; c < kJoinColumns; ++c) sum[c] = __fadd_rn(sum[c], v[a][c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kJoinColumns; ++c) {
+        if (column + c >= q.columns) break;
+        const int64_t at = q.at + (column + c) * p.out_stride + f;
+        if (p.out_bf16) {
+            uint16_t* d = static_cast<uint16_t*>(p.out) + at;
+            *d = to_bf16(p.accumulate ? __fadd_rn(bf_1(*d), sum[c]) : sum[c]);
+        } else {
+            float* d = static_cast<float*>(p.out) + at;
+            *d = p.accumulate ? __fadd_rn(*d, sum[c]) : sum[c];
+        }
+    }
 }
 
 // An operand copied to 16-byte-aligned rows, for inputs that TMA cannot read.
@@ -672,15 +819,69 @@ cudaError_t encode_experts(CUtensorMap* map, const Operand& o, int box_x, int bo
                              CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int kKind>
-cudaError_t launch_pairs(GroupedParams& p, int64_t tiles, cudaStream_t s) {
+// How the work is dealt out, from what the host knows: `tiles` at most, of
+// `steps` steps and `each` columns on average, `columns` at most.
+struct Plan {
+    bool split = false;
+    int64_t pairs = 0, slot_columns = 0, partial_bytes = 0, part_bytes = 0;
+    int64_t bytes() const { return partial_bytes + part_bytes; }
+};
+
+// Steps are dealt out, and parts of tiles joined by a second kernel, where
+// whole tiles would leave pairs idle for more steps than that second kernel and its
+// launch take (kSplitGain, some 5 us).  Tiles of few columns wait for
+// memory, not for the tensor core: fewer pairs at once then go on faster (0.25 us a step
+// against 0.36 with all of them).  3072 tokens, 184 x 412, weight gradient: 24.3 us
+// whole, 13.7 split; 32 tokens over 8 experts of 11008 x 4096, input gradient (128
+// tiles of few columns): 107 whole, 113 split.
+constexpr double kSplitGain = 16;
+Plan plan_work(int64_t tiles, double steps, int64_t columns, double each) {
+    Plan q;
+    q.pairs = std::min<int64_t>(tiles, kPairs);
+    const double rounds = double(ceil_div(tiles, kPairs)) * (each <= 64 ? 0.7 : 1.0);
+    if (tiles < 2 * kPairs && (rounds - double(tiles) / kPairs) * steps > kSplitGain) {
+        q.split = true;
+        q.pairs = std::min<int64_t>(kPairs, std::max(tiles, int64_t(double(tiles) * steps / kMinPart)));
+        q.slot_columns = std::min<int64_t>(kTile, round_up(columns, 32));
+        q.partial_bytes = 2 * q.pairs * q.slot_columns * kTile * 4;
+        q.part_bytes = 2 * q.pairs * int64_t(sizeof(GroupedPart));
+    }
+    return q;
+}
+
+Plan product_plan(int64_t rows, int64_t experts, int64_t to, int64_t from) {
+    // at most: every expert's last tile may be short
+    const int64_t n = rows / kTile + std::min(rows, experts);
+    return plan_work(ceil_div(to, kTile) * n, double(ceil_div(from, kDepth)), rows, double(rows) / double(n));
+}
+
+Plan grad_plan(int64_t rows, int64_t experts, int64_t out_features, int64_t in_features) {
+    return plan_work(experts * ceil_div(in_features, kTile) * ceil_div(out_features, kTile),
+                     double(rows) / double(experts * kDepth), out_features, kTile);
+}
+
+template <int kKind, bool kSplit>
+cudaError_t launch_kernel(GroupedParams& p, const Plan& q, cudaStream_t s) {
     static std::atomic<uint64_t> allowed{0};
-    const void* k = (const void*)grouped_pairs<kKind>;
+    const void* k = (const void*)grouped_pairs<kKind, kSplit>;
     const cudaError_t e = allow_shared_memory(k, smem_bytes(kKind), &allowed);
     if (e != cudaSuccess) return e;
     void* args[] = {&p};
-    return launch_grid(k, dim3(unsigned(2 * std::min<int64_t>(tiles, kPairs))), dim3(threads(kKind)),
-                       smem_bytes(kKind), args, s);
+    return launch_grid(k, dim3(unsigned(2 * q.pairs)), dim3(threads(kKind)), smem_bytes(kKind), args, s);
+}
+
+template <int kKind>
+cudaError_t launch_pairs(GroupedParams& p, const Plan& q, char* ws, cudaStream_t s) {
+    if (!q.split) return launch_kernel<kKind, false>(p, q, s);
+    p.slot_columns = int(q.slot_columns);
+    p.partial = reinterpret_cast<float*>(ws);
+    p.parts = reinterpret_cast<GroupedPart*>(ws + q.partial_bytes);
+    const cudaError_t e = launch_kernel<kKind, true>(p, q, s);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&p};
+    return launch_grid((const void*)grouped_join,
+                       dim3(unsigned(2 * q.pairs), unsigned(q.slot_columns / kJoinColumns)), dim3(kTile), 0,
+                       args, s);
 }
 
 dpr_status check_sizes(int64_t rows, int64_t experts, int64_t out_features, int64_t in_features) {
@@ -737,7 +938,9 @@ dpr_status product_workspace(bool input_grad, const void* x, int64_t x_stride, i
     Operand a, b;
     operands(input_grad, x, x_stride, rows, experts, weight, weight_stride, expert_stride,
              out_features, in_features, &a, &b);
-    *bytes = a.bytes() + b.bytes();
+    *bytes = a.bytes() + b.bytes() +
+             product_plan(rows, experts, input_grad ? in_features : out_features,
+                          input_grad ? out_features : in_features).bytes();
     return DPR_OK;
 }
 
@@ -788,9 +991,8 @@ dpr_status product(bool input_grad, const void* x, int64_t x_stride, int64_t row
     if (e == cudaSuccess) e = encode(&p.b, b, kDepth, kHalf);
     if (e == cudaSuccess) e = encode(&p.b_piece, b, kDepth, kPiece);
     if (e != cudaSuccess) return record_cuda_status(e);
-    // at most: every expert's last tile may be short
-    const int64_t tiles = p.m_tiles * (rows / kTile + std::min(rows, experts));
-    e = input_grad ? launch_pairs<kInputGrad>(p, tiles, s) : launch_pairs<kForward>(p, tiles, s);
+    const Plan q = product_plan(rows, experts, to, from);
+    e = input_grad ? launch_pairs<kInputGrad>(p, q, ws, s) : launch_pairs<kForward>(p, q, ws, s);
     return record_cuda_status(e);
 }
 
@@ -872,7 +1074,8 @@ dpr_status dpr_grouped_linear_weight_grad_workspace(const void* dy, int64_t dy_s
     Operand a, steps, b;
     grad_operands(dy, dy_stride, x, x_stride, x_ckpt, rows, out_features, in_features, &a, &steps,
                   &b);
-    *bytes = a.bytes() + steps.bytes() + b.bytes();
+    *bytes = a.bytes() + steps.bytes() + b.bytes() +
+             grad_plan(rows, experts, out_features, in_features).bytes();
     return DPR_OK;
 }
 
@@ -934,9 +1137,9 @@ dpr_status dpr_grouped_linear_weight_grad(const void* dy, int64_t dy_stride, con
         if (e == cudaSuccess) e = encode(&p.b, b, 64, kDepth);
         if (e != cudaSuccess) return record_cuda_status(e);
     }
-    const int64_t tiles = experts * p.m_tiles * p.n_tiles;
-    e = x_ckpt && rows > 0 ? launch_pairs<kWeightGradSaved>(p, tiles, s)
-                           : launch_pairs<kWeightGrad>(p, tiles, s);
+    const Plan q = grad_plan(rows, experts, out_features, in_features);
+    e = x_ckpt && rows > 0 ? launch_pairs<kWeightGradSaved>(p, q, ws, s)
+                           : launch_pairs<kWeightGrad>(p, q, ws, s);
     return record_cuda_status(e);
 }
 

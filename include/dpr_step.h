@@ -70,8 +70,8 @@ dpr_status dpr_rmsnorm_backward(const void* dy, int64_t dy_stride, const void* d
  *   dpr_grouped_linear_input_grad   dx_t = W_e^T dy_t
  *   dpr_grouped_linear_weight_grad  dW_e = sum over e's tokens of dy_t x_t^T
  * offsets ([experts + 1] int32) is read on the device, as a router leaves it;
- * values are taken as limited to 0 .. rows, an end as no less than its
- * beginning, and no row may belong to two experts.  An expert may have no
+ * every value is taken as limited to 0 .. rows and as no less than those before
+ * it, so that no row has two experts whatever the values are.  An expert may have no
  * tokens (its weight is not read; its weight gradient is zero).  Rows that
  * belong to no expert are neither read nor written, whatever they hold.
  *
@@ -81,8 +81,9 @@ dpr_status dpr_rmsnorm_backward(const void* dy, int64_t dy_stride, const void* d
  * gradients read x, or its checkpoint when x_ckpt is not NULL (x is then
  * ignored); with accumulate != 0 they are added to.  The workspace is 16-byte
  * aligned and may be reused by the next call on the same stream; its size
- * depends on the sizes and, because inputs whose rows are not 16-byte aligned
- * are first copied into it, on the addresses and strides.
+ * depends on the sizes (long sums of few tiles are split over the GPU, their
+ * parts joined in order) and, because inputs whose rows are not 16-byte aligned
+ * are first copied into it, on the strides and on the addresses modulo 16.
  */
 #define DPR_MAX_EXPERTS 1024
 

@@ -54,12 +54,12 @@ def rms_backward_bounds(dy, h, w, rstd, dh, dtype, grad_dtype):
 
 
 def spans(offsets, rows):
-    """(begin, end) of every expert, limited as the calls take them."""
-    out = []
-    for a, b in zip(offsets, offsets[1:]):
-        a = min(max(a, 0), rows)
-        out.append((a, min(max(b, a), rows)))
-    return out
+    """(begin, end) of every expert, limited as the calls take them: to the rows, and to no less than
+    the offsets before."""
+    edges = []
+    for a in offsets:
+        edges.append(max(min(max(a, 0), rows), edges[-1] if edges else 0))
+    return list(zip(edges, edges[1:]))
 
 
 def product(x, offsets, weight, transpose):
@@ -85,7 +85,8 @@ def weight_grads(dy, offsets, x):
 
 def sum_bound(want, size, length, dtype, parts=1):
     """A sum of `length` exact products with the terms' magnitudes `size`, as the tensor core makes
-    it (weight_grad_chunk_bound), rounded to dtype."""
+    it (weight_grad_chunk_bound), in at most `parts` parts (a GB300 has 76 pairs of SMs), rounded to
+    dtype."""
     d = weight_grad_chunk_bound(max(length, 1), parts) * size
     return d + ROUND[dtype] * (want.abs() + d) + TINY[dtype]
 

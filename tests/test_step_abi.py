@@ -273,7 +273,7 @@ def test_reference_by_hand():
     # a gradient along h is removed: y does not change with h's length
     dx, dw = S.rms_backward(h, h, torch.ones(4), rstd)
     assert dx.abs().max() < 1e-15 and dw.tolist() == pytest.approx([3.6, 6.4, 0, 0])
-    assert S.spans([-5, 3, 2, 100], 10) == [(0, 3), (3, 3), (2, 10)]
+    assert S.spans([-5, 3, 2, 100], 10) == [(0, 3), (3, 3), (3, 10)]
     x = torch.eye(2)
     w = torch.tensor([[[1.0, 2.0], [3.0, 4.0]], [[5.0, 6.0], [7.0, 8.0]]])
     out, _ = S.product(x, [0, 1, 2], w, False)
