@@ -370,7 +370,12 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
             const uint32_t count = uint32_t(s.last - s.first);
             for (uint32_t k = (step0 & 1) ^ uint32_t(turn); k < count; k += 2) {
                 const uint32_t st = (step0 + k) % kStages, round = (step0 + k) / kStages;
-                if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
+                // The stage's use before this one was the other group's (their number is odd), and
+                // loads may land out of order.  Until that use is over, `full` may still be in its
+                // phase, and then this wait would take the one before it, long complete, for its own.
+                const bool landed = (round == 0 || tc::mbar_wait(free_(st), (round & 1) ^ 1)) &&
+                                    tc::mbar_wait(full(st), round & 1);
+                if (!(ok = __all_sync(0xFFFFFFFFu, landed))) break;
                 uint32_t w[4][4], step[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
