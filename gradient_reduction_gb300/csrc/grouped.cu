@@ -54,7 +54,7 @@ constexpr int smem_bytes(int kind) {
 }
 // Registers per thread after the split of the restoring kernel (as in the
 // weight gradient of one layer); together no more than the launch's.
-constexpr int kIssueRegs = 24, kSumRegs = 168, kRestoreRegs = 56;
+constexpr int kIssueRegs = 40, kSumRegs = 160, kRestoreRegs = 56;
 static_assert(kIssueRegs + 2 * kSumRegs + 2 * kRestoreRegs <= 5 * 96, "the block's registers");
 
 }  // namespace
@@ -365,126 +365,134 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     Tile s;
     s.e = 0;
     const Work work = work_of<kSplit>(p, table, pair, pairs);
-    if constexpr (kSaved)
-        if (warp < 4) tc::give_registers<kIssueRegs>();
-    if (warp == 0) {
-        if (tc::elect_one()) {
+    if (warp < 4) {
+        // The roles of the warps that give registers up are inside this branch: behind it the
+        // compiler would count on all of the launch's again.
+        if constexpr (kSaved) tc::give_registers<kIssueRegs>();
+        if (warp == 0) {
+            if (tc::elect_one()) {
+                int st = 0;
+                uint32_t round = 0;
+                for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
+                    const int m = s.m + int(rank) * kHalf;
+                    const int half = s.size >> 1, c = s.n + int(rank) * half;
+                    for (int k = s.first; k < s.last; ++k) {
+                        if (!(ok = tc::mbar_wait(free_(st), (round & 1) ^ 1))) break;
+                        const uint32_t a = a_at + st * kOperandBytes, b = b_at + st * kOperandBytes;
+                        const int d = k * kDepth;
+                        if constexpr (kGrad) {
+                            const int t = s.k + d;
+                            if constexpr (kSaved) {
+                                tc::mbar_expect(full(st), kOperandBytes + kCodeBytes + kStepBytes);
+                                tc::tma_load(codes + st * kCodeBytes, &p.a, m, t, full(st));
+                                tc::tma_load(codes + st * kCodeBytes + kCodeBytes / 2, &p.a, m + 64, t,
+                                             full(st));
+                                tc::tma_load(steps + st * kStepBytes, &p.steps,
+                                             (m / kBlockChannels) & ~15, t, full(st));
+                            } else {
+                                tc::mbar_expect(full(st), 2 * kOperandBytes);
+                                tc::tma_load(a, &p.a, m, t, full(st));
+                                tc::tma_load(a + kGroupBytes, &p.a, m + 64, t, full(st));
+                            }
+                            tc::tma_load(b, &p.b, c, t, full(st));
+                            tc::tma_load(b + kGroupBytes, &p.b, c + 64, t, full(st));
+                        } else {
+                            tc::mbar_expect(full(st), kOperandBytes + half * kDepth * 2);
+                            if constexpr (kKind == kForward) {
+                                tc::tma_load(a, &p.a, d, m, s.e, full(st));
+                            } else {
+                                tc::tma_load(a, &p.a, m, d, s.e, full(st));
+                                tc::tma_load(a + kGroupBytes, &p.a, m + 64, d, s.e, full(st));
+                            }
+                            if (half == kHalf) {
+                                tc::tma_load(b, &p.b, d, c, full(st));
+                            } else {
+                                for (int r = 0; r < half; r += kPiece)
+                                    tc::tma_load(b + r * kDepth * 2, &p.b_piece, d, c + r, full(st));
+                            }
+                        }
+                        if (++st == kStages) { st = 0; ++round; }
+                    }
+                }
+                // every load has landed and every signal of the matrix instructions has arrived
+                // here before the CTA may leave: the last use of each stage
+                const uint32_t total = round * kStages + st;
+                for (int k = 0; k < kStages; ++k) {
+                    const uint32_t uses = total / kStages + (uint32_t(k) < total % kStages);
+                    if (uses == 0) continue;
+                    ok &= tc::mbar_wait(full(k), (uses - 1) & 1);
+                    if (ok) ok = tc::mbar_wait(free_(k), (uses - 1) & 1);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (rank == 0 && tc::elect_one()) {
+                constexpr bool kAlongM = kKind != kForward, kAlongN = kGrad;
+                // 16 elements further along the sum
+                constexpr uint32_t a_next = (kAlongM ? 2048 : 32) >> 4;
+                constexpr uint32_t b_next = (kAlongN ? 2048 : 32) >> 4;
+                const uint64_t a0 = kAlongM ? tc::operand(a_at, kGroupBytes, 1024)
+                                            : tc::operand_along_k(a_at);
+                const uint64_t b0 = kAlongN ? tc::operand(b_at, kGroupBytes, 1024)
+                                            : tc::operand_along_k(b_at);
+                uint32_t st = 0, round = 0, acc = 0, acc_round = 0;
+                for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
+                    const uint32_t instruction = tc::bf16_instruction(kTile, s.size, kAlongM, kAlongN);
+                    for (int left = s.last - s.first; ok && left > 0; left -= kChunk) {
+                        if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
+                        const uint32_t d = tmem + acc * kTile;
+                        bool add = false;
+                        for (int k = min(left, kChunk); k > 0; --k) {
+                            if (!(ok = tc::mbar_wait(ready(st), round & 1))) break;
+                            tc::fence_after_sync();
+                            const uint64_t a = a0 + st * (kOperandBytes >> 4);
+                            const uint64_t b = b0 + st * (kOperandBytes >> 4);
+#pragma unroll
+                            for (int j = 0; j < kDepth / 16; ++j) {
+                                tc::mma(d, a + j * a_next, b + j * b_next, instruction, add);
+                                add = true;
+                            }
+                            tc::commit_both(free_(st));
+                            if (++st == kStages) { st = 0; ++round; }
+                        }
+                        if (!ok) break;
+                        tc::commit_both(summed(acc));
+                        if (++acc == 2) { acc = 0; ++acc_round; }
+                    }
+                }
+                // the other CTA's last signals have to land here before this one may leave
+                for (uint32_t a = 0; a < 2; ++a) {
+                    const uint32_t uses = acc_round + (a < acc);
+                    if (ok && uses > 0) ok = tc::mbar_wait(stored(a), (uses - 1) & 1);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 2 && !kSaved) {
             int st = 0;
             uint32_t round = 0;
             for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
-                const int m = s.m + int(rank) * kHalf;
-                const int half = s.size >> 1, c = s.n + int(rank) * half;
                 for (int k = s.first; k < s.last; ++k) {
-                    if (!(ok = tc::mbar_wait(free_(st), (round & 1) ^ 1))) break;
-                    const uint32_t a = a_at + st * kOperandBytes, b = b_at + st * kOperandBytes;
-                    const int d = k * kDepth;
-                    if constexpr (kGrad) {
-                        const int t = s.k + d;
-                        if constexpr (kSaved) {
-                            tc::mbar_expect(full(st), kOperandBytes + kCodeBytes + kStepBytes);
-                            tc::tma_load(codes + st * kCodeBytes, &p.a, m, t, full(st));
-                            tc::tma_load(codes + st * kCodeBytes + kCodeBytes / 2, &p.a, m + 64, t,
-                                         full(st));
-                            tc::tma_load(steps + st * kStepBytes, &p.steps,
-                                         (m / kBlockChannels) & ~15, t, full(st));
-                        } else {
-                            tc::mbar_expect(full(st), 2 * kOperandBytes);
-                            tc::tma_load(a, &p.a, m, t, full(st));
-                            tc::tma_load(a + kGroupBytes, &p.a, m + 64, t, full(st));
+                    if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
+                    const int valid = s.k_count - k * kDepth;
+                    if (kGrad && valid < kDepth) {
+                        // rows of the step that belong to no token of the expert: 128 bytes in
+                        // each group of 64 channels, whatever the order of the pieces in them
+                        for (int r = valid + (lane >> 3); r < kDepth; r += 4) {
+                            const uint32_t at = st * kOperandBytes + r * 128 + (lane & 7) * 16;
+                            store_shared(a_at + at, 0, 0, 0, 0);
+                            store_shared(a_at + at + kGroupBytes, 0, 0, 0, 0);
+                            store_shared(b_at + at, 0, 0, 0, 0);
+                            store_shared(b_at + at + kGroupBytes, 0, 0, 0, 0);
                         }
-                        tc::tma_load(b, &p.b, c, t, full(st));
-                        tc::tma_load(b + kGroupBytes, &p.b, c + 64, t, full(st));
-                    } else {
-                        tc::mbar_expect(full(st), kOperandBytes + half * kDepth * 2);
-                        if constexpr (kKind == kForward) {
-                            tc::tma_load(a, &p.a, d, m, s.e, full(st));
-                        } else {
-                            tc::tma_load(a, &p.a, m, d, s.e, full(st));
-                            tc::tma_load(a + kGroupBytes, &p.a, m + 64, d, s.e, full(st));
-                        }
-                        if (half == kHalf) {
-                            tc::tma_load(b, &p.b, d, c, full(st));
-                        } else {
-                            for (int r = 0; r < half; r += kPiece)
-                                tc::tma_load(b + r * kDepth * 2, &p.b_piece, d, c + r, full(st));
-                        }
+                        tc::fence_to_async();
+                        __syncwarp();
                     }
+                    if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(st), 0));
                     if (++st == kStages) { st = 0; ++round; }
                 }
             }
-            // every load has landed and every signal of the matrix instructions has arrived
-            // here before the CTA may leave: the last use of each stage
-            const uint32_t total = round * kStages + st;
-            for (int k = 0; k < kStages; ++k) {
-                const uint32_t uses = total / kStages + (uint32_t(k) < total % kStages);
-                if (uses == 0) continue;
-                ok &= tc::mbar_wait(full(k), (uses - 1) & 1);
-                if (ok) ok = tc::mbar_wait(free_(k), (uses - 1) & 1);
-            }
         }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (rank == 0 && tc::elect_one()) {
-            constexpr bool kAlongM = kKind != kForward, kAlongN = kGrad;
-            // 16 elements further along the sum
-            constexpr uint32_t a_next = (kAlongM ? 2048 : 32) >> 4;
-            constexpr uint32_t b_next = (kAlongN ? 2048 : 32) >> 4;
-            const uint64_t a0 = kAlongM ? tc::operand(a_at, kGroupBytes, 1024)
-                                        : tc::operand_along_k(a_at);
-            const uint64_t b0 = kAlongN ? tc::operand(b_at, kGroupBytes, 1024)
-                                        : tc::operand_along_k(b_at);
-            uint32_t st = 0, round = 0, acc = 0, acc_round = 0;
-            for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
-                const uint32_t instruction = tc::bf16_instruction(kTile, s.size, kAlongM, kAlongN);
-                for (int left = s.last - s.first; ok && left > 0; left -= kChunk) {
-                    if (!(ok = tc::mbar_wait(stored(acc), (acc_round & 1) ^ 1))) break;
-                    const uint32_t d = tmem + acc * kTile;
-                    bool add = false;
-                    for (int k = min(left, kChunk); k > 0; --k) {
-                        if (!(ok = tc::mbar_wait(ready(st), round & 1))) break;
-                        tc::fence_after_sync();
-                        const uint64_t a = a0 + st * (kOperandBytes >> 4);
-                        const uint64_t b = b0 + st * (kOperandBytes >> 4);
-#pragma unroll
-                        for (int j = 0; j < kDepth / 16; ++j) {
-                            tc::mma(d, a + j * a_next, b + j * b_next, instruction, add);
-                            add = true;
-                        }
-                        tc::commit_both(free_(st));
-                        if (++st == kStages) { st = 0; ++round; }
-                    }
-                    if (!ok) break;
-                    tc::commit_both(summed(acc));
-                    if (++acc == 2) { acc = 0; ++acc_round; }
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == 2 && !kSaved) {
-        int st = 0;
-        uint32_t round = 0;
-        for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
-            for (int k = s.first; k < s.last; ++k) {
-                if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
-                const int valid = s.k_count - k * kDepth;
-                if (kGrad && valid < kDepth) {
-                    // rows of the step that belong to no token of the expert: 128 bytes in
-                    // each group of 64 channels, whatever the order of the pieces in them
-                    for (int r = valid + (lane >> 3); r < kDepth; r += 4) {
-                        const uint32_t at = st * kOperandBytes + r * 128 + (lane & 7) * 16;
-                        store_shared(a_at + at, 0, 0, 0, 0);
-                        store_shared(a_at + at + kGroupBytes, 0, 0, 0, 0);
-                        store_shared(b_at + at, 0, 0, 0, 0);
-                        store_shared(b_at + at + kGroupBytes, 0, 0, 0, 0);
-                    }
-                    tc::fence_to_async();
-                    __syncwarp();
-                }
-                if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(st), 0));
-                if (++st == kStages) { st = 0; ++round; }
-            }
-        }
-    } else if (warp >= 4 && warp < 4 + kSumWarps) {
+    } else if (warp < 4 + kSumWarps) {
         if constexpr (kSaved) tc::take_registers<kSumRegs>();
         constexpr int kColumns = kTile / 2;
         const int quarter = warp & 3;               // the lanes this warp may read
@@ -570,7 +578,12 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
             const int count = s.last - s.first;
             for (int k = (step0 & 1) ^ turn; k < count; k += 2) {
                 const uint32_t st = (step0 + k) % kStages, round = (step0 + k) / kStages;
-                if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
+                // The stage's use before this one was the other group's (their number is odd), and
+                // loads may land out of order.  Until that use is over, `full` may still be in its
+                // phase, and then this wait would take the one before it, long complete, for its own.
+                const bool landed = (round == 0 || tc::mbar_wait(free_(st), (round & 1) ^ 1)) &&
+                                    tc::mbar_wait(full(st), round & 1);
+                if (!(ok = __all_sync(0xFFFFFFFFu, landed))) break;
                 const int valid = s.k_count - (s.first + k) * kDepth;
                 uint32_t w[4][4], step[4];
 #pragma unroll
@@ -617,7 +630,8 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     }
     if (!ok) atomicAdd(&g_wait_failures, 1u);
     __syncwarp();
-    // nobody leaves while the other CTA may still signal or read this one
+    // Nobody leaves while the other CTA may still signal or read this one: every signal has been
+    // waited for by a thread of the CTA that it goes to, so this barrier need not order them.
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_meet();

@@ -26,7 +26,9 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The same without ordering memory: the stores before it need not have arrived
-// (which takes about a microsecond).
+// (which takes about a microsecond).  A signal to another CTA's barrier may then
+// still be on its way: a CTA may leave after it only if it has waited for all that
+// it is sent.
 __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }

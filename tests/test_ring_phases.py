@@ -70,7 +70,7 @@ def test_without_it_some_are():
     assert any(run(60, False, rng) for _ in range(2000))
 
 
-@pytest.mark.parametrize("name", ["weight_grad.cu"])
+@pytest.mark.parametrize("name", ["grouped.cu", "weight_grad.cu"])
 def test_the_kernels_have_the_guard(name):
     code = open(os.path.join(ROOT, "gradient_reduction_gb300", "csrc", name)).read()
     assert re.search(r"round == 0 \|\| tc::mbar_wait\(free_\(st\), \(round & 1\) \^ 1\)\) &&\s+"
