@@ -16,15 +16,20 @@ from ._operators import (_DTYPES, _CheckpointArg, _checkpoint_arg, _code, _devic
                          _vector, _workspace, _workspace_bytes, _wrong_device, _wrong_shape)
 
 
-def _optional(t, rows: int, width: int, dtype, what: str, dev: int):
-    """(address, row stride) of a matrix of this shape and type; zeros for None."""
+def _like(t, shape, rows: int, width: int, dtype, what: str, dev: int):
+    """(address, row stride) of a matrix of `rows` x `width` and this type;
+    zeros for None.  A tensor of the call's own shape takes the short way."""
     if t is None:
         return 0, 0
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: need {dtype}, got {t.dtype}")
+    if len(shape) == 2 and t.shape == shape and t.get_device() == dev:
+        stride, inner = t.stride()
+        if inner == 1 and stride >= width:
+            return t.data_ptr(), stride
     p, r, w, stride = _matrix(t, what, dev)
     if r != rows or w != width:
         _wrong_shape(what, r, w, rows, width)
-    if t.dtype != dtype:
-        raise ValueError(f"{what}: need {dtype}, got {t.dtype}")
     return p, stride
 
 
@@ -42,9 +47,10 @@ def dpr_rmsnorm_forward(x: torch.Tensor, weight, eps: float, y=None, rstd=None, 
     as dpr_checkpoint_save(h) and (y) would; with y_checkpoint y may be None."""
     dev = _device(x, "x")
     px, rows, width, sx = _matrix(x, "x", dev)
-    pr, sr = _optional(residual, rows, width, x.dtype, "residual", dev)
-    ph, sh = _optional(h, rows, width, x.dtype, "h", dev)
-    py, sy = _optional(y, rows, width, x.dtype, "y", dev)
+    shape, dtype = x.shape, x.dtype
+    pr, sr = _like(residual, shape, rows, width, dtype, "residual", dev)
+    ph, sh = _like(h, shape, rows, width, dtype, "h", dev)
+    py, sy = _like(y, shape, rows, width, dtype, "y", dev)
     st = lib().dpr_rmsnorm_forward(
         px, sx, pr, sr, rows, width, _code(x, "x"), _vector(weight, width, "weight", dev),
         0 if weight is None else _code(weight, "weight"), eps, ph, sh, py, sy,
@@ -64,14 +70,15 @@ def dpr_rmsnorm_backward(dy: torch.Tensor, h, weight, rstd: torch.Tensor, dx: to
     `accumulate`."""
     dev = _device(dy, "dy")
     pd, rows, width, sd = _matrix(dy, "dy", dev)
-    po, so = _optional(dx, rows, width, dy.dtype, "dx", dev)
-    if not po and rows > 0:
+    shape, dtype = dy.shape, dy.dtype
+    if dx is None:
         raise ValueError("dx is needed")
-    pe, se = _optional(dh, rows, width, dy.dtype, "dh", dev)
+    po, so = _like(dx, shape, rows, width, dtype, "dx", dev)
+    pe, se = _like(dh, shape, rows, width, dtype, "dh", dev)
     ph = sh = 0
     ref = None
     if isinstance(h, torch.Tensor):
-        ph, sh = _optional(h, rows, width, dy.dtype, "h", dev)
+        ph, sh = _like(h, shape, rows, width, dtype, "h", dev)
     else:
         ref = ctypes.byref(_checkpoint_arg(h, "h", rows, width, dev))
     if rstd is None:
