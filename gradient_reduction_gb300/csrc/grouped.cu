@@ -255,16 +255,40 @@ __device__ __forceinline__ void store_shared(uint32_t at, uint32_t a, uint32_t b
                  "r"(d) : "memory");
 }
 
+// The old values of a column that will be added to, all loads in flight together;
+// bf16 as it is, in the lower half.
+template <bool kBf16, int kN>
+__device__ __forceinline__ void load_column(const char* q, int64_t stride, int count, float (&old)[kN]) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+        old[j] = 0.0f;
+        if (j < count) {
+            if constexpr (kBf16) {
+                uint32_t h;
+                asm volatile("ld.global.u16 %0, [%1];" : "=r"(h) : "l"(q) : "memory");
+                old[j] = __uint_as_float(h);
+            } else {
+                asm volatile("ld.global.f32 %0, [%1];" : "=f"(old[j]) : "l"(q) : "memory");
+            }
+        }
+        q += stride;
+        asm volatile("" : "+l"(q));
+    }
+}
+
 // Consecutive rows of the output at one column: `count` of a thread's kN sums,
 // the rows `stride` bytes apart.  With kAdd the old values of 16 rows are
 // loaded together.  The address advances step by step and is hidden from the
 // compiler, which would otherwise compute all of them at once and spill the sums.
+// `pause` (ns) keeps 16 rows from the next 16: all pairs store at about the same
+// time, and the loads of the next tile wait behind their stores.
 template <bool kBf16, bool kAdd, int kN>
 __device__ __forceinline__ void store_column(char* d, int64_t stride, int count,
-                                             const float (&sum)[kN]) {
+                                             const float (&sum)[kN], unsigned pause = 0) {
 #pragma unroll
     for (int j0 = 0; j0 < kN; j0 += 16) {
         if (j0 >= count) break;
+        if (pause) __nanosleep(pause);
         float old[16];
         if constexpr (kAdd) {
             const char* q = d;
@@ -503,11 +527,34 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
         for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
             const int half = s.size >> 1;           // a multiple of 16
             const int last = s.last;
+            // A sum of one accumulator is added to the old values, loaded while it is being made:
+            // rounded once, as by adding them behind it, but with a tile's loads in flight together
+            // (16384 tokens, 32 experts of 4864 x 4096: fp32 1265 us without, 1069 with; bf16 1161
+            // and 681).
+            const bool preload = kGrad && !kSplit && p.accumulate && s.steps <= kChunk;
+            if (preload && s.steps > 0) {
+                const int f = s.m + int(rank) * kHalf + quarter * 32 + lane;
+                const int count = f < p.m_size ? min(half, s.columns - side * half) : 0;
+                const int64_t size = p.out_bf16 ? 2 : 4;
+                const char* q = static_cast<const char*>(p.out) +
+                                (int64_t(s.n + side * half) * p.out_stride + int64_t(s.e) * p.out_expert_stride + f) * size;
+                if (p.out_bf16) load_column<true>(q, p.out_stride * size, count, sum);
+                else load_column<false>(q, p.out_stride * size, count, sum);
+            } else {
 #pragma unroll
-            for (int j = 0; j < kColumns; ++j) sum[j] = 0.0f;
+                for (int j = 0; j < kColumns; ++j) sum[j] = 0.0f;
+            }
             for (int k = s.first; k < last; k += kChunk) {
                 if (!(ok = tc::mbar_wait_warp(summed(acc), acc_round & 1))) break;
                 tc::fence_after_sync();
+                if (preload && p.out_bf16) {
+#pragma unroll
+                    for (int j = 0; j < kColumns; ++j) {
+                        uint32_t v = __float_as_uint(sum[j]);
+                        asm volatile("shl.b32 %0, %0, 16;" : "+r"(v));
+                        sum[j] = __uint_as_float(v);
+                    }
+                }
                 const uint32_t from = tmem + acc * kTile + side * half + (uint32_t(quarter) << 21);
 #pragma unroll
                 for (int c = 0; c < kColumns; c += 16) {
@@ -546,12 +593,16 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
                 const int64_t size = p.out_bf16 ? 2 : 4;
                 char* d = static_cast<char*>(p.out) + (at + int64_t(side * half) * p.out_stride + f) * size;
                 const int64_t stride = p.out_stride * size;
+                // fp32 tiles spread their stores over 4 us of the next one's sum, which has to take
+                // longer; bf16's, and those of sums that wait for restored operands, are no
+                // hindrance (16384 tokens, 8 experts of 4864 x 4096: 373 us without, 361 with)
+                const bool more = kKind == kWeightGrad && s.steps >= kChunk && s.next < work.end;
                 if (p.out_bf16) {
-                    if (kGrad && p.accumulate) store_column<true, true>(d, stride, count, sum);
+                    if (kGrad && p.accumulate && !preload) store_column<true, true>(d, stride, count, sum);
                     else store_column<true, false>(d, stride, count, sum);
                 } else {
-                    if (kGrad && p.accumulate) store_column<false, true>(d, stride, count, sum);
-                    else store_column<false, false>(d, stride, count, sum);
+                    if (kGrad && p.accumulate && !preload) store_column<false, true>(d, stride, count, sum);
+                    else store_column<false, false>(d, stride, count, sum, more ? 500 : 0);
                 }
             }
         }
@@ -845,8 +896,8 @@ struct Plan {
 // whole tiles would leave pairs idle for more steps than that second kernel and its
 // launch take (kSplitGain, some 5 us).  Tiles of few columns wait for
 // memory, not for the tensor core: fewer pairs at once then go on faster (0.25 us a step
-// against 0.36 with all of them).  3072 tokens, 184 x 412, weight gradient: 24.3 us
-// whole, 13.7 split; 32 tokens over 8 experts of 11008 x 4096, input gradient (128
+// against 0.36 with all of them).  16384 tokens, 200 x 512, weight gradient: 77.6 us
+// whole, 19.8 split; 32 tokens over 8 experts of 11008 x 4096, input gradient (128
 // tiles of few columns): 107 whole, 113 split.
 constexpr double kSplitGain = 16;
 Plan plan_work(int64_t tiles, double steps, int64_t columns, double each) {
