@@ -293,7 +293,10 @@ def dpr_grad_plan_destroy(plan: GradPlan) -> None:
 def _norm(plan: GradPlan, norm: torch.Tensor) -> int:
     if plan.handle is None:
         raise ValueError("the plan is closed")
-    return _statistic(norm, 1, "norm", _device(norm, "norm"))
+    dev = _device(norm, "norm")
+    if dev != plan.device:
+        raise ValueError(f"the plan's tensors are on cuda:{plan.device}, norm is on cuda:{dev}")
+    return _statistic(norm, 1, "norm", dev)
 
 
 def dpr_grad_norm(plan: GradPlan, norm: torch.Tensor, scale: float = 1.0, workspace=None,

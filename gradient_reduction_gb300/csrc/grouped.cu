@@ -19,6 +19,14 @@
 //
 // Sums run over 1024 elements in tensor memory, whose accumulation truncates,
 // and are then added, rounded, to fp32 sums in registers.
+//
+// Weights whose rows are not 16-byte aligned cannot be loaded as they lie, but
+// every eighth row of them can: eight rows further a row starts at the same place
+// within 16 bytes.  So eight maps, each over its eighth of the rows, load pieces
+// of rows with the (at most seven) elements in front of them, and eight warps
+// move them to their places on the way (kForwardOdd, kInputGradOdd), as others
+// restore checkpoints.
+#include <type_traits>
 #include <algorithm>
 #include <atomic>
 
@@ -30,7 +38,7 @@ namespace dpr {
 
 namespace {
 
-enum Product { kForward, kInputGrad, kWeightGrad, kWeightGradSaved };
+enum Product { kForward, kInputGrad, kForwardOdd, kInputGradOdd, kWeightGrad, kWeightGradSaved };
 
 constexpr int kTile = 256;               // features, and columns at most, of a tile
 constexpr int kHalf = 128;               // of each CTA
@@ -40,20 +48,25 @@ constexpr int kOperandBytes = kHalf * kDepth * 2;
 constexpr int kGroupBytes = 64 * kDepth * 2;     // 64 channels of an operand along M or N
 constexpr int kCodeBytes = kHalf * kDepth;
 constexpr int kStepBytes = 16 * kDepth;  // 16 step bytes a token, 4 of them used
+constexpr int kRawBytes = kHalf * (kDepth + 8) * 2;  // of a step's unaligned weights, at most
 constexpr int kPiece = 16;               // rows of a load of part of a tile's tokens
 constexpr int kSumWarps = 8;
 constexpr int kRestoreWarps = 4;         // of each of the two groups
 constexpr int kPairs = 76;               // of a GB300's 152 SMs
 
 __host__ __device__ constexpr bool is_weight_grad(int kind) { return kind >= kWeightGrad; }
-__host__ __device__ constexpr int stages(int kind) { return kind == kWeightGradSaved ? 5 : 6; }
-__host__ __device__ constexpr int threads(int kind) { return kind == kWeightGradSaved ? 640 : 384; }
+__host__ __device__ constexpr bool is_odd(int kind) { return kind == kForwardOdd || kind == kInputGradOdd; }
+// Kinds whose M side is made on the way, by two more groups of warps.
+__host__ __device__ constexpr bool is_made(int kind) { return kind == kWeightGradSaved || is_odd(kind); }
+__host__ __device__ constexpr int stages(int kind) { return is_odd(kind) ? 4 : is_made(kind) ? 5 : 6; }
+__host__ __device__ constexpr int threads(int kind) { return is_made(kind) ? 640 : 384; }
 constexpr int smem_bytes(int kind) {
-    return 1024 + stages(kind) * (2 * kOperandBytes +
-                                  (kind == kWeightGradSaved ? kCodeBytes + kStepBytes : 0));
+    return 1024 + stages(kind) * (2 * kOperandBytes + (is_odd(kind)    ? kRawBytes
+                                                       : is_made(kind) ? kCodeBytes + kStepBytes
+                                                                       : 0));
 }
-// Registers per thread after the split of the restoring kernel (as in the
-// weight gradient of one layer); together no more than the launch's.
+// Registers per thread after the split of those kernels (as in the weight
+// gradient of one layer); together no more than the launch's.
 constexpr int kIssueRegs = 40, kSumRegs = 160, kRestoreRegs = 56;
 static_assert(kIssueRegs + 2 * kSumRegs + 2 * kRestoreRegs <= 5 * 96, "the block's registers");
 
@@ -81,6 +94,14 @@ struct GroupedParams {
     int slot_columns;        // columns of a part's room, which has kTile features
     float* partial;          // [2 * pairs][slot_columns][kTile]
     struct GroupedPart* parts;   // [2 * pairs]
+};
+
+// Weights whose rows are not aligned: rows j, j + 8, j + 16 and so on of all
+// experts are map j's, which begins at the 16 bytes that hold row j's start.
+struct GroupedOddParams : GroupedParams {
+    CUtensorMap odd[8];
+    int weight_rows;         // of an expert
+    unsigned start, step;    // bytes behind 16 of row 0, and from row to row
 };
 
 // A part of a tile that begins its sum; the next pairs' first parts follow it.
@@ -276,6 +297,26 @@ __device__ __forceinline__ void load_column(const char* q, int64_t stride, int c
     }
 }
 
+__device__ __forceinline__ uint32_t select_word(uint32_t which, uint32_t yes, uint32_t no) {
+    uint32_t r;
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tselp.b32 %0, %2, %3, p;\n\t}"
+        : "=r"(r) : "r"(which), "r"(yes), "r"(no));
+    return r;
+}
+
+// The 16 bytes that begin 4 * `words` bytes and `bits` bits in 32: to w[0 .. 3].
+// A word's choice is a select: lanes of one warp shift differently, and with the
+// branches that a choice of four by ?: becomes a step of unaligned weights took
+// 1.3 us instead of 0.47.
+__device__ __forceinline__ void shift_words(uint32_t (&w)[8], uint32_t words, uint32_t bits) {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = select_word(words & 2, w[k + 2], w[k]);
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = select_word(words & 1, w[k + 1], w[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], bits);
+}
+
 // Consecutive rows of the output at one column: `count` of a thread's kN sums,
 // the rows `stride` bytes apart.  With kAdd the old values of 16 rows are
 // loaded together.  The address advances step by step and is hidden from the
@@ -323,15 +364,24 @@ __device__ __forceinline__ void store_column(char* d, int64_t stride, int count,
     }
 }
 
+template <int kKind>
+using KindParams = std::conditional_t<is_odd(kKind), GroupedOddParams, GroupedParams>;
+
 // Warps of a CTA: 0 issues the TMA loads, 1 the matrix instructions (first CTA
 // only), 4-11 keep the sums and store them.  2 passes a loaded stage on to the
-// first CTA (and writes the zeros behind an expert's last token); with
-// checkpoints 12-19 do, which restore x on the way, in two groups that take turns.
+// first CTA (and writes the zeros behind an expert's last token); where the M
+// side is made on the way 12-19 do, in two groups that take turns: they restore
+// checkpoints, or move unaligned weights to their places.
 template <int kKind, bool kSplit>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kKind), 1)
-grouped_pairs(const __grid_constant__ GroupedParams p) {
+grouped_pairs(const __grid_constant__ KindParams<kKind> p) {
     constexpr bool kGrad = is_weight_grad(kKind);
     constexpr bool kSaved = kKind == kWeightGradSaved;
+    constexpr bool kOdd = is_odd(kKind), kMade = is_made(kKind);
+    constexpr bool kWeightAlongK = kKind == kForward || kKind == kForwardOdd;   // else along M
+    // a load of unaligned weights: 72 x 16 of them, or 136 x 8
+    constexpr int kOddRows = kWeightAlongK ? 16 : 8;
+    constexpr int kOddPitch = ((kWeightAlongK ? kDepth : kHalf) + 8) * 2;
     constexpr int kStages = stages(kKind);
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[3 * kStages + 4];
@@ -344,6 +394,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     const uint32_t b_at = base + kStages * kOperandBytes;        // [kStages]
     const uint32_t codes = base + 2 * kStages * kOperandBytes;   // [kStages], with checkpoints
     const uint32_t steps = codes + kStages * kCodeBytes;         // [kStages]
+    const uint32_t pieces = codes;                               // [kStages], of unaligned weights
     const uint32_t bar0 = tc::smem_addr(bars);
     const auto full = [&](int s) { return bar0 + 8u * s; };                      // loads landed
     const auto free_ = [&](int s) { return bar0 + 8u * (kStages + s); };         // stage consumed
@@ -361,7 +412,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
             const int of = lane / kStages;
             tc::mbar_init(bar0 + 8u * lane,
                           of < 2                    ? 1
-                          : of == 2                 ? (kSaved ? 2 * kRestoreWarps : 2)
+                          : of == 2                 ? (kMade ? 2 * kRestoreWarps : 2)
                           : lane < 3 * kStages + 2  ? 1
                                                     : 2 * kSumWarps);
         }
@@ -369,11 +420,13 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     }
     if (threadIdx.x == 64) {
         if (p.rows > 0) {                // else the maps are empty
-            tc::tma_prefetch_map(&p.a);
+            if constexpr (!kOdd) tc::tma_prefetch_map(&p.a);
             tc::tma_prefetch_map(&p.b);
         }
         if constexpr (!kGrad) tc::tma_prefetch_map(&p.b_piece);
         if constexpr (kSaved) tc::tma_prefetch_map(&p.steps);
+        if constexpr (kOdd)
+            for (int j = 0; j < 8; ++j) tc::tma_prefetch_map(&p.odd[j]);
     }
     if (warp == 1) tc::tmem_alloc(tc::smem_addr(&tmem_slot), 512);
     tc::fence_before_sync();
@@ -392,7 +445,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
     if (warp < 4) {
         // The roles of the warps that give registers up are inside this branch: behind it the
         // compiler would count on all of the launch's again.
-        if constexpr (kSaved) tc::give_registers<kIssueRegs>();
+        if constexpr (kMade) tc::give_registers<kIssueRegs>();
         if (warp == 0) {
             if (tc::elect_one()) {
                 int st = 0;
@@ -421,8 +474,15 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
                             tc::tma_load(b, &p.b, c, t, full(st));
                             tc::tma_load(b + kGroupBytes, &p.b, c + 64, t, full(st));
                         } else {
-                            tc::mbar_expect(full(st), kOperandBytes + half * kDepth * 2);
-                            if constexpr (kKind == kForward) {
+                            tc::mbar_expect(full(st), (kOdd ? 8 * kOddRows * kOddPitch : kOperandBytes) +
+                                                          half * kDepth * 2);
+                            if constexpr (kOdd) {
+                                const int row = s.e * p.weight_rows + (kWeightAlongK ? m : d);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    tc::tma_load(pieces + st * kRawBytes + j * kOddRows * kOddPitch, &p.odd[j],
+                                                 kWeightAlongK ? d : m, (row - j + 7) >> 3, full(st));
+                            } else if constexpr (kKind == kForward) {
                                 tc::tma_load(a, &p.a, d, m, s.e, full(st));
                             } else {
                                 tc::tma_load(a, &p.a, m, d, s.e, full(st));
@@ -451,7 +511,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
             __syncwarp();
         } else if (warp == 1) {
             if (rank == 0 && tc::elect_one()) {
-                constexpr bool kAlongM = kKind != kForward, kAlongN = kGrad;
+                constexpr bool kAlongM = !kWeightAlongK, kAlongN = kGrad;
                 // 16 elements further along the sum
                 constexpr uint32_t a_next = (kAlongM ? 2048 : 32) >> 4;
                 constexpr uint32_t b_next = (kAlongN ? 2048 : 32) >> 4;
@@ -491,7 +551,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
                 }
             }
             __syncwarp();
-        } else if (warp == 2 && !kSaved) {
+        } else if (warp == 2 && !kMade) {
             int st = 0;
             uint32_t round = 0;
             for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
@@ -517,7 +577,7 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
             }
         }
     } else if (warp < 4 + kSumWarps) {
-        if constexpr (kSaved) tc::take_registers<kSumRegs>();
+        if constexpr (kMade) tc::take_registers<kSumRegs>();
         constexpr int kColumns = kTile / 2;
         const int quarter = warp & 3;               // the lanes this warp may read
         const int side = (warp - 4) >> 2;           // half of the columns
@@ -677,6 +737,57 @@ grouped_pairs(const __grid_constant__ GroupedParams p) {
                 if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(st), 0));
             }
             step0 += uint32_t(count);
+        }
+    } else if (kOdd && warp >= 12) {
+        if constexpr (kOdd) {
+            tc::give_registers<kRestoreRegs>();
+            const int turn = (warp - 12) >> 2;
+            // 16 bytes of a row a lane; 8 neighbouring lanes read and write 128 consecutive bytes of a
+            // row, whose 16-byte pieces are permuted by the row's number where they are written
+            constexpr int kLanes = kWeightAlongK ? 8 : 16, kRows = 128 / kLanes;
+            const int at = int(threadIdx.x) & 127, row0 = at / kLanes, c = at % kLanes;
+            const uint32_t write = uint32_t((c >> 3) * kGroupBytes + row0 * 128 + ((c ^ row0) & 7) * 16);
+            uint32_t step0 = 0;                     // steps of the tiles before
+            for (int n = work.begin; ok && tile_at<kKind, kSplit>(p, table, work, n, s); n = s.next) {
+                const int count = s.last - s.first;
+                for (int k = int(step0 & 1) ^ turn; k < count; k += 2) {
+                    // the stages' number is even: a group always has the same ones and waits for each
+                    // of their uses
+                    const uint32_t st = (step0 + k) % kStages, round = (step0 + k) / kStages;
+                    if (!(ok = tc::mbar_wait_warp(full(st), round & 1))) break;
+                    const int d = (s.first + k) * kDepth;
+                    const int first = s.e * p.weight_rows + (kWeightAlongK ? s.m + int(rank) * kHalf : d);
+                    const int row = first + row0, j = row & 7;
+                    const uint32_t read = pieces + st * kRawBytes +
+                                          (j * kOddRows + (row >> 3) - ((first - j + 7) >> 3)) * kOddPitch + c * 16;
+                    const uint32_t shift = (p.start + uint32_t(j) * p.step) & 15;
+                    const uint32_t words = shift >> 2, bits = (shift & 3) * 8;
+                    // rows of the sum behind the expert's last one
+                    const int valid = kWeightAlongK ? kHalf : p.k_size - d;
+                    const uint32_t to = a_at + st * kOperandBytes + write;
+#pragma unroll 2
+                    for (int i0 = 0; i0 < 8; i0 += 2) {     // two rows' loads in flight
+                        uint32_t w[2][8];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t* v = w[h >> 1] + 4 * (h & 1);
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                         : "r"(read + (i0 + (h >> 1)) * (kRows / 8) * kOddPitch + (h & 1) * 16));
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            shift_words(w[h], words, bits);
+                            if ((i0 + h) * kRows + row0 >= valid) w[h][0] = w[h][1] = w[h][2] = w[h][3] = 0;
+                            store_shared(to + (i0 + h) * kRows * 128, w[h][0], w[h][1], w[h][2], w[h][3]);
+                        }
+                    }
+                    tc::fence_to_async();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tc::map_to(ready(st), 0));
+                }
+                step0 += uint32_t(count);
+            }
         }
     }
     if (!ok) atomicAdd(&g_wait_failures, 1u);
@@ -926,7 +1037,7 @@ Plan grad_plan(int64_t rows, int64_t experts, int64_t out_features, int64_t in_f
 }
 
 template <int kKind, bool kSplit>
-cudaError_t launch_kernel(GroupedParams& p, const Plan& q, cudaStream_t s) {
+cudaError_t launch_kernel(KindParams<kKind>& p, const Plan& q, cudaStream_t s) {
     static std::atomic<uint64_t> allowed{0};
     const void* k = (const void*)grouped_pairs<kKind, kSplit>;
     const cudaError_t e = allow_shared_memory(k, smem_bytes(kKind), &allowed);
@@ -936,14 +1047,14 @@ cudaError_t launch_kernel(GroupedParams& p, const Plan& q, cudaStream_t s) {
 }
 
 template <int kKind>
-cudaError_t launch_pairs(GroupedParams& p, const Plan& q, char* ws, cudaStream_t s) {
+cudaError_t launch_pairs(KindParams<kKind>& p, const Plan& q, char* ws, cudaStream_t s) {
     if (!q.split) return launch_kernel<kKind, false>(p, q, s);
     p.slot_columns = int(q.slot_columns);
     p.partial = reinterpret_cast<float*>(ws);
     p.parts = reinterpret_cast<GroupedPart*>(ws + q.partial_bytes);
     const cudaError_t e = launch_kernel<kKind, true>(p, q, s);
     if (e != cudaSuccess) return e;
-    void* args[] = {&p};
+    void* args[] = {static_cast<GroupedParams*>(&p)};
     return launch_grid((const void*)grouped_join,
                        dim3(unsigned(2 * q.pairs), unsigned(q.slot_columns / kJoinColumns)), dim3(kTile), 0,
                        args, s);
@@ -984,12 +1095,45 @@ dpr_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
     return aligned(ws, 16) ? DPR_OK : DPR_ERR_ALIGNMENT;
 }
 
-// The operands of the product (x) or of the input gradient (dy).
-void operands(bool input_grad, const void* x, int64_t x_stride, int64_t rows, int64_t experts,
+// Unaligned weights are read as they lie where their rows follow one another
+// through all experts, unless so many tokens read them that copying them once is
+// faster.  8 experts of 11008 x 4095, product (input gradient): 32 tokens 152 us
+// (155) as they lie, 404 (399) copied; 4096 tokens 329 (352) and 501 (509); 16384
+// tokens 1090 (1229) and 1039 (1069).  Aligned weights take 115 us for 32 tokens.
+constexpr int64_t kOddTokens = 1024;     // an expert, on average
+bool read_odd(const Operand& w, int64_t rows) {
+    const int64_t experts = w.rows / w.inner;
+    return w.copy && w.width >= kDepth && w.stride >= w.width && w.stride < (int64_t(1) << 30) &&
+           w.rows >= kDepth && w.rows < (int64_t(1) << 30) &&
+           (experts == 1 || w.outer == w.inner * w.stride) && rows <= kOddTokens * experts;
+}
+
+cudaError_t encode_odd(GroupedOddParams& p, const Operand& w, bool along_k) {
+    p.weight_rows = int(w.inner);
+    p.start = unsigned(reinterpret_cast<uintptr_t>(w.p) & 15);
+    p.step = unsigned(w.stride * 2 & 15);
+    for (int j = 0; j < 8; ++j) {
+        const char* row = static_cast<const char*>(w.p) + j * w.stride * 2;
+        const int64_t front = reinterpret_cast<uintptr_t>(row) & 15;
+        const int64_t dims[2] = {w.width + front / 2, ceil_div(w.rows - j, 8)}, strides[1] = {w.stride * 16};
+        const int box[2] = {(along_k ? kDepth : kHalf) + 8, along_k ? 16 : 8};
+        const cudaError_t e = encode_tensor_map(&p.odd[j], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, row - front, 2,
+                                                dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// The operands of the product (x) or of the input gradient (dy).  The result is whether the
+// weights, unaligned, are read as they lie.
+bool operands(bool input_grad, const void* x, int64_t x_stride, int64_t rows, int64_t experts,
               const void* weight, int64_t weight_stride, int64_t expert_stride,
               int64_t out_features, int64_t in_features, Operand* a, Operand* b) {
     *a = operand(weight, weight_stride, expert_stride, 2, experts, out_features, in_features);
     *b = operand(x, x_stride, 0, 2, 1, rows, input_grad ? out_features : in_features);
+    const bool odd = read_odd(*a, rows);
+    if (odd) a->copy = false;
+    return odd;
 }
 
 dpr_status product_workspace(bool input_grad, const void* x, int64_t x_stride, int64_t rows,
@@ -1041,9 +1185,9 @@ dpr_status product(bool input_grad, const void* x, int64_t x_stride, int64_t row
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     Operand a, b;
-    operands(input_grad, x, x_stride, rows, experts, weight, weight_stride, expert_stride,
-             out_features, in_features, &a, &b);
-    GroupedParams p = {};
+    const bool odd = operands(input_grad, x, x_stride, rows, experts, weight, weight_stride, expert_stride,
+                              out_features, in_features, &a, &b);
+    GroupedOddParams p = {};
     p.offsets = offsets; p.experts = int(experts); p.rows = int(rows);
     p.m_size = int(to); p.m_tiles = int(ceil_div(to, kTile));
     p.k_size = int(from);
@@ -1052,12 +1196,16 @@ dpr_status product(bool input_grad, const void* x, int64_t x_stride, int64_t row
     copies.add(a, ws, true);
     copies.add(b, ws, false);
     cudaError_t e = copies.launch(offsets, rows, s);
-    if (e == cudaSuccess) e = encode_experts(&p.a, a, 64, input_grad ? kDepth : kHalf);
+    if (e == cudaSuccess)
+        e = odd ? encode_odd(p, a, !input_grad) : encode_experts(&p.a, a, 64, input_grad ? kDepth : kHalf);
     if (e == cudaSuccess) e = encode(&p.b, b, kDepth, kHalf);
     if (e == cudaSuccess) e = encode(&p.b_piece, b, kDepth, kPiece);
     if (e != cudaSuccess) return record_cuda_status(e);
     const Plan q = product_plan(rows, experts, to, from);
-    e = input_grad ? launch_pairs<kInputGrad>(p, q, ws, s) : launch_pairs<kForward>(p, q, ws, s);
+    if (odd)
+        e = input_grad ? launch_pairs<kInputGradOdd>(p, q, ws, s) : launch_pairs<kForwardOdd>(p, q, ws, s);
+    else
+        e = input_grad ? launch_pairs<kInputGrad>(p, q, ws, s) : launch_pairs<kForward>(p, q, ws, s);
     return record_cuda_status(e);
 }
 

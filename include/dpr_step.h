@@ -83,7 +83,7 @@ dpr_status dpr_rmsnorm_backward(const void* dy, int64_t dy_stride, const void* d
  * aligned and may be reused by the next call on the same stream; its size
  * depends on the sizes (long sums of few tiles are split over the GPU, their
  * parts joined in order) and, because inputs whose rows are not 16-byte aligned
- * are first copied into it, on the strides and on the addresses modulo 16.
+ * may first be copied into it, on the strides and on the addresses modulo 16.
  */
 #define DPR_MAX_EXPERTS 1024
 

@@ -203,3 +203,14 @@ def test_refusals():
                         ([g[:50], g[50:100]], [g[50:100], out[:50]])):
         with pytest.raises((dpr.DprError, ValueError)):
             dpr.dpr_grad_plan_create(grads, outs)
+
+
+def test_norm_on_another_device_than_the_plan():
+    H.device()
+    plan = dpr.dpr_grad_plan_create([torch.ones(8, device="cuda")])
+    norm = torch.empty(1, device="cuda")
+    plan.device += 1                 # as of a plan made there
+    for call in (lambda: dpr.dpr_grad_norm(plan, norm), lambda: dpr.dpr_grad_clip(plan, norm, 1.0),
+                 lambda: dpr.dpr_grad_norm_clip(plan, norm, 1.0)):
+        with pytest.raises(ValueError, match="cuda"):
+            call()

@@ -144,6 +144,37 @@ def test_strides_and_addresses(pad, shift):
     apart.check_guards("weights")
 
 
+# widths whose rows start anywhere: rows of all experts follow one another, experts' first rows lie
+# anywhere too; one tile and several, sums in parts, fewer rows or channels than a step
+ODD = [((3, 0, 20), 136, 67, 0), ((40,), 96, 6001, 1), ((5, 0, 300), 257, 129, 3), ((1,), 64, 65, 0),
+       ((0, 0, 7, 2), 67, 515, 5), ((70, 1), 300, 1003, 2), ((2,), 4097, 701, 7), ((33,) * 9, 75, 65, 1),
+       ((600, 0, 900), 200, 331, 4), ((9, 4), 40, 71, 1), ((9,), 63, 71, 1), ((9, 4), 70, 61, 1),
+       ((130, 5, 64), 192, 256, 1), ((17, 3), 128, 65, 6), ((5000,), 72, 131, 1)]
+
+
+@pytest.mark.parametrize("input_grad", [False, True], ids=["product", "input_grad"])
+@pytest.mark.parametrize("counts,o,i,shift", ODD)
+def test_weights_at_any_address(counts, o, i, shift, input_grad):
+    """Without padding, between NaN, next to experts whose weights are NaN."""
+    H.device()
+    offs, experts = offsets_of(counts), len(counts)
+    have, give = (o, i) if input_grad else (i, o)
+    x, w = randn(offs[-1], have, seed=1), randn(experts, o, i, seed=2)
+    for e, c in enumerate(counts):
+        if c == 0:
+            w[e] = NAN
+    memory = torch.full((experts * o * i + 64,), NAN, dtype=BF, device="cuda")
+    pw = memory[16 + shift:16 + shift + w.numel()].view(experts, o, i)
+    pw.copy_(w)
+    for dtype in (BF, F32):
+        out = Placed(offs[-1], give, dtype, 3)
+        f = dpr.dpr_grouped_linear_input_grad if input_grad else dpr.dpr_grouped_linear
+        f(x.cuda(), device_offsets(offs), pw, out.view)
+        want, size = S.product(x, offs, w, input_grad)
+        R.check(out.view, want, S.sum_bound(want, size, have, dtype, 76), "out")
+        out.check_guards("out")
+
+
 def test_one_row_for_all_tokens():
     H.device()
     w, x = randn(2, 72, 64, seed=1), randn(1, 64, seed=2)

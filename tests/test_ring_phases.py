@@ -19,20 +19,20 @@ def passed(phase, parity):
     return phase & 1 != parity
 
 
-def run(steps, guarded, rng):
+def run(steps, guarded, rng, stages=STAGES):
     """One interleaving of the producer, its loads, both groups and the matrix instructions; the
     number of steps restored before their load had landed."""
-    full, free = [0] * STAGES, [0] * STAGES      # phases completed
+    full, free = [0] * stages, [0] * stages      # phases completed
     restored = [False] * steps
     flying, issued, consumed, early = [], 0, 0, 0
     at = list(range(GROUPS))                     # each group's next step
     while consumed < steps:
         moves = []
-        if issued < steps and passed(free[issued % STAGES], (issued // STAGES & 1) ^ 1):
+        if issued < steps and passed(free[issued % stages], (issued // stages & 1) ^ 1):
             moves.append("issue")
         moves += [("land", k) for k in flying]
         for g in range(GROUPS):
-            st, r = at[g] % STAGES, at[g] // STAGES
+            st, r = at[g] % stages, at[g] // stages
             if at[g] < steps and passed(full[st], r & 1):
                 if not guarded or r == 0 or passed(free[st], (r & 1) ^ 1):
                     moves.append(("restore", g))
@@ -44,14 +44,14 @@ def run(steps, guarded, rng):
             flying.append(issued)
             issued += 1
         elif m == "consume":
-            free[consumed % STAGES] += 1
+            free[consumed % stages] += 1
             consumed += 1
         elif m[0] == "land":
             flying.remove(m[1])
-            full[m[1] % STAGES] += 1
+            full[m[1] % stages] += 1
         else:
             k = at[m[1]]
-            if full[k % STAGES] != k // STAGES + 1:
+            if full[k % stages] != k // stages + 1:
                 early += 1
                 if not guarded:
                     return early                 # from here on anything may happen
@@ -68,6 +68,11 @@ def test_with_the_guard_no_step_is_restored_early():
 def test_without_it_some_are():
     rng = random.Random(1)
     assert any(run(60, False, rng) for _ in range(2000))
+
+
+def test_of_an_even_number_of_stages_each_group_has_its_own():
+    rng = random.Random(1)
+    assert all(run(60, False, rng, stages=4) == 0 for _ in range(2000))
 
 
 @pytest.mark.parametrize("name", ["grouped.cu", "weight_grad.cu"])

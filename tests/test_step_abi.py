@@ -157,7 +157,12 @@ def test_product_refusals(L, name):
     assert size(X, 128, 64, 4, W, 128, 128 * 128, 128, 128, None) == INVALID
     assert size(X + 2, 128, 64, 4, W, 128, 128 * 128, 128, 128, ctypes.byref(n)) == OK
     assert n.value == 64 * 128 * 2
-    assert size(X, 128, 64, 4, W, 129, 128 * 129, 128, 128, ctypes.byref(n)) == OK
+    assert size(X, 128, 64, 4, W, 129, 129 * 129, 128, 128, ctypes.byref(n)) == OK
+    assert n.value == 4 * 128 * 128 * 2
+    # but not weights that few tokens read, whose rows follow one another through all experts
+    assert size(X, 128, 64, 4, W, 129, 128 * 129, 128, 128, ctypes.byref(n)) == OK and n.value == 0
+    assert size(X, 128, 64, 4, W + 2, 128, 128 * 128, 128, 128, ctypes.byref(n)) == OK and n.value == 0
+    assert size(X, 128, 1 << 16, 4, W, 129, 128 * 129, 128, 128, ctypes.byref(n)) == OK
     assert n.value == 4 * 128 * 128 * 2
     assert call(xs=129, work=None) == INVALID and call(xs=129, n=16) == INVALID
     assert call(xs=129, work=WS + 4) == ALIGN and call(xs=129, work=X) == ALIAS
