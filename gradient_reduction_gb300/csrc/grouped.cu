@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(kThreads) copy_rows(const __grid_constant__ Co
         const int shift = int(reinterpret_cast<uintptr_t>(from) & 15);
         const char* base = from - shift;
         const int span = shift + c.bytes;        // bytes from the first aligned 16 on
-        const int words = shift >> 2, bits = (shift & 3) * 8;
+        const uint32_t words = uint32_t(shift) >> 2, bits = uint32_t(shift & 3) * 8;
         for (int v0 = 0; v0 * 16 < c.bytes; v0 += 32 * kCopyAhead) {
             uint4 own[kCopyAhead], after[kCopyAhead];
 #pragma unroll
@@ -907,14 +907,8 @@ __global__ void __launch_bounds__(kThreads) copy_rows(const __grid_constant__ Co
                 if (lane == 31) {
                     w[4] = after[j].x; w[5] = after[j].y; w[6] = after[j].z; w[7] = after[j].w;
                 }
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t lo = words == 0 ? w[k] : words == 1 ? w[k + 1] : words == 2 ? w[k + 2] : w[k + 3];
-                    const uint32_t hi = words == 0 ? w[k + 1] : words == 1 ? w[k + 2] : words == 2 ? w[k + 3] : w[k + 4];
-                    o[k] = __funnelshift_r(lo, hi, bits);
-                }
-                if (v * 16 < c.bytes) st_v4(to + int64_t(v) * 16, make_uint4(o[0], o[1], o[2], o[3]));
+                shift_words(w, words, bits);
+                if (v * 16 < c.bytes) st_v4(to + int64_t(v) * 16, make_uint4(w[0], w[1], w[2], w[3]));
             }
         }
     }

@@ -108,17 +108,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
 // TMA load of one box of a two-dimensional tensor: x (innermost, x times the
 // element size a multiple of 16 bytes) and y; parts outside the tensor read
 // as zeros and still count towards the barrier's bytes.
-// 16 bytes to shared memory, the first `bytes` of them (0 at least) from `src`, zeros behind.
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(max(bytes, 0))
-                 : "memory");
-}
-// Arrives at `bar` (one of its count) when the thread's copies so far have landed.
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
                                          uint32_t bar) {
     asm volatile(
