@@ -6,7 +6,9 @@ flat-bucket gather of fragmented gradients, the ring-order reduce-scatter
 with averaging and the fp32 partition cast, the all-gather and the fused
 all-reduce, and the operators of the backward pass that make those gradients
 (include/dpr_ops.h): layer norm, 8-bit activation checkpoints and the weight
-gradient read from them.  This package is the thin Python binding of those
+gradient read from them, and those around them in a training step with experts
+(include/dpr_step.h): RMS norm, products grouped by expert, and the norm and
+clipping of gradients.  This package is the thin Python binding of those
 calls.
 """
 from ._binding import (  # noqa: F401

@@ -26,11 +26,12 @@
 // four warps take turns, so that one group's latencies hide behind the other.
 //
 // Per step of 64 tokens a CTA reads 25 KB into its ring of five stages and
-// takes 0.36 us, 0.354 us being the rate of the measured bf16 matrix peak under
-// the power limit.  8192 tokens, 4096 x 4096, fp32: 171 us with the join (1.60
-// PFLOP/s, 0.85 of the measured burst peak, 0.95 of the sustained one); 4096
-// tokens, 11008 x 4096, bf16: 225 us (1.64 PFLOP/s).  What is left is filling
-// and draining (some 8 us), the join and the last, dealt-out tiles.
+// takes 0.38 us, 0.354 us being the rate of the measured bf16 matrix peak under
+// the power limit (0.36 without the restoring warps' wait for the stage's last
+// use, which no run may do without).  8192 tokens, 4096 x 4096, fp32: 180 us with
+// the join (1.53 PFLOP/s, 0.80 of the measured burst peak, 0.90 of the sustained
+// one); 4096 tokens, 11008 x 4096, bf16: 241 us (1.53 PFLOP/s).  What is left is
+// filling and draining (some 8 us), the join and the last, dealt-out tiles.
 //
 // What made it fast, 8192 tokens, 4096 x 4096, fp32: releasing arrivals at CTA
 // scope 341 -> 230 us, one ring with one commit a step 230 -> 220, electing the
