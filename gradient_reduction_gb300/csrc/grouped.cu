@@ -708,8 +708,10 @@ grouped_pairs(const __grid_constant__ KindParams<kKind> p) {
                 // The stage's use before this one was the other group's (their number is odd), and
                 // loads may land out of order.  Until that use is over, `full` may still be in its
                 // phase, and then this wait would take the one before it, long complete, for its own.
-                const bool landed = (round == 0 || tc::mbar_wait(free_(st), (round & 1) ^ 1)) &&
-                                    tc::mbar_wait(full(st), round & 1);
+                bool landed = round > 0 && tc::mbar_passed(free_(st), (round & 1) ^ 1, full(st), round & 1);
+                if (!__all_sync(0xFFFFFFFFu, landed))
+                    landed = (round == 0 || tc::mbar_wait(free_(st), (round & 1) ^ 1)) &&
+                             tc::mbar_wait(full(st), round & 1);
                 if (!(ok = __all_sync(0xFFFFFFFFu, landed))) break;
                 const int valid = s.k_count - (s.first + k) * kDepth;
                 uint32_t w[4][4], step[4];

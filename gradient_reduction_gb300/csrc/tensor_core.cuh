@@ -105,6 +105,22 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
 }
 
+// Have both phases passed, `first` before `then` was looked at?  Without a wait, and
+// in the time of one look.
+__device__ __forceinline__ bool mbar_passed(uint32_t first, uint32_t first_parity, uint32_t then,
+                                            uint32_t then_parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "and.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(first), "r"(first_parity), "r"(then), "r"(then_parity)
+        : "memory");
+    return done != 0;
+}
+
 // TMA load of one box of a two-dimensional tensor: x (innermost, x times the
 // element size a multiple of 16 bytes) and y; parts outside the tensor read
 // as zeros and still count towards the barrier's bytes.

@@ -30,8 +30,9 @@
 // the power limit (0.36 without the restoring warps' wait for the stage's last
 // use, which no run may do without).  8192 tokens, 4096 x 4096, fp32: 180 us with
 // the join (1.53 PFLOP/s, 0.80 of the measured burst peak, 0.90 of the sustained
-// one); 4096 tokens, 11008 x 4096, bf16: 241 us (1.53 PFLOP/s).  What is left is
-// filling and draining (some 8 us), the join and the last, dealt-out tiles.
+// one); 4096 tokens, 11008 x 4096, bf16: 229 us (1.61 PFLOP/s; 240 with two waits
+// in turn instead of one look at both barriers first).  What is left is filling
+// and draining (some 8 us), the join and the last, dealt-out tiles.
 //
 // What made it fast, 8192 tokens, 4096 x 4096, fp32: releasing arrivals at CTA
 // scope 341 -> 230 us, one ring with one commit a step 230 -> 220, electing the
@@ -374,8 +375,10 @@ weight_grad_pairs(const __grid_constant__ WeightGradParams p) {
                 // The stage's use before this one was the other group's (their number is odd), and
                 // loads may land out of order.  Until that use is over, `full` may still be in its
                 // phase, and then this wait would take the one before it, long complete, for its own.
-                const bool landed = (round == 0 || tc::mbar_wait(free_(st), (round & 1) ^ 1)) &&
-                                    tc::mbar_wait(full(st), round & 1);
+                bool landed = round > 0 && tc::mbar_passed(free_(st), (round & 1) ^ 1, full(st), round & 1);
+                if (!__all_sync(0xFFFFFFFFu, landed))
+                    landed = (round == 0 || tc::mbar_wait(free_(st), (round & 1) ^ 1)) &&
+                             tc::mbar_wait(full(st), round & 1);
                 if (!(ok = __all_sync(0xFFFFFFFFu, landed))) break;
                 uint32_t w[4][4], step[4];
 #pragma unroll
