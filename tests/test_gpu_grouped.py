@@ -175,6 +175,25 @@ def test_weights_at_any_address(counts, o, i, shift, input_grad):
         out.check_guards("out")
 
 
+# more tiles than pairs of SMs, and a last round that is not full
+@pytest.mark.parametrize("counts,o,i", [((300, 0, 1, 520, 256), 6300, 2200), ((700, 90), 5000, 4200),
+                                        ((513, 2, 0), 9000, 2240), ((400, 300), 5003, 4201)])
+@pytest.mark.parametrize("input_grad", [False, True], ids=["product", "input_grad"])
+def test_several_rounds_of_tiles(counts, o, i, input_grad):
+    H.device()
+    offs, experts = offsets_of(counts), len(counts)
+    have, give = (o, i) if input_grad else (i, o)
+    x, w = randn(offs[-1], have, seed=1), randn(experts, o, i, seed=2)
+    f = dpr.dpr_grouped_linear_input_grad if input_grad else dpr.dpr_grouped_linear
+    want, size = S.product(x, offs, w, input_grad)
+    xs, ws = x.cuda(), w.cuda()
+    for dtype in (BF, F32):
+        out = Placed(offs[-1], give, dtype, 3)
+        f(xs, device_offsets(offs), ws, out.view)
+        R.check(out.view, want, S.sum_bound(want, size, have, dtype, 76), "out")
+        out.check_guards("out")
+
+
 def test_one_row_for_all_tokens():
     H.device()
     w, x = randn(2, 72, 64, seed=1), randn(1, 64, seed=2)
