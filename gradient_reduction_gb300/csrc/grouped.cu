@@ -1007,29 +1007,35 @@ cudaError_t encode_experts(CUtensorMap* map, const Operand& o, int box_x, int bo
                              CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// How the work is dealt out, from what the host knows: `tiles` at most, of
-// `steps` steps and `each` columns on average, `columns` at most.
+// How the work is dealt out, from what the host knows: `most` tiles at most,
+// `tiles` of experts that have about as many tokens, of `steps` steps and `each`
+// columns on average, `columns` at most.
 struct Plan {
     bool split = false;
     int64_t pairs = 0, slot_columns = 0, partial_bytes = 0, part_bytes = 0;
     int64_t bytes() const { return partial_bytes + part_bytes; }
 };
 
-// Steps are dealt out, and parts of tiles joined by a second kernel, where
-// whole tiles would leave pairs idle for more steps than that second kernel and its
-// launch take (kSplitGain, some 5 us).  Tiles of few columns wait for
-// memory, not for the tensor core: fewer pairs at once then go on faster (0.25 us a step
-// against 0.36 with all of them).  16384 tokens, 200 x 512, weight gradient: 77.6 us
-// whole, 19.8 split; 32 tokens over 8 experts of 11008 x 4096, input gradient (128
-// tiles of few columns): 107 whole, 113 split.
-constexpr double kSplitGain = 16;
-Plan plan_work(int64_t tiles, double steps, int64_t columns, double each) {
+// Steps are dealt out, and parts of tiles joined by a second kernel, where whole
+// tiles would take longer: pairs in different places of the sum share less in L2
+// (kSplitSlow), and the parts' stores and the second kernel take kSplitCost steps more
+// than the stores of whole tiles.  Tiles of few columns wait for memory, not for the
+// tensor core: fewer pairs at once then go on faster (0.25 us a step against 0.36 with
+// all of them).  Whole and dealt out: weight gradient of 16384 tokens, 200 x 512, 78 and
+// 20 us, 2048 x 2560 (80 tiles of 256 steps) 147 and 124, 2048 x 4096 (128 tiles) 152
+// and 206; product of 512 tokens, 4096 x 11008 (32 tiles of 172 steps), 52 and 45, of
+// 1024 tokens, 4096 x 4096 (64 tiles of 64 steps), 24 and 35; of 32 tokens over 8 experts
+// of 11008 x 4096, input gradient (128 tiles of few columns), 107 and 113.  More tiles:
+// whole (4096 tokens, 8 experts of 4096 x 4096, 3.4 rounds, 86 and 129).
+constexpr double kSplitSlow = 1.15, kSplitCost = 32;
+Plan plan_work(int64_t most, int64_t tiles, double steps, int64_t columns, double each) {
     Plan q;
-    q.pairs = std::min<int64_t>(tiles, kPairs);
-    const double rounds = double(ceil_div(tiles, kPairs)) * (each <= 64 ? 0.7 : 1.0);
-    if (tiles < 2 * kPairs && (rounds - double(tiles) / kPairs) * steps > kSplitGain) {
+    q.pairs = std::min<int64_t>(most, kPairs);
+    const double whole = double(ceil_div(tiles, kPairs)) * steps * (each <= 64 ? 0.7 : 1.0);
+    const double dealt = std::max(double(tiles) * steps / kPairs, double(kMinPart));
+    if (tiles < 2 * kPairs && whole > kSplitSlow * dealt + kSplitCost) {
         q.split = true;
-        q.pairs = std::min<int64_t>(kPairs, std::max(tiles, int64_t(double(tiles) * steps / kMinPart)));
+        q.pairs = std::min<int64_t>(kPairs, std::max(most, int64_t(double(most) * steps / kMinPart)));
         q.slot_columns = std::min<int64_t>(kTile, round_up(columns, 32));
         q.partial_bytes = 2 * q.pairs * q.slot_columns * kTile * 4;
         q.part_bytes = 2 * q.pairs * int64_t(sizeof(GroupedPart));
@@ -1039,13 +1045,15 @@ Plan plan_work(int64_t tiles, double steps, int64_t columns, double each) {
 
 Plan product_plan(int64_t rows, int64_t experts, int64_t to, int64_t from) {
     // at most: every expert's last tile may be short
-    const int64_t n = rows / kTile + std::min(rows, experts);
-    return plan_work(ceil_div(to, kTile) * n, double(ceil_div(from, kDepth)), rows, double(rows) / double(n));
+    const int64_t short_ones = std::min(rows, experts), m = ceil_div(to, kTile);
+    const int64_t n = rows / kTile + short_ones;
+    return plan_work(m * n, m * std::max(ceil_div(rows, kTile), short_ones), double(ceil_div(from, kDepth)),
+                     rows, double(rows) / double(n));
 }
 
 Plan grad_plan(int64_t rows, int64_t experts, int64_t out_features, int64_t in_features) {
-    return plan_work(experts * ceil_div(in_features, kTile) * ceil_div(out_features, kTile),
-                     double(rows) / double(experts * kDepth), out_features, kTile);
+    const int64_t tiles = experts * ceil_div(in_features, kTile) * ceil_div(out_features, kTile);
+    return plan_work(tiles, tiles, double(rows) / double(experts * kDepth), out_features, kTile);
 }
 
 template <int kKind, bool kSplit>
