@@ -1,6 +1,8 @@
 // RMS norm, backward: dx needs one sum along every row, dweight one down every
 // column.  With n = h rstd and g = dy weight,
-//   dx = dh + rstd g - h rstd^3 avg(g h),   dweight = sum_rows dy n.
+//   dx = dh + rstd (g - n avg(g n)),   dweight = sum_rows dy n.
+// n, of about 1 in any row, comes first: rstd^3 avg(g h) takes as many operations,
+// but its rstd^2 leaves fp32 for rows (and gradients) whose dx is well inside it.
 //
 // Rows of up to 8192 channels take one pass: the threads of a block own columns
 // and keep their sums in registers over all of the block's rows; a second,
@@ -29,7 +31,7 @@ struct RmsGradParams {
     const float* rstd;
     void* dx;
     int64_t dx_stride;
-    float* row_avg;           // [rows]: rstd^3 avg(g h) (two passes)
+    float* row_avg;           // [rows]: avg(g n) (two passes)
     float* partial;           // [slices][partial_width]: dweight of a slice of the rows, or NULL
     int64_t rows;
     int width;
@@ -64,11 +66,6 @@ __device__ __forceinline__ void load_weight(const RmsGradParams& p, int c, float
 #pragma unroll
         for (int k = 0; k < V; ++k) w[k] = 1.0f;
     }
-}
-
-// rstd^3 avg(g h) from the row's sum of rstd g h.
-__device__ __forceinline__ float along(const RmsGradParams& p, float sum, float rstd) {
-    return __fmul_rn(__fmul_rn(divide(sum, p.count, p.inv_width), rstd), rstd);
 }
 
 // V elements of the row's h: the stored one or its checkpoint.
@@ -214,7 +211,7 @@ __global__ void __launch_bounds__(512) rms_grad_rows(const __grid_constant__ Rms
          first += stride, row += stride, turn ^= 1) {
         F2 g[E / 2], x[E / 2];
         F2 sum = f2(0.0f);
-        const float r = rstd;
+        const F2 r = f2(rstd);
         const bool live = row < p.rows;
         {
             float d[E], f[E];
@@ -228,15 +225,14 @@ __global__ void __launch_bounds__(512) rms_grad_rows(const __grid_constant__ Rms
 #pragma unroll
                 for (int k = 0; k < V; ++k) f[i * V + k] = v[k];
             }
-            const F2 r2 = f2(r);
 #pragma unroll
             for (int k = 0; k < E / 2; ++k) {
-                // a channel past the row's end has d = 0
-                const F2 dr = mul2(f2(d[2 * k], d[2 * k + 1]), r2);
-                x[k] = f2(f[2 * k], f[2 * k + 1]);
-                g[k] = mul2(dr, w[k]);
+                // a channel past the row's end has d = 0 and x = 0
+                const F2 dy2 = f2(d[2 * k], d[2 * k + 1]);
+                x[k] = mul2(f2(f[2 * k], f[2 * k + 1]), r);
+                g[k] = mul2(dy2, w[k]);
                 sum = fma2(g[k], x[k], sum);
-                dw[k] = fma2(dr, x[k], dw[k]);
+                dw[k] = fma2(dy2, x[k], dw[k]);
             }
         }
         if (p.dh) {
@@ -251,8 +247,9 @@ __global__ void __launch_bounds__(512) rms_grad_rows(const __grid_constant__ Rms
         load(row + stride);
         const float a = row_sum(total(sum), s[turn]);
         if (live) {
-            const F2 minus = f2(-along(p, a, r));
-            float d[E];
+            const F2 minus = f2(-divide(a, p.count, p.inv_width));
+            float d[E], r1, same;
+            halves(r, r1, same);
 #pragma unroll
             for (int k = 0; k < E / 2; ++k)
                 halves(fma2(x[k], minus, g[k]), d[2 * k], d[2 * k + 1]);
@@ -265,10 +262,10 @@ __global__ void __launch_bounds__(512) rms_grad_rows(const __grid_constant__ Rms
                     if (p.dh) {
                         unpack(dh[i], v);
 #pragma unroll
-                        for (int k = 0; k < V; ++k) v[k] = __fadd_rn(v[k], d[i * V + k]);
+                        for (int k = 0; k < V; ++k) v[k] = __fmaf_rn(d[i * V + k], r1, v[k]);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < V; ++k) v[k] = d[i * V + k];
+                        for (int k = 0; k < V; ++k) v[k] = __fmul_rn(d[i * V + k], r1);
                     }
                     Raw<T, V> out;
                     pack(v, out);
@@ -306,8 +303,8 @@ __device__ __forceinline__ float group_sum_all(float v, float (*s)[16]) {
 // memory, p.depth of them in all.  A thread owns 16-byte pieces of the row, piece i
 // at i * blockDim.x + threadIdx.x; with 32 channels a thread there is no room for
 // their weights in its registers, and it loads them for every row.
-// 16384 x 4096 bf16 with dh and the join: 84 us, 6.4 TB/s (0.95 of the measured
-// copy rate); from a checkpoint 84 us, 5.6 TB/s; without dh 72 and 78 us.  A row's
+// 16384 x 4096 bf16 with dh and the join: 82 us, 6.5 TB/s (0.97 of the measured
+// copy rate); from a checkpoint 80 us, 5.9 TB/s; without dh 67 and 73 us.  A row's
 // chain of loads, sum, barrier and second half bounds the last three, with 16 warps an
 // SM.  What was tried: dy and h unpacked again after the sum 91 and 96 us (22 and 31
 // instructions an element); two rows a turn with their values in registers, the
@@ -333,8 +330,8 @@ __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ R
     const uint32_t h_bytes = kSaved ? uint32_t(p.width) : dy_bytes;
     const uint32_t stage = dy_bytes + h_bytes + (p.dh ? dy_bytes : 0);
     const uint32_t mine = tc::smem_addr(ring) + threadIdx.y * p.depth * stage;
-    const int64_t stride = int64_t(gridDim.x) * blockDim.y;
-    const int64_t row0 = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int rows = int(p.rows), stride = int(gridDim.x * blockDim.y);   // rows are counted in 30 bits
+    const int row0 = int(blockIdx.x * blockDim.y + threadIdx.y);
     const auto fetch = [&](int64_t r, uint32_t k) {
         const void* h = kSaved ? static_cast<const void*>(p.ckpt.codes + r * p.ckpt.code_stride)
                                : static_cast<const T*>(p.h) + r * p.h_stride;
@@ -352,8 +349,8 @@ __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ R
     };
     uint32_t asked = 0;                 // rows fetched so far, by the first thread
     if (tx == 0)
-        for (; asked < uint32_t(p.depth) && row0 + asked * stride < p.rows; ++asked)
-            fetch(row0 + asked * stride, asked);
+        for (; asked < uint32_t(p.depth) && row0 + int(asked) * stride < rows; ++asked)
+            fetch(row0 + int(asked) * stride, asked);
 
     constexpr bool kKeep = E <= 16;
     F2 w[kKeep ? E / 2 : 1], dw[E / 2];
@@ -376,7 +373,7 @@ __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ R
     };
     Small now, next;
     const auto load_small = [&](int64_t r, Small& m) {
-        if (r >= p.rows) return;
+        if (r >= rows) return;
         m.rstd = p.rstd[r];
         if constexpr (kSaved) {
 #pragma unroll
@@ -393,54 +390,49 @@ __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ R
     uint32_t k = 0, parity = 0, last = 0;    // `last`: the stage of the turn before
     int turn = 0;
     bool ok = true;
-    for (int64_t row = row0; row < p.rows; row += stride, dx += dx_row, turn ^= 1) {
-        F2 g[E / 2], h[E / 2];               // rstd dy weight, and h
+    for (int row = row0; row < rows; row += stride, dx += dx_row, turn ^= 1) {
+        F2 g[E / 2], n[E / 2];
         F2 sum = f2(0.0f);
         const F2 r2 = f2(now.rstd);
         const uint32_t at = mine + k * stage, first = k;
-        // The condition always holds.  As a branch it makes the compiler finish this half before
-        // the sum's exchanges: 84 us instead of 92 (without dh 72 instead of 85).
-        if (row < p.rows) {
-            if (ok) ok = tc::mbar_wait(full + 8 * k, parity);
-            if (++k == uint32_t(p.depth)) { k = 0; parity ^= 1; }
+        if (ok) ok = tc::mbar_wait(full + 8 * k, parity);
+        if (++k == uint32_t(p.depth)) { k = 0; parity ^= 1; }
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const uint32_t piece = uint32_t(i * threads + tx);
-                if (int(piece) * V >= p.width) continue;
-                Raw<T, V> raw;
-                F2 d[V / 2], x[V / 2], mine_w[V / 2];
-                if constexpr (kSaved) {
-                    CodeRaw<V> c;
-                    load_shared(at + dy_bytes + piece * V, c.w);
-                    decode2<V>(c, now.step[i], x);
-                } else {
-                    load_shared(at + dy_bytes + piece * 16, raw.w);
-                    unpack2(raw, x);
-                }
-                load_shared(at + piece * 16, raw.w);
-                unpack2(raw, d);
-                if constexpr (!kKeep) weights(i, mine_w);
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t piece = uint32_t(i * threads + tx);
+            if (int(piece) * V >= p.width) continue;
+            Raw<T, V> raw;
+            F2 d[V / 2], x[V / 2], mine_w[V / 2];
+            if constexpr (kSaved) {
+                CodeRaw<V> c;
+                load_shared(at + dy_bytes + piece * V, c.w);
+                decode2<V>(c, now.step[i], x);
+            } else {
+                load_shared(at + dy_bytes + piece * 16, raw.w);
+                unpack2(raw, x);
+            }
+            load_shared(at + piece * 16, raw.w);
+            unpack2(raw, d);
+            if constexpr (!kKeep) weights(i, mine_w);
 #pragma unroll
-                for (int e = 0; e < V / 2; ++e) {
-                    const int q = i * V / 2 + e;
-                    const F2 dr = mul2(d[e], r2);
-                    g[q] = mul2(dr, kKeep ? w[kKeep ? q : 0] : mine_w[e]);
-                    h[q] = x[e];
-                    sum = fma2(g[q], x[e], sum);
-                    dw[q] = fma2(dr, x[e], dw[q]);
-                }
+            for (int e = 0; e < V / 2; ++e) {
+                const int q = i * V / 2 + e;
+                n[q] = mul2(x[e], r2);
+                g[q] = mul2(d[e], kKeep ? w[kKeep ? q : 0] : mine_w[e]);
+                sum = fma2(g[q], n[q], sum);
+                dw[q] = fma2(d[e], n[q], dw[q]);
             }
         }
         load_small(row + stride, next);
         const float total_sum = group_sum_all(total(sum), s[turn]);
         // the whole group is past the turn before: its stage is free (after a failed
         // wait it is not known to be)
-        if (tx == 0 && ok && row != row0 && row0 + asked * stride < p.rows) {
-            fetch(row0 + asked * stride, last);
+        if (tx == 0 && ok && row != row0 && row0 + int(asked) * stride < rows) {
+            fetch(row0 + int(asked) * stride, last);
             ++asked;
         }
         last = first;
-        const F2 minus = f2(-along(p, total_sum, now.rstd));
+        const F2 minus = f2(-divide(total_sum, p.count, p.inv_width));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const uint32_t piece = uint32_t(i * threads + tx);
@@ -451,13 +443,13 @@ __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ R
                 load_shared(at + dy_bytes + h_bytes + piece * 16, raw.w);
                 unpack2(raw, o);
 #pragma unroll
-                for (int e = 0; e < V / 2; ++e) o[e] = fma2(h[i * V / 2 + e], minus, o[e]);
+                for (int e = 0; e < V / 2; ++e)
+                    o[e] = fma2(fma2(n[i * V / 2 + e], minus, g[i * V / 2 + e]), r2, o[e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < V / 2; ++e) o[e] = mul2(h[i * V / 2 + e], minus);
+                for (int e = 0; e < V / 2; ++e)
+                    o[e] = mul2(fma2(n[i * V / 2 + e], minus, g[i * V / 2 + e]), r2);
             }
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) o[e] = add2(g[i * V / 2 + e], o[e]);
             pack2(o, raw);
             st_v4(dx + i * threads * V, make_uint4(raw.w[0], raw.w[1], raw.w[2], raw.w[3]));
         }
@@ -479,7 +471,7 @@ __global__ void __launch_bounds__(512) rms_grad_staged(const __grid_constant__ R
     store_columns<V, NV>(p, dw, reinterpret_cast<float*>(ring));
 }
 
-// Two passes: rstd^3 avg(g h) of every row, blockDim.x threads per row.
+// Two passes: avg(g n) of every row, blockDim.x threads per row.
 template <typename T, int V, bool kSaved>
 __global__ void __launch_bounds__(256) rms_grad_sums(const __grid_constant__ RmsGradParams p) {
     __shared__ float s[8][32];
@@ -489,6 +481,7 @@ __global__ void __launch_bounds__(256) rms_grad_sums(const __grid_constant__ Rms
     const bool live = row < p.rows;
     float a = 0.0f;
     if (live) {
+        const float rstd = p.rstd[row];
         const T* dy = static_cast<const T*>(p.dy) + row * p.dy_stride;
         for (int c = int(threadIdx.x) * V; c < p.width; c += int(blockDim.x) * V) {
             Raw<T, V> rd;
@@ -500,11 +493,11 @@ __global__ void __launch_bounds__(256) rms_grad_sums(const __grid_constant__ Rms
             src.get(x);
             load_weight<V>(p, c, w);
 #pragma unroll
-            for (int k = 0; k < V; ++k) a = __fmaf_rn(__fmul_rn(d[k], w[k]), x[k], a);
+            for (int k = 0; k < V; ++k) a = __fmaf_rn(__fmul_rn(d[k], w[k]), __fmul_rn(x[k], rstd), a);
         }
     }
     a = row_sum(a, s);
-    if (live && threadIdx.x == 0) p.row_avg[row] = along(p, __fmul_rn(a, p.rstd[row]), p.rstd[row]);
+    if (live && threadIdx.x == 0) p.row_avg[row] = divide(a, p.count, p.inv_width);
 }
 
 // dx of a tile of 32 V columns by a slice of the rows, and the tile's column
@@ -536,9 +529,10 @@ __global__ void __launch_bounds__(256) rms_grad_columns(const __grid_constant__ 
             src.get(x);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
-                dw[k] = __fmaf_rn(d[k], __fmul_rn(x[k], rstd), dw[k]);
-                d[k] = __fmaf_rn(-x[k], avg, __fmul_rn(__fmul_rn(d[k], w[k]), rstd));
-                if (p.dh) d[k] = __fadd_rn(d[k], add[k]);
+                x[k] = __fmul_rn(x[k], rstd);
+                dw[k] = __fmaf_rn(d[k], x[k], dw[k]);
+                const float v = __fmaf_rn(-x[k], avg, __fmul_rn(d[k], w[k]));
+                d[k] = p.dh ? __fmaf_rn(v, rstd, add[k]) : __fmul_rn(v, rstd);
             }
             pack(d, rd);
             store_raw(static_cast<T*>(p.dx) + row * p.dx_stride + c, rd);

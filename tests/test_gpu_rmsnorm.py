@@ -252,3 +252,30 @@ def test_rows_past_32_bits():
     R.check(x[-3:], want, d_y, "y")
     R.check(rstd[-3:], want_rstd, d_rstd, "rstd")
     assert not x[:-3].any()
+
+
+@pytest.mark.parametrize("saved", [False, True], ids=["stored", "saved"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("width", [24, 100, 1001, 4096, 8192, 12288, 20000])
+@pytest.mark.parametrize("size,grad", [(2.0 ** 57, 2.0 ** -50), (2.0 ** 40, 2.0 ** -60), (2.0 ** 40, 2.0 ** -90),
+                                       (2.0 ** -62, 16.0)])
+def test_backward_of_large_and_small_rows(size, grad, width, dtype, saved):
+    """Rows whose rstd^2 leaves fp32 or takes small gradients out of it, while the outputs are in it.
+    (Only the last operation on dx may round a subnormal number: half of TINY.)"""
+    H.device()
+    rows = 40
+    h = (activation(rows, width, 1, F32) * size).to(dtype)
+    dy = (torch.randn(rows, width, generator=gen(2)) * grad).to(dtype)
+    w = weight_of(width, dtype)
+    rstd = S.rms_forward(h, w, 0.0)[1].float()
+    source, hh = h.cuda(), h.double()
+    if saved:
+        source = dpr.dpr_checkpoint_empty(rows, width)
+        dpr.dpr_checkpoint_save(h.cuda(), source)
+        hh = R.decode(source.codes.cpu(), source.steps.cpu())
+    dx, dw = torch.empty(rows, width, dtype=dtype, device="cuda"), torch.empty(width, device="cuda")
+    dpr.dpr_rmsnorm_backward(dy.cuda(), source, w.cuda(), rstd.cuda(), dx, dw)
+    want, want_w = S.rms_backward(dy, hh, w, rstd)
+    d_dx, d_dw = S.rms_backward_bounds(dy, hh, w, rstd, None, dtype, F32)
+    R.check(dw, want_w, d_dw, "dweight")
+    R.check(dx, want, d_dx, "dx")
