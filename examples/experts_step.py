@@ -52,10 +52,9 @@ class Block:
 
 def sort_tokens(expert: torch.Tensor, experts: int):
     """The order that sorts tokens by expert, and the experts' offsets, without leaving the device."""
-    order = torch.argsort(expert, stable=True)
-    offsets = torch.zeros(experts + 1, dtype=torch.int32, device="cuda")
-    offsets[1:] = torch.cumsum(torch.bincount(expert, minlength=experts), 0)
-    return order, offsets
+    by_expert, order = torch.sort(expert, stable=True)
+    # (torch.bincount would wait for the device: the length of its result is the largest value's)
+    return order, torch.searchsorted(by_expert, torch.arange(experts + 1, device="cuda"), out_int32=True)
 
 
 def forward(block: Block, x: torch.Tensor, residual: torch.Tensor, expert: torch.Tensor):

@@ -52,6 +52,20 @@ def test_block_with_experts(hidden, out, experts, ranks, tokens):
         assert torch.equal(parts, first[0]) and torch.equal(block.norm, first[1])
 
 
+def test_tokens_are_sorted_without_waiting_for_the_device():
+    H.device()
+    m = example()
+    expert = torch.tensor([3, 0, 3, 5, 0, 0, 2], device="cuda")
+    m.sort_tokens(expert, 7)                 # what is loaded once is loaded
+    torch.cuda.set_sync_debug_mode("error")
+    try:
+        order, offsets = m.sort_tokens(expert, 7)
+    finally:
+        torch.cuda.set_sync_debug_mode("default")
+    assert order.tolist() == [1, 4, 5, 6, 0, 2, 3]
+    assert offsets.dtype == torch.int32 and offsets.tolist() == [0, 3, 3, 4, 6, 6, 7, 7]
+
+
 class Work:
     """Buffers of all operators, and a pass through them."""
 
