@@ -469,8 +469,9 @@ using namespace dpr;
 namespace {
 
 constexpr int64_t kJoinPieces = 152;            // up to here the clipping's blocks join the sums
-// pieces are counted in 31 bits (a launch's blocks)
-constexpr int64_t kMostElements = (int64_t(1) << 30) * kUnit;
+// Of a list: more than the card's memory has room for.  (Pieces, a launch's blocks, are counted in
+// 31 bits; these make 2^25, and one for each tensor.)
+constexpr int64_t kMostElements = int64_t(1) << 38;
 
 // One tensor of a plan.
 struct Tensor {

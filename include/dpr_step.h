@@ -134,8 +134,9 @@ dpr_status dpr_grouped_linear_weight_grad(const void* dy, int64_t dy_stride, con
  * whatever the elements' magnitudes (a norm beyond fp32 is infinite).  An infinite norm clips to zero (and the
  * infinities to NaN), a NaN makes every gradient NaN: a diverged step shows.
  *
- * The list is recorded once: n tensors of numel[i] elements (0 allowed) at
- * src[i], written to dst[i], each bf16 or fp32 (src_dtype[i], dst_dtype[i]).
+ * The list is recorded once: n tensors of numel[i] elements (0 allowed, at most
+ * DPR_MAX_ELEMS, 2^38 in all) at src[i], written to dst[i], each bf16 or fp32
+ * (src_dtype[i], dst_dtype[i]).
  * dst == NULL, or dst[i] == src[i] with the same type, is in place; otherwise
  * outputs overlap neither one another nor any input.  Any element-aligned
  * addresses are accepted; where both rows of a tensor can be 32-byte aligned

@@ -163,6 +163,22 @@ def test_more_than_32_bits_of_elements():
     assert not g[:-5].any()
 
 
+def test_a_list_of_more_elements_than_one_tensor_may_have():
+    H.device()
+    gs = [torch.zeros((1 << 33) + 16, dtype=BF, device="cuda") for _ in range(2)]
+    for g in gs:
+        g[-5:] = 3.0
+    norm = torch.empty(1, device="cuda")
+    with dpr.dpr_grad_plan_create(gs) as plan:
+        dpr.dpr_grad_norm_clip(plan, norm, 1.0)
+    want = 90.0 ** 0.5
+    assert abs(norm.item() - want) <= S.NORM_ERROR * want
+    one = torch.full((5,), 3 / want, dtype=torch.float64)
+    for g in gs:
+        R.check(g[-5:], one, S.clip_bound(one, BF), "last elements")
+        assert not g[:64].any() and not g[-69:-5].any()
+
+
 def test_refusals():
     H.device()
     g, norm = torch.ones(100000, device="cuda"), torch.empty(1, device="cuda")

@@ -245,6 +245,15 @@ def test_plan_refusals(L):
     assert L.dpr_grad_norm_clip(None, 1.0, 1.0, Y, WS, 1 << 20, None) == INVALID
 
 
+def test_plan_of_a_long_list(L):
+    """Lists of more elements than one tensor may have, up to 2^38."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses would make a plan where there is a device")
+    apart = [BASE + i * 64 * GB for i in range(17)]
+    assert _plan(L, [(p, FP32, (1 << 33) + 8) for p in apart[:2]]) == CUDA
+    assert _plan(L, [(p, BF16, 1 << 34) for p in apart]) == UNSUP
+
+
 def test_binding_refuses_what_is_not_on_the_gpu():
     import gradient_reduction_gb300 as dpr
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
