@@ -96,8 +96,14 @@ def dpr_rmsnorm_backward(dy: torch.Tensor, h, weight, rstd: torch.Tensor, dx: to
         _check("dpr_rmsnorm_backward", st)
 
 
+def _needed(t, what: str):
+    if t is None:
+        raise ValueError(f"{what}: a tensor is needed")
+
+
 def _experts(t: torch.Tensor, what: str, dev: int):
     """(address, experts, rows, width, row stride, expert stride) of [experts, rows, width]."""
+    _needed(t, what)
     if t.get_device() != dev:
         _wrong_device(t, what)
     if t.dim() != 3 or t.shape[0] == 0:
@@ -118,6 +124,7 @@ def _bf16(t: torch.Tensor, what: str):
 
 def _offsets(t: torch.Tensor, experts: int, dev: int) -> int:
     """Address of the experts' offsets."""
+    _needed(t, "offsets")
     if t.dtype != torch.int32:
         raise ValueError(f"offsets: need torch.int32, got {t.dtype}")
     return _vector(t, experts + 1, "offsets", dev)
@@ -129,6 +136,8 @@ def _grouped_product(fn: str, x, what: str, offsets, weight, out, out_what: str,
     dev = _device(x, what)
     px, rows, width, sx = _matrix(x, what, dev)
     _bf16(x, what)
+    _needed(weight, "weight")
+    _needed(out, out_what)
     _bf16(weight, "weight")
     pw, experts, o, i, sw, ew = _experts(weight, "weight", dev)
     have, give = (i, o) if fn == "dpr_grouped_linear" else (o, i)
@@ -293,6 +302,7 @@ def dpr_grad_plan_destroy(plan: GradPlan) -> None:
 def _norm(plan: GradPlan, norm: torch.Tensor) -> int:
     if plan.handle is None:
         raise ValueError("the plan is closed")
+    _needed(norm, "norm")
     dev = _device(norm, "norm")
     if dev != plan.device:
         raise ValueError(f"the plan's tensors are on cuda:{plan.device}, norm is on cuda:{dev}")

@@ -305,6 +305,19 @@ def test_binding_refusals():
             dpr.dpr_grouped_linear_weight_grad(*bad)
 
 
+def test_missing_tensors():
+    H.device()
+    x, w = randn(8, 64).cuda(), randn(2, 72, 64).cuda()
+    y, at = torch.empty(8, 72, device="cuda"), device_offsets([0, 3, 8])
+    for f, a, b in ((dpr.dpr_grouped_linear, x, y), (dpr.dpr_grouped_linear_input_grad, y.to(BF), x)):
+        for bad in ((a, None, w, b), (a, at, None, b), (a, at, w, None)):
+            with pytest.raises(ValueError, match="needed"):
+                f(*bad)
+    for bad in ((y.to(BF), None, x, torch.empty(2, 72, 64, device="cuda")), (y.to(BF), at, x, None)):
+        with pytest.raises(ValueError, match="needed"):
+            dpr.dpr_grouped_linear_weight_grad(*bad)
+
+
 def test_no_wait_ran_out():
     H.device()
     assert dpr.dpr_device_wait_failures() == 0

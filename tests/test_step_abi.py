@@ -269,6 +269,18 @@ def test_binding_refuses_what_is_not_on_the_gpu():
             call()
 
 
+def test_binding_names_a_tensor_that_is_missing():
+    from gradient_reduction_gb300 import _step
+    plan = _step.GradPlan(1, 0, 0, ())
+    try:
+        for call, what in ((lambda: _step._offsets(None, 2, 0), "offsets"), (lambda: _step._experts(None, "dweight", 0), "dweight"),
+                           (lambda: _step._norm(plan, None), "norm")):
+            with pytest.raises(ValueError, match=f"{what}: a tensor is needed"):
+                call()
+    finally:
+        plan.handle = None               # made up
+
+
 def test_no_kernel_takes_a_buffer_as_unchanging():
     """Programmatic launches are resident while the grid before them still writes what they will
     read: nothing may go through the non-coherent path."""
