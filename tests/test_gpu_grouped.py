@@ -7,6 +7,7 @@ import torch
 import gradient_reduction_gb300 as dpr
 from tests import gpu_helpers as H
 from tests import operators_reference as R
+from tests import step_cases as C
 from tests import step_reference as S
 from tests.test_gpu_operators import BF, F32, Placed, checkpoint, gen
 
@@ -192,6 +193,69 @@ def test_several_rounds_of_tiles(counts, o, i, input_grad):
         f(xs, device_offsets(offs), ws, out.view)
         R.check(out.view, want, S.sum_bound(want, size, have, dtype, 76), "out")
         out.check_guards("out")
+
+
+@pytest.mark.parametrize("odd", [False, True], ids=["aligned", "odd"])
+@pytest.mark.parametrize("case", range(len(C.PRODUCTS_IN_PARTS)))
+@pytest.mark.parametrize("input_grad", [False, True], ids=["product", "input_grad"])
+def test_products_dealt_out_over_experts(input_grad, case, odd):
+    H.device()
+    counts, along, to = (C.ODD_PRODUCTS_IN_PARTS if odd else C.PRODUCTS_IN_PARTS)[case]
+    o, i = (along, to) if input_grad else (to, along)
+    offs, experts = offsets_of(counts, 2), len(counts)
+    rows = offs[-1] + 3
+    x, w = randn(rows, along, seed=1), randn(experts, o, i, seed=2)
+    x[:2] = NAN
+    x[offs[-1]:] = NAN
+    for e, c in enumerate(counts):
+        if c == 0:
+            w[e] = NAN
+    px = Placed(rows, along, BF, -along % 8, 0, x)
+    f = dpr.dpr_grouped_linear_input_grad if input_grad else dpr.dpr_grouped_linear
+    want, size = S.product(x, offs, w, input_grad)
+    mine = slice(offs[0], offs[-1])
+    for dtype in (BF, F32):
+        out = Placed(rows, to, dtype, 3)
+        out.view.fill_(7)
+        f(px.view, device_offsets(offs), w.cuda(), out.view)
+        R.check(out.view[mine], want[mine], S.sum_bound(want, size, along, dtype, 76)[mine], "out")
+        assert bool((out.view[:2] == 7).all()) and bool((out.view[offs[-1]:] == 7).all())
+        out.check_guards("out")
+
+
+@pytest.mark.parametrize("saved", [False, True], ids=["stored", "saved"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("counts,o,i", C.GRADS_IN_PARTS)
+def test_weight_gradients_dealt_out_over_experts(counts, o, i, dtype, saved):
+    H.device()
+    offs, experts = offsets_of(counts, 2), len(counts)
+    rows = offs[-1] + 3
+    dy, x = randn(rows, o, seed=1), randn(rows, i, seed=2)
+    for t in (dy, x):
+        t[:2] = NAN
+        t[offs[-1]:] = NAN
+    pd, px = Placed(rows, o, BF, -o % 8, 0, dy), Placed(rows, i, BF, -i % 8, 0, x)
+    source, xx = px.view, x.double()
+    if saved:
+        source = dpr.dpr_checkpoint_empty(rows, i)
+        dpr.dpr_checkpoint_save(x.cuda(), source)
+        xx = R.decode(source.codes.cpu(), source.steps.cpu())
+    pw = Placed(experts * o, i, dtype, 5)
+    dw = pw.view.unflatten(0, (experts, o))
+    dw.fill_(NAN)
+    dpr.dpr_grouped_linear_weight_grad(pd.view, device_offsets(offs), source, dw)
+    want, size = S.weight_grads(dy, offs, xx)
+    bound = S.sum_bound(want, size, max(counts), dtype, 76)
+    R.check(dw, want, bound, "dweight")
+    first = dw.clone()
+    dpr.dpr_grouped_linear_weight_grad(pd.view, device_offsets(offs), source, dw)
+    assert torch.equal(dw, first)
+    old = torch.randn(experts, o, i, generator=gen(3)).to(dtype)
+    dw.copy_(old)
+    dpr.dpr_grouped_linear_weight_grad(pd.view, device_offsets(offs), source, dw, accumulate=True)
+    total = want + old.double()
+    R.check(dw, total, bound + (R.ROUND[dtype] + R.U) * (total.abs() + old.double().abs()), "added")
+    pw.check_guards("dweight")
 
 
 def test_one_row_for_all_tokens():

@@ -10,6 +10,7 @@ import subprocess
 import pytest
 import torch
 
+from tests import step_cases as C
 from tests import step_reference as S
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -197,6 +198,31 @@ def test_weight_gradient_refusals(L):
     assert call(ds=129, ws=None) == INVALID and call(ds=129, ws=X) == ALIAS
     assert call(rows=0, dy=None, x=None, ws=None, acc=1) == OK
     assert L.dpr_grouped_linear_weight_grad_workspace(X, 128, H, 64, None, 64, 4, 128, 64, None) == INVALID
+
+
+@pytest.mark.parametrize("name", ["dpr_grouped_linear", "dpr_grouped_linear_input_grad"])
+def test_which_products_are_dealt_out(L, name):
+    """Aligned operands, and unaligned weights that few tokens read, need memory for parts alone."""
+    for cases, parts in ((C.PRODUCTS_IN_PARTS, True), (C.ODD_PRODUCTS_IN_PARTS, True), (C.PRODUCTS_WHOLE, False)):
+        for counts, along, to in cases:
+            o, i = (along, to) if name.endswith("input_grad") else (to, along)
+            stride = i if parts else -(-i // 8) * 8
+            n = ctypes.c_int64()
+            assert getattr(L, name + "_workspace")(X, -(-along // 8) * 8, sum(counts), len(counts), W, stride, o * stride,
+                                                   o, i, ctypes.byref(n)) == OK
+            assert (n.value > 0) == parts, (counts, o, i)
+
+
+@pytest.mark.parametrize("saved", [False, True], ids=["stored", "saved"])
+def test_which_weight_gradients_are_dealt_out(L, saved):
+    for cases, parts in ((C.GRADS_IN_PARTS, True), (C.GRADS_WHOLE, False)):
+        for counts, o, i in cases:
+            n = ctypes.c_int64()
+            aligned = [-(-v // 16) * 16 for v in (o, i)]
+            c = _ckpt(code_stride=aligned[1], step_stride=-(-i // 512) * 16) if saved else None
+            assert L.dpr_grouped_linear_weight_grad_workspace(X, aligned[0], H, aligned[1], c, sum(counts), len(counts),
+                                                              o, i, ctypes.byref(n)) == OK
+            assert (n.value > 0) == parts, (counts, o, i)
 
 
 def _plan(L, tensors, outs=None):
