@@ -131,6 +131,34 @@ def test_infinities_and_nan_stay_in_their_row(width, dtype):
     R.check(dx[ok], want, bound, f"rows beside {bad}")
 
 
+@pytest.mark.parametrize("layout", ["plain", "half", "odd"])
+@pytest.mark.parametrize("width", [96, 1000, 1001, 4096, 5000])
+def test_forward_of_many_bf16_rows_with_checkpoints(width, layout):
+    """From 1024 rows on a thread takes 32 channels."""
+    H.device()
+    pad, shift = LAYOUTS[layout]
+    rows = 1100
+    x, r = activation(rows, width, width, BF), activation(rows, width, width + 1, BF)
+    w = weight_of(width, BF)
+    h = added(x, r)
+    px, pr = (Placed(rows, width, BF, pad, shift, t) for t in (x, r))
+    ph, py = Placed(rows, width, BF, pad, shift), Placed(rows, width, BF, pad, shift)
+    rstd = torch.empty(rows, device="cuda")
+    hc, hs, h_saved = checkpoint(rows, width, None if layout == "plain" else pad, shift)
+    yc, ys, y_saved = checkpoint(rows, width, None if layout == "plain" else pad, shift)
+    dpr.dpr_rmsnorm_forward(px.view, w.cuda(), EPS, py.view, rstd, pr.view, ph.view, h_saved, y_saved)
+    want, want_rstd = S.rms_forward(h, w, EPS)
+    d_y, d_rstd = S.rms_forward_bounds(h, w, EPS, BF)
+    assert torch.equal(ph.view.cpu(), h)
+    R.check(py.view, want, d_y, "y")
+    R.check(rstd, want_rstd, d_rstd, "rstd")
+    same_saved(h_saved, h)
+    same_saved(y_saved, py.view.cpu())
+    for p, what in ((px, "x"), (pr, "residual"), (ph, "h"), (py, "y"), (hc, "codes"), (hs, "steps"),
+                    (yc, "codes"), (ys, "steps")):
+        p.check_guards(what)
+
+
 # --- backward ------------------------------------------------------------------
 
 def run_backward(rows, width, dtype, pad, shift, saved, with_dh, grad_dtype=F32, accumulate=False):
@@ -235,6 +263,41 @@ def test_gradient_against_differences():
         measured = (value(*a)[0] - value(*b)[0]) / (2 * step)
         size = float((dy.abs()).sum()) * 1e-3
         assert abs(float(slope) - measured) < size
+
+
+@pytest.mark.parametrize("width", [40, 300, 1001])
+def test_gradient_against_differences_along_the_row(width):
+    """The forward's fp32 outputs differenced along the row itself, where the slope is none but for
+    eps: the term that takes the part along the row away makes up for all the rest.  And along the
+    weight.  The bound is the sum of the same difference quotient's distance from the slope in 64
+    bits, of the outputs' errors over the step's length, and of the gradients' own errors."""
+    H.device()
+    rows, step = 5, 2.0 ** -6
+    h, w = torch.randn(rows, width, generator=gen(1)), weight_of(width, F32)
+    dy = h * torch.rand(rows, width, generator=gen(2))          # a gradient along the row
+    u = w * torch.rand(width, generator=gen(3))
+    _, rstd = S.rms_forward(h, w, EPS)
+    rstd = rstd.float()
+    want, want_w = S.rms_backward(dy, h, w, rstd)
+    d_dx, d_dw = S.rms_backward_bounds(dy, h, w, rstd, None, F32, F32)
+    kept = rstd.double()[:, None] * dy.double() * w.double()    # without that term
+    dx, dw = torch.empty(rows, width, device="cuda"), torch.empty(width, device="cuda")
+    dpr.dpr_rmsnorm_backward(dy.cuda(), h.cuda(), w.cuda(), rstd.cuda(), dx, dw)
+    for got, exact, error, ends in ((dx.cpu().double() * h.double(), want * h.double(), d_dx * h.double().abs(),
+                                     [(h + a * step * h, w) for a in (1, -1)]),
+                                    (dw.cpu().double() * u.double(), want_w * u.double(), d_dw * u.double().abs(),
+                                     [(h, w + a * step * u) for a in (1, -1)])):
+        measured, in64, rounding = 0.0, 0.0, 0.0
+        for sign, (a, b) in zip((1, -1), ends):
+            y = torch.empty(rows, width, device="cuda")
+            dpr.dpr_rmsnorm_forward(a.cuda(), b.cuda(), EPS, y)
+            measured += sign * float((y.cpu().double() * dy.double()).sum()) / (2 * step)
+            in64 += sign * float((S.rms_forward(a, b, EPS)[0] * dy.double()).sum()) / (2 * step)
+            rounding += float((S.rms_forward_bounds(a, b, EPS, F32)[0] * dy.double().abs()).sum()) / (2 * step)
+        bound = abs(in64 - float(exact.sum())) + rounding + float(error.sum())
+        assert abs(float(got.sum()) - measured) <= bound
+        if got.dim() == 2:
+            assert float(((kept - want) * h.double()).sum()) > 1000 * bound
 
 
 def test_rows_past_32_bits():
