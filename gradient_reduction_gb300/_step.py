@@ -226,7 +226,9 @@ def _weight_grad_bytes(dy: int, dy_stride: int, x: tuple, rows: int, experts: in
 
 
 class GradPlan:
-    """Owns a dpr_grad_plan and keeps its tensors alive."""
+    """Owns a dpr_grad_plan and keeps its tensors alive.  Keep it as long as the steps and
+    the graphs captured with it: closing it frees device memory, which may wait for all of
+    the device's work and must not happen while a stream is captured."""
 
     def __init__(self, handle: int, device: int, workspace_bytes: int, tensors: tuple):
         self.handle = handle

@@ -32,6 +32,11 @@ extern "C" {
  * y_ckpt may be NULL; else the call also saves h, or y as rounded to `dtype`,
  * exactly as dpr_checkpoint_save would; with y_ckpt y may be NULL: the output
  * in 8 bits alone.
+ *
+ * The squares are summed in fp32: a row whose sum of squares is beyond it has
+ * rstd 0, and where eps is none, one whose squares are below 1e-38 loses digits.  The
+ * order of a row's sum goes by the width, the layouts and the number of rows, so
+ * that a token by itself and the same token among 1024 may differ in the last bit.
  */
 dpr_status dpr_rmsnorm_forward(const void* x, int64_t x_stride, const void* residual,
                                int64_t residual_stride, int64_t rows, int64_t width, int dtype,
@@ -73,7 +78,8 @@ dpr_status dpr_rmsnorm_backward(const void* dy, int64_t dy_stride, const void* d
  * every value is taken as limited to 0 .. rows and as no less than those before
  * it, so that no row has two experts whatever the values are.  An expert may have no
  * tokens (its weight is not read; its weight gradient is zero).  Rows that
- * belong to no expert are neither read nor written, whatever they hold.
+ * belong to no expert are not written, and what they hold has no effect (they
+ * may be read).  At most DPR_MAX_GRAD_ROWS rows.
  *
  * x, dy and weight are bf16; weight e starts at weight + e * expert_stride,
  * its rows `weight_stride` apart.  Products are exact and summed in fp32; y,
@@ -131,8 +137,9 @@ dpr_status dpr_grouped_linear_weight_grad(const void* dy, int64_t dy_stride, con
  *   out     = g * factor
  * `scale` (positive, finite) undoes a loss scale or averages; `norm` is one
  * fp32 number on the device.  The sum neither overflows nor underflows,
- * whatever the elements' magnitudes (a norm beyond fp32 is infinite).  An infinite norm clips to zero (and the
- * infinities to NaN), a NaN makes every gradient NaN: a diverged step shows.
+ * whatever the elements' magnitudes (a norm beyond fp32 is infinite).  An
+ * infinite norm clips to zero (and the infinities to NaN), a NaN makes every
+ * gradient NaN: a diverged step shows.
  *
  * The list is recorded once: n tensors of numel[i] elements (0 allowed, at most
  * DPR_MAX_ELEMS, 2^38 in all) at src[i], written to dst[i], each bf16 or fp32
@@ -141,15 +148,18 @@ dpr_status dpr_grouped_linear_weight_grad(const void* dy, int64_t dy_stride, con
  * outputs overlap neither one another nor any input.  Any element-aligned
  * addresses are accepted; where both rows of a tensor can be 32-byte aligned
  * together, the widest accesses are taken.  The plan may be used on any stream
- * of the device it was made on, by several calls at once if their outputs
- * (and their workspaces) differ; it must outlive the work enqueued with it.
+ * of the device it was made on, and by several calls of dpr_grad_norm at once if
+ * their norms and workspaces differ.  It must outlive the work enqueued with it
+ * and the graphs captured with it.  Making and destroying a plan allocate and
+ * free device memory, which may wait for all of the device's work: once before
+ * the steps and once behind them, and not while a stream is captured.
  *
  *   dpr_grad_norm        the norm
  *   dpr_grad_clip        the clipping by a norm that the device holds already
  *                        (of several devices' gradients, say)
  *   dpr_grad_norm_clip   both in one call
- * In place and with a factor of exactly 1 nothing is read or written but the
- * norm.  dpr_grad_norm and dpr_grad_norm_clip take dpr_grad_norm_workspace
+ * In place and with a factor of exactly 1 no gradient is written (they may be
+ * read).  dpr_grad_norm and dpr_grad_norm_clip take dpr_grad_norm_workspace
  * bytes, 16-byte aligned, which the next call on the same stream may reuse.
  */
 typedef struct dpr_grad_plan dpr_grad_plan;
