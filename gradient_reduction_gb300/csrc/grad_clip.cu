@@ -268,10 +268,24 @@ __device__ __forceinline__ bool sum_pieces(const GradParams& p, Sum& s) {
     return ok;
 }
 
-__device__ __forceinline__ float factor_of(const GradParams& p, float norm) {
-    // NaN stays NaN
-    const float clip = norm <= p.max_norm ? 1.0f : __fdiv_rn(p.max_norm, norm);
-    return __fmul_rn(p.scale, clip);
+// What an element is multiplied by, in two steps: a factor below the normal numbers (of a
+// step that diverged: a norm of 1e38 clipped to 0.01) has few digits or none, while the
+// clipped gradients are normal numbers.  There 2^64 of it come second, and 2^-64 first,
+// which is exact where the result is normal.
+struct Factor {
+    float first, second;
+    __device__ __forceinline__ float times(float v) const { return __fmul_rn(__fmul_rn(v, first), second); }
+    __device__ __forceinline__ bool one() const { return second == 1.0f; }   // then the first is 1 too
+};
+
+__device__ __forceinline__ Factor factor_of(const GradParams& p, float norm) {
+    if (norm <= p.max_norm) return Factor{1.0f, p.scale};
+    const float clip = __fdiv_rn(p.max_norm, norm), f = __fmul_rn(p.scale, clip);
+    if (!(f < 0x1p-126f)) return Factor{1.0f, f};     // NaN stays NaN
+    // clip itself is subnormal, or the scale is below 2^-58
+    return Factor{0x1p-64f, p.max_norm < 0x1p60f
+                                ? __fmul_rn(p.scale, __fdiv_rn(__fmul_rn(p.max_norm, 0x1p64f), norm))
+                                : __fmul_rn(__fmul_rn(p.scale, 0x1p64f), clip)};
 }
 
 // Both roundings are fp32's where the sum has no fp64 part.  fp64 takes the
@@ -327,11 +341,11 @@ __global__ void __launch_bounds__(kGradThreads, 4) clip_pieces(const __grid_cons
         norm = join(p);
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
     }
-    const float factor = factor_of(p, norm);
-    if (q.in_place && factor == 1.0f) return;    // as they are
+    const Factor factor = factor_of(p, norm);
+    if (q.in_place && factor.one()) return;      // as they are
     visit<true>(q, l, [&](float (&v)[kUnit]) {
 #pragma unroll
-        for (int k = 0; k < kUnit; ++k) v[k] = __fmul_rn(v[k], factor);
+        for (int k = 0; k < kUnit; ++k) v[k] = factor.times(v[k]);
     });
 }
 
@@ -409,19 +423,19 @@ __global__ void __launch_bounds__(kFewThreads) clip_few(const __grid_constant__ 
     const float norm = joined;
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
     if constexpr (kClip) {
-        const float factor = factor_of(p, norm);
-        if (i >= p.n || (q.in_place && factor == 1.0f)) return;
+        const Factor factor = factor_of(p, norm);
+        if (i >= p.n || (q.in_place && factor.one())) return;
 #pragma unroll
         for (int k = 0; k < kPer; ++k)
 #pragma unroll
-            for (int j = 0; j < kUnit; ++j) v[k][j] = __fmul_rn(v[k][j], factor);
+            for (int j = 0; j < kUnit; ++j) v[k][j] = factor.times(v[k][j]);
         if (q.wide) {
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int at = k * kGradThreads + tx;
                 if (at < q.count) store_unit(q.dst, q.dst_bf16, int64_t(at) * kUnit, v[k]);
             }
-            if (edge != kNone) store_one(q.dst, q.dst_bf16, edge, __fmul_rn(one, factor));
+            if (edge != kNone) store_one(q.dst, q.dst_bf16, edge, factor.times(one));
         } else {
 #pragma unroll
             for (int k = 0; k < kPer; ++k)

@@ -116,6 +116,31 @@ def test_magnitudes_whose_squares_leave_fp32(value, n):
                 assert abs(norm.item() - want) <= S.NORM_ERROR * want + 2.0 ** -149
 
 
+@pytest.mark.parametrize("dst", [BF, F32])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("n", [5, 9000, 300000])
+@pytest.mark.parametrize("max_norm,scale", [(1e-2, 1.0), (1e-6, 0.25), (1.0, 2.0 ** -20), (2.0 ** 100, 2.0 ** -110)])
+def test_factors_below_the_normal_numbers(max_norm, scale, n, shift, dst):
+    """Gradients of a diverged step: max_norm / norm, or its product with scale, is subnormal, the
+    clipped gradients are not.  (Those that are: half of TINY for each of two roundings.)"""
+    H.device()
+    g = torch.randn(n, generator=gen(1))
+    g[::max(n // 4, 1)] *= 5e37
+    src, out = Placed(1, n, F32, 0, shift, g[None]), Placed(1, n, dst, 0, 8)
+    norm = torch.empty(1, device="cuda")
+    want, clipped = S.clip([g], scale, max_norm)
+    with dpr.dpr_grad_plan_create([src.view[0]], [out.view[0]]) as plan:
+        for call in (dpr.dpr_grad_norm_clip, dpr.dpr_grad_clip):
+            out.view.fill_(9)
+            call(plan, norm, max_norm, scale=scale)
+            assert abs(norm.item() - want) <= S.NORM_ERROR * want
+            R.check(out.view[0], clipped[0], S.clip_bound(clipped[0], dst) + 2.0 ** -149, "out")
+            out.check_guards("out")
+    with dpr.dpr_grad_plan_create([src.view[0]]) as plan:
+        dpr.dpr_grad_norm_clip(plan, norm, max_norm, scale=scale)
+        R.check(src.view[0], clipped[0], S.clip_bound(clipped[0], F32) + 2.0 ** -149, "in place")
+
+
 @pytest.mark.parametrize("n", [1000, 50000])
 def test_infinities_and_nan_show(n):
     H.device()
