@@ -369,6 +369,65 @@ def test_binding_refusals():
             dpr.dpr_grouped_linear_weight_grad(*bad)
 
 
+@pytest.mark.parametrize("wide", [4096, 4099], ids=["aligned", "odd"])
+def test_activations_past_32_bits(wide):
+    """Inputs and outputs of more than 2^32 elements; an expert with the last rows alone, one with none,
+    and one with the rows around element 2^32."""
+    H.device()
+    rows, narrow = (1 << 20) + 5000, 72
+    offs = [(1 << 20) - 300, (1 << 20) + 300, (1 << 20) + 300, rows - 77, rows - 70, rows]
+    mine = [slice(offs[0], offs[1]), slice(offs[3], rows)]
+    w = randn(5, wide, narrow, seed=1, scale=0.1)
+    x = torch.full((rows, narrow), NAN, dtype=BF)
+    for k, m in enumerate(mine):
+        x[m] = randn(m.stop - m.start, narrow, seed=2 + k)
+    offs[2:4] = [offs[1], rows - 77]             # expert 2 has the many rows between: NaN
+    y = torch.full((rows, wide), 7.0, dtype=BF, device="cuda")
+    dpr.dpr_grouped_linear(x.cuda(), device_offsets(offs), w.cuda(), y)
+    assert bool((y[:offs[0]] == 7).all())
+    back = torch.empty(rows, narrow, device="cuda")
+    dpr.dpr_grouped_linear_input_grad(y, device_offsets(offs), w.cuda(), back)
+    dw = torch.empty(5, wide, narrow, device="cuda")
+    dpr.dpr_grouped_linear_weight_grad(y, device_offsets(offs), x.cuda(), dw)
+    for e, m in ((0, mine[0]), (3, slice(rows - 77, rows - 70)), (4, slice(rows - 70, rows))):
+        got = y[m].cpu()
+        n = m.stop - m.start
+        want, size = S.product(x[m], [0, n], w[e:e + 1], False)
+        R.check(got, want, S.sum_bound(want, size, narrow, BF, 76), "y")
+        want, size = S.product(got, [0, n], w[e:e + 1], True)
+        R.check(back[m], want, S.sum_bound(want, size, wide, F32, 76), "dx")
+        want, size = S.weight_grads(got, [0, n], x[m])
+        R.check(dw[e], want[0], S.sum_bound(want, size, n, F32, 76)[0], "dweight")
+
+
+@pytest.mark.parametrize("dtype,wide", [(BF, 4096), (F32, 4096), (F32, 4095)])
+def test_weights_past_32_bits(dtype, wide):
+    """Experts' matrices of more than 2^32 elements in all: gradients of the last, products with them."""
+    H.device()
+    experts, o = 260, 4100
+    rows, counts = 37, [0] * experts
+    counts[0], counts[257], counts[259] = 5, 12, 20
+    offs = offsets_of(counts)
+    dy, x = randn(rows, o, seed=1), randn(rows, wide, seed=2)
+    dw = torch.empty(experts, o, wide, dtype=dtype, device="cuda")
+    dw[1].fill_(NAN)
+    dw[258].fill_(NAN)
+    dpr.dpr_grouped_linear_weight_grad(dy.cuda(), device_offsets(offs), x.cuda(), dw)
+    assert not dw[1].any() and not dw[258].any()
+    for e in (0, 257, 259):
+        m = slice(offs[e], offs[e + 1])
+        want, size = S.weight_grads(dy[m], [0, counts[e]], x[m])
+        R.check(dw[e], want[0], S.sum_bound(want, size, counts[e], dtype, 76)[0], "dweight")
+    if dtype == F32:
+        return
+    y = torch.empty(rows, o, device="cuda")
+    dpr.dpr_grouped_linear(x.cuda(), device_offsets(offs), dw, y)
+    for e in (0, 257, 259):
+        m = slice(offs[e], offs[e + 1])
+        want, size = S.product(x[m], [0, counts[e]], dw[e:e + 1].cpu(), False)
+        R.check(y[m], want, S.sum_bound(want, size, wide, F32, 76), "y")
+
+
 def test_missing_tensors():
     H.device()
     x, w = randn(8, 64).cuda(), randn(2, 72, 64).cuda()

@@ -342,3 +342,26 @@ def test_backward_of_large_and_small_rows(size, grad, width, dtype, saved):
     d_dx, d_dw = S.rms_backward_bounds(dy, hh, w, rstd, None, dtype, F32)
     R.check(dw, want_w, d_dw, "dweight")
     R.check(dx, want, d_dx, "dx")
+
+
+@pytest.mark.parametrize("pad", [0, 3], ids=["staged", "odd"])
+def test_backward_of_rows_past_32_bits(pad):
+    """The last rows of more than 2^32 elements; a broadcast dh; the others' gradient is dh."""
+    H.device()
+    rows, width = 300000, 16384 - 8 + pad
+    tail = activation(3, width, 1, BF)
+    dy = torch.zeros(rows, width, dtype=BF, device="cuda")
+    dy[-3:] = tail.flip(0).cuda()
+    h = torch.zeros(rows, width, dtype=BF, device="cuda")
+    h[-3:] = tail.cuda()
+    dh = (1e-2 * torch.randn(1, width, generator=gen(2))).to(BF)
+    w, rstd = weight_of(width, BF), torch.rand(rows, generator=gen(3)) + 0.5
+    dw = torch.empty(width, device="cuda")
+    dpr.dpr_rmsnorm_backward(dy, h, w.cuda(), rstd.cuda(), dy, dw, dh=dh.cuda().expand(rows, width))
+    args = tail.flip(0), tail, w, rstd[-3:], dh.expand(3, width)
+    want, want_w = S.rms_backward(*args)
+    bound, bound_w = S.rms_backward_bounds(*args, BF, F32)
+    R.check(dy[-3:], want, bound, "dx")
+    R.check(dw, want_w, bound_w, "dweight")
+    for at in (0, 131072, 262144, rows - 4):
+        assert torch.equal(dy[at].cpu(), dh[0])
