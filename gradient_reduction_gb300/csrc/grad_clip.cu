@@ -283,9 +283,9 @@ __device__ __forceinline__ Factor factor_of(const GradParams& p, float norm) {
     const float clip = __fdiv_rn(p.max_norm, norm), f = __fmul_rn(p.scale, clip);
     if (!(f < 0x1p-126f)) return Factor{1.0f, f};     // NaN stays NaN
     // clip itself is subnormal, or the scale is below 2^-58
-    return Factor{0x1p-64f, p.max_norm < 0x1p60f
-                                ? __fmul_rn(p.scale, __fdiv_rn(__fmul_rn(p.max_norm, 0x1p64f), norm))
-                                : __fmul_rn(__fmul_rn(p.scale, 0x1p64f), clip)};
+    return Factor{0x1p-64f, __fmul_rn(p.scale, p.max_norm < 0x1p60f
+                                                   ? __fdiv_rn(__fmul_rn(p.max_norm, 0x1p64f), norm)
+                                                   : __fmul_rn(clip, 0x1p64f))};
 }
 
 // Both roundings are fp32's where the sum has no fp64 part.  fp64 takes the

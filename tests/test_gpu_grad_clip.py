@@ -141,6 +141,20 @@ def test_factors_below_the_normal_numbers(max_norm, scale, n, shift, dst):
         R.check(src.view[0], clipped[0], S.clip_bound(clipped[0], F32) + 2.0 ** -149, "in place")
 
 
+@pytest.mark.parametrize("n", [100, 300000])
+@pytest.mark.parametrize("max_norm", [0.0, 1.0, 2.0 ** 100])
+@pytest.mark.parametrize("scale", [2.0 ** -70, 1.0, 2.0 ** 100])
+def test_an_infinite_norm_clips_to_zero_at_any_scale(scale, max_norm, n):
+    H.device()
+    g = torch.randn(n, generator=gen(1))
+    g[3] = float("inf")
+    norm, out = torch.empty(1, device="cuda"), torch.full((n,), 9.0, device="cuda")
+    with dpr.dpr_grad_plan_create([g.cuda()], [out]) as plan:
+        dpr.dpr_grad_norm_clip(plan, norm, max_norm, scale=scale)
+        assert norm.item() == float("inf") and bool(out[3].isnan())
+        assert int((out == 0).sum()) == n - 1
+
+
 @pytest.mark.parametrize("n", [1000, 50000])
 def test_infinities_and_nan_show(n):
     H.device()
